@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgg.so")
 
 SOURCES = ["gg_api.cpp", "gg_kernels.hip", "gg_noalloc.hip"]
-HEADERS = ["gg_kernels.h"]
+HEADERS = ["gg_device.h", "gg_host.h", "gg_kernels.h"]
 
 # Packed-fp32 VALU ops are disabled for all device code.
 HIP_FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",
