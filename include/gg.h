@@ -248,6 +248,73 @@ int gg_scale_rows(const void* x, const float* probs, int64_t M, int64_t H, void*
 int gg_scale_rows_backward(const void* dxs, const void* x, const float* probs, int64_t M, int64_t H,
                            void* dx, float* dprobs, hipStream_t stream);
 
+/* ---- Expert products over an 8-bit copy of the frozen weights.
+ *
+ * For one frozen matrix W_e [N][K] of each expert, held as int8 values wq_e
+ * with one fp32 scale ws_e[n] for each output channel (W_e ~ ws_e[n] wq_e[n][k]):
+ *
+ *   forward      Y[r][n]  = bf16(s_r ws_e[n] sum_k q_r[k] wq_e[n][k])
+ *   input grad.  dX[r][k] = bf16(s_r sum_n q_r[n] wq_e[n][k])
+ *
+ * where (q_r, s_r) is the row's operand v, quantized for each token:
+ *
+ *   s = max|v| / 127,   q[i] = v[i] 127 / max|v|, rounded to nearest even
+ *
+ * v is the row of x (forward), ws_e[n] dY[r][n] (input gradient: the channel
+ * scales belong to the summed dimension there), or, with an activation, its
+ * value or derivative at a saved H1 row [gate | up]:
+ *
+ *   forward      v = A   = bf16(act(gate) * up)
+ *   input grad.  v = ws_e[n] dH1[n],
+ *                dH1 = [bf16(dA up act'(gate)) | bf16(dA act(gate))]
+ *
+ * with act and the rounding points of gg_forward_fc1_glu / gg_dgrad_glu.
+ * Sums are exact in 32-bit integers, so a row's result depends neither on the
+ * rest of the batch nor on any order.  A row of zeros gives zeros; a row with
+ * a NaN or an infinity gives NaN in that row alone.
+ *
+ * Limits: 1 <= E <= GG_MAX_EXPERTS; N and K positive multiples of 8, at most
+ * GG_INT8_MAX_SUM (32-bit sums of 127 * 127 cannot overflow); one packed
+ * expert matrix below 2 GiB; 0 <= M < 2^31.  Conventions as above. */
+#define GG_INT8_MAX_SUM 131072
+#define GG_ACT_NONE (-1)   /* `activation` of the int8 calls: the operand itself */
+
+/* Quantize M rows of x (DEVICE bf16 [M][K], 16-byte aligned) into q (DEVICE
+ * int8 [M][K], 8-byte aligned) and s (DEVICE fp32 [M]).  Also quantizes
+ * weights for each output channel: the rows are then W's.  One launch. */
+int gg_int8_quantize_rows(const void* x, int64_t M, int64_t K, int8_t* q, float* s, hipStream_t stream);
+
+/* Bytes of a packed 8-bit matrix of E experts: the matrices with both
+ * dimensions zero-padded (output columns to a multiple of 32, the summed
+ * dimension to one of 128) in the operand order of the int8 matrix
+ * instruction, then the fp32 channel scales.  transposed = 0: for
+ * gg_int8_forward; 1: W^T, for gg_int8_dgrad.  0 for sizes outside the limits. */
+size_t gg_int8_packed_bytes(int64_t E, int64_t N, int64_t K, int transposed);
+
+/* Lay out wq (DEVICE int8 [E][N][K]) and ws (DEVICE fp32 [E][N]) as above into
+ * `packed` (DEVICE, 16-byte aligned).  Once for frozen weights.  One launch. */
+int gg_int8_pack(const int8_t* wq, const float* ws, int64_t E, int64_t N, int64_t K, int transposed,
+                 void* packed, size_t packed_bytes, hipStream_t stream);
+
+/* Bytes of the workspace of gg_int8_forward (width = K) or gg_int8_dgrad
+ * (width = N): the quantized operand rows and their scales. */
+size_t gg_int8_workspace_bytes(int64_t M, int64_t width);
+
+/* Forward: x [M][K] with GG_ACT_NONE, or H1 [M][2K] with an activation, in
+ * which case a_out (may be NULL) receives A [M][K].  packed: gg_int8_pack(...,
+ * transposed = 0).  y [M][N].  Two launches. */
+int gg_int8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed,
+                    int64_t E, int64_t N, int64_t K, int activation, void* a_out,
+                    void* workspace, size_t workspace_bytes, void* y, hipStream_t stream);
+
+/* Input gradient: dy [M][N] with GG_ACT_NONE (h1 and dh1_out NULL); with an
+ * activation N = 2F (F a multiple of 8), dy is dA [M][F], h1 [M][2F] the saved
+ * FC1 output, and dh1_out (may be NULL) receives dH1 [M][2F].  packed:
+ * gg_int8_pack(..., transposed = 1).  dx [M][K].  Two launches. */
+int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed,
+                  int64_t E, int64_t N, int64_t K, int activation, void* dh1_out,
+                  void* workspace, size_t workspace_bytes, void* dx, hipStream_t stream);
+
 /* ---- For callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid allocation).
  * gg_dgrad without a workspace argument: dH1 goes to a static device array

@@ -56,13 +56,16 @@ GG_ERR_HIP = 6
 
 GG_ACT_SWIGLU = 0
 GG_ACT_QGEGLU = 1
+GG_ACT_NONE = -1
 ACTIVATIONS = {"swiglu": GG_ACT_SWIGLU, "qgeglu": GG_ACT_QGEGLU}
 
 EXPORTED = ("gg_status_string", "gg_packed_bytes", "gg_dgrad_workspace_bytes", "gg_pack_weights",
             "gg_forward_fc1_swiglu", "gg_forward_fc2", "gg_dgrad", "gg_round_bf16",
             "gg_dgrad_glu_workspace_bytes", "gg_forward_fc1_glu", "gg_dgrad_glu", "gg_dgrad_recompute",
             "gg_frag_bytes", "gg_pack_frag", "gg_forward_fc2_frag", "gg_dgrad_noalloc",
-            "gg_scale_rows", "gg_scale_rows_backward")
+            "gg_scale_rows", "gg_scale_rows_backward",
+            "gg_int8_quantize_rows", "gg_int8_packed_bytes", "gg_int8_pack", "gg_int8_workspace_bytes",
+            "gg_int8_forward", "gg_int8_dgrad")
 
 
 def _load() -> ctypes.CDLL:
@@ -94,9 +97,18 @@ def _load() -> ctypes.CDLL:
     lib.gg_dgrad_recompute.argtypes = [p, p, p, i64, p, p, i64, i64, i64, i32, p, p, sz, p, p, p]
     lib.gg_scale_rows.argtypes = [p, p, i64, i64, p, p]
     lib.gg_scale_rows_backward.argtypes = [p, p, p, i64, i64, p, p, p]
+    lib.gg_int8_quantize_rows.argtypes = [p, i64, i64, p, p, p]
+    lib.gg_int8_packed_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gg_int8_packed_bytes.restype = sz
+    lib.gg_int8_pack.argtypes = [p, p, i64, i64, i64, i32, p, sz, p]
+    lib.gg_int8_workspace_bytes.argtypes = [i64, i64]
+    lib.gg_int8_workspace_bytes.restype = sz
+    lib.gg_int8_forward.argtypes = [p, p, i64, p, i64, i64, i64, i32, p, p, sz, p, p]
+    lib.gg_int8_dgrad.argtypes = [p, p, p, i64, p, i64, i64, i64, i32, p, p, sz, p, p]
     for name in ("gg_pack_weights", "gg_pack_frag", "gg_forward_fc1_swiglu", "gg_forward_fc2",
                  "gg_forward_fc2_frag", "gg_dgrad", "gg_round_bf16", "gg_forward_fc1_glu", "gg_dgrad_glu",
-                 "gg_dgrad_recompute", "gg_dgrad_noalloc", "gg_scale_rows", "gg_scale_rows_backward"):
+                 "gg_dgrad_recompute", "gg_dgrad_noalloc", "gg_scale_rows", "gg_scale_rows_backward",
+                 "gg_int8_quantize_rows", "gg_int8_pack", "gg_int8_forward", "gg_int8_dgrad"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -538,6 +550,145 @@ def gg_scale_rows_backward(dxs: torch.Tensor, x: torch.Tensor, probs: torch.Tens
     _check(lib.gg_scale_rows_backward(dxs.data_ptr(), x.data_ptr(), pr.data_ptr(), M, H, dx.data_ptr(),
                                       _ptr(dprobs), _stream_ptr(stream, dxs.device)), "gg_scale_rows_backward")
     return dx, dprobs
+
+
+def _typed_cuda(t: torch.Tensor, dtype, name: str, shape, device) -> torch.Tensor:
+    """A contiguous device tensor of the given dtype and shape (None: any size there), on the given device."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} device tensor")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def int8_packed_bytes(E: int, N: int, K: int, transposed: bool = False) -> int:
+    return int(lib.gg_int8_packed_bytes(E, N, K, int(bool(transposed))))
+
+
+def int8_workspace_bytes(M: int, width: int) -> int:
+    """Workspace of gg_int8_forward (width = K) or gg_int8_dgrad (width = N)."""
+    return int(lib.gg_int8_workspace_bytes(M, width))
+
+
+def gg_int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of x (bf16 [M, K]) to int8 with one scale each: (q int8 [M, K], s
+    float32 [M]), x ~ s[:, None] * q.  Frozen weights [E, N, K] are quantized
+    for each output channel as x = w.view(E * N, K)."""
+    _bf16_cuda(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else _typed_cuda(q, torch.int8, "q", (M, K), x.device)
+    s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else _probs_cuda(s, M, x.device, "s")
+    _check(lib.gg_int8_quantize_rows(x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(), _stream_ptr(stream, x.device)),
+           "gg_int8_quantize_rows")
+    return q, s
+
+
+def _int8_pack(wq, ws, transposed, packed, stream):
+    _typed_cuda(wq, torch.int8, "wq", (None, None, None), None)
+    E, N, K = wq.shape
+    _typed_cuda(ws, torch.float32, "ws", (E, N), wq.device)
+    need = int8_packed_bytes(E, N, K, transposed)
+    if need == 0:
+        raise ValueError(f"E={E}, N={N}, K={K} is outside the limits of the int8 calls")
+    if packed is None:
+        packed = torch.empty(need, dtype=torch.uint8, device=wq.device)
+    _workspace(packed, need, wq.device)
+    _check(lib.gg_int8_pack(wq.data_ptr(), ws.data_ptr(), E, N, K, int(transposed), packed.data_ptr(),
+                            packed.numel() * packed.element_size(), _stream_ptr(stream, wq.device)), "gg_int8_pack")
+    return packed
+
+
+def gg_int8_pack(wq: torch.Tensor, ws: torch.Tensor, packed: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """8-bit weights wq (int8 [E, N, K]) with channel scales ws (float32
+    [E, N]), laid out once for gg_int8_forward: a byte buffer of
+    int8_packed_bytes(E, N, K)."""
+    return _int8_pack(wq, ws, False, packed, stream)
+
+
+def gg_int8_pack_transposed(wq: torch.Tensor, ws: torch.Tensor, packed: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The same weights laid out for gg_int8_dgrad (int8_packed_bytes(E, N, K, True) bytes)."""
+    return _int8_pack(wq, ws, True, packed, stream)
+
+
+def _int8_packed(packed: torch.Tensor, E: int, N: int, K: int, transposed: bool, device) -> torch.Tensor:
+    need = int8_packed_bytes(E, N, K, transposed)
+    if need == 0:
+        raise ValueError(f"E={E}, N={N}, K={K} is outside the limits of the int8 calls")
+    if not isinstance(packed, torch.Tensor) or not packed.is_cuda or not packed.is_contiguous() or packed.device != device:
+        raise ValueError(f"packed must be a contiguous tensor on {device}")
+    if packed.numel() * packed.element_size() < need:
+        raise ValueError(f"packed holds {packed.numel() * packed.element_size()} bytes, {need} needed")
+    return packed
+
+
+def gg_int8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
+                    activation=None, save_a: bool = False, a_out: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(y [M, N], A or None): the rows quantized to 8 bits, times each expert's
+    8-bit matrix (gg_int8_pack).  activation None: x is [M, K]; "swiglu" |
+    "qgeglu": x is H1 [M, 2K], the product's operand is A = act(gate) * up
+    [M, K], returned with save_a (or given a_out)."""
+    _bf16_cuda(x, "x")
+    dev, M = x.device, x.shape[0]
+    act = GG_ACT_NONE if activation is None else _activation(activation)
+    _bf16_cuda(x, "x", shape=(M, K if act == GG_ACT_NONE else 2 * K))
+    _int8_packed(packed, E, N, K, False, dev)
+    off = _offsets(offsets, E, dev)
+    if a_out is not None:
+        _bf16_cuda(a_out, "a_out", shape=(M, K), device=dev)
+    if act == GG_ACT_NONE and (save_a or a_out is not None):
+        raise ValueError("A exists with an activation only")
+    workspace = _workspace(workspace, int8_workspace_bytes(M, K), dev)
+    if a_out is None and save_a:
+        a_out = _out(None, (M, K), "a_out", dev)
+    y = _out(y, (M, N), "y", dev)
+    _check(lib.gg_int8_forward(x.data_ptr(), off.data_ptr(), M, packed.data_ptr(), E, N, K, act, _ptr(a_out),
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(), y.data_ptr(),
+                               _stream_ptr(stream, dev)), "gg_int8_forward")
+    return y, a_out
+
+
+def gg_int8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
+                  h1: Optional[torch.Tensor] = None, activation=None, save_dh1: bool = True,
+                  dh1_out: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                  ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(dx [M, K], dH1 or None): input gradient through 8-bit weights
+    (gg_int8_pack_transposed).  activation None: dy is [M, N]; else N = 2F, dy
+    is dA [M, F], h1 the saved [M, 2F], and dH1 [M, 2F] is returned unless
+    save_dh1 is False."""
+    _bf16_cuda(dy, "dy")
+    dev, M = dy.device, dy.shape[0]
+    act = GG_ACT_NONE if activation is None else _activation(activation)
+    if (act == GG_ACT_NONE) != (h1 is None):
+        raise ValueError("h1 and an activation go together")
+    _bf16_cuda(dy, "dy", shape=(M, N if act == GG_ACT_NONE else N // 2))
+    if h1 is not None:
+        _bf16_cuda(h1, "h1", shape=(M, N), device=dev)
+    _int8_packed(packed, E, N, K, True, dev)
+    off = _offsets(offsets, E, dev)
+    if dh1_out is not None:
+        if h1 is None:
+            raise ValueError("dH1 exists with an activation only")
+        _bf16_cuda(dh1_out, "dh1_out", shape=(M, N), device=dev)
+    workspace = _workspace(workspace, int8_workspace_bytes(M, N), dev)
+    if dh1_out is None and h1 is not None and save_dh1:
+        dh1_out = _out(None, (M, N), "dh1_out", dev)
+    dx = _out(dx, (M, K), "dx", dev)
+    _check(lib.gg_int8_dgrad(dy.data_ptr(), _ptr(h1), off.data_ptr(), M, packed.data_ptr(), E, N, K, act,
+                             _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                             dx.data_ptr(), _stream_ptr(stream, dev)), "gg_int8_dgrad")
+    return dx, dh1_out
 
 
 class ScaleRows(torch.autograd.Function):

@@ -1,0 +1,62 @@
+// Internal interface between the C-ABI entry points of the 8-bit expert
+// products (gg_int8_api.cpp) and their kernels (gg_int8.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gg {
+
+// Layout of a packed 8-bit matrix W [rows][cont] (rows: output columns of the
+// product, cont: the summed dimension): 32-row blocks, each of cont_p / 32
+// steps of 1 KiB in the operand order of the 32x32x32 int8 matrix
+// instruction: lane l's 16 bytes are row 32b + (l & 31), columns
+// 32s + 16(l >> 5) onwards.  Both dimensions are padded with zeros.
+constexpr int I8_ROWS = 32, I8_STEP = 32, I8_PAD = 128;
+inline int64_t i8_rows_p(int64_t rows) { return (rows + I8_ROWS - 1) / I8_ROWS * I8_ROWS; }
+inline int64_t i8_cont_p(int64_t cont) { return (cont + I8_PAD - 1) / I8_PAD * I8_PAD; }
+
+// What a row's 8-bit values are made from.
+enum QuantMode {
+    Q_PLAIN = 0,    // v = x
+    Q_GLU = 1,      // v = bf16(act(gate) * up) of x = [gate | up]
+    Q_SCALED = 2,   // v = cs_e[n] * x[n]
+    Q_DGLU = 3      // v = cs_e[n] * dH1[n], dH1 = bf16(derivative of the activation at h1, times x)
+};
+
+struct QuantParams {
+    const uint16_t* x;       // [M][K] bf16 (Q_GLU: [M][2K], Q_DGLU: [M][K/2])
+    const uint16_t* h1;      // Q_DGLU: [M][K]
+    const int64_t* offsets;  // [E+1], or null: every row below M
+    const float* cs;         // Q_SCALED, Q_DGLU: column scales [E][cs_ld]
+    int cs_ld;
+    int M, E, K;             // K: values of a quantized row
+    float slope;
+    uint16_t* v_out;         // Q_GLU: A [M][K], Q_DGLU: dH1 [M][K]; null: not kept
+    int8_t* q;               // [M][ldq], columns K .. ldq-1 zero
+    int ldq;
+    float* s;                // [M]
+};
+
+// out[r][n] = bf16(s[r] * ws_e[n] * sum_k q[r][k] W_e[n][k])
+struct Int8Params {
+    const int8_t* q;         // [M][ldq]
+    const float* s;          // [M]
+    const int64_t* offsets;  // [E+1]
+    const int8_t* w;         // packed matrices
+    int64_t w_stride;        // bytes of one expert's matrix
+    const float* ws;         // [E][ws_ld] output column scales, or null (all one)
+    int ws_ld;
+    int ldq;
+    int M, E, N;             // N: output columns, a multiple of 8
+    uint16_t* out;           // [M][N]
+};
+
+hipError_t launch_quant_rows(QuantMode mode, const QuantParams& p, int num_cu, hipStream_t s);
+hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s);
+// q [E][N][K] and s [E][N] into the packed layout: W = q_e (rows N, summed K), or with
+// `transposed` q_e^T (rows K, summed N); the scales [E][i8_cont_p(N)] follow the matrices.
+hipError_t launch_int8_pack(const int8_t* q, const float* s, int E, int N, int K, int transposed, int8_t* packed,
+                            hipStream_t stream);
+
+}  // namespace gg

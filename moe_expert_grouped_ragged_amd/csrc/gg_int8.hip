@@ -1,0 +1,423 @@
+// 8-bit expert products on CDNA4: token quantization (with the activation or
+// its derivative fused in), the packed weight layout, and the ragged grouped
+// int8 product.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gg_device.h"
+#include "gg_int8.h"
+#include "gg_kernels.h"
+
+namespace gg {
+
+typedef __attribute__((ext_vector_type(4))) int i32x4;
+typedef __attribute__((ext_vector_type(16))) int i32x16;
+
+// ---------------------------------------------------------------- quantization
+//
+// Per row: top = max|v|, s = top / 127, q = rint(127 v / top) to nearest even;
+// a zero row gives s = 0, q = 0, and a row with a NaN or infinity s = NaN,
+// q = 0, so that its products are NaN and no other row's are.  127 v is exact
+// for bf16 v, and 127 v / top is then either a tie exactly or at least 1/512
+// away from one, so the quotient (a product with 1/top and one residual
+// correction) rounds as the exact quotient does.  Rows whose top is far from
+// one are scaled by a power of two first, so 1/top neither overflows nor
+// loses bits.
+//
+// One wavefront per row; its values stay in registers between the maximum
+// and the rounding (rows of more than NC * 64 units compute them twice).
+template <int MODE>
+struct QuantUnit {
+    static constexpr int VALS = MODE == Q_DGLU ? 16 : 8;   // values a lane makes at a time
+};
+
+template <int MODE>
+__device__ __forceinline__ void quant_unit(const QuantParams& p, int64_t r, const float* cs, int c, float* v,
+                                           bool store) {
+    if constexpr (MODE == Q_PLAIN || MODE == Q_SCALED) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p.x + r * p.K + c * 8);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = lo_f(xw[i]);
+            v[2 * i + 1] = hi_f(xw[i]);
+        }
+    } else if constexpr (MODE == Q_GLU) {
+        const uint16_t* row = p.x + r * 2 * p.K + c * 8;
+        const uint4 g4 = *reinterpret_cast<const uint4*>(row);
+        const uint4 u4 = *reinterpret_cast<const uint4*>(row + p.K);
+        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+        uint32_t aw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {   // the arithmetic of the FC1 epilogue
+                const float g = y ? hi_f(gw[i]) : lo_f(gw[i]);
+                const float u = y ? hi_f(uw[i]) : lo_f(uw[i]);
+                const float sg = g * __builtin_amdgcn_rcpf(1.0f + __expf(-(p.slope * g)));
+                a[y] = sg * u;
+            }
+            aw[i] = pack2(a[0], a[1]);
+            v[2 * i] = lo_f(aw[i]);
+            v[2 * i + 1] = hi_f(aw[i]);
+        }
+        if (store) *reinterpret_cast<uint4*>(p.v_out + r * p.K + c * 8) = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+    } else {
+        const int F = p.K / 2;
+        const uint16_t* hrow = p.h1 + r * p.K + c * 8;
+        const uint4 g4 = *reinterpret_cast<const uint4*>(hrow);
+        const uint4 u4 = *reinterpret_cast<const uint4*>(hrow + F);
+        const uint4 d4 = *reinterpret_cast<const uint4*>(p.x + r * F + c * 8);
+        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+        const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+        uint32_t og[4], ou[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float dg[2], du[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {   // the arithmetic of the dgrad FC2 epilogue
+                const float g = y ? hi_f(gw[i]) : lo_f(gw[i]);
+                const float u = y ? hi_f(uw[i]) : lo_f(uw[i]);
+                const float da = y ? hi_f(dw[i]) : lo_f(dw[i]);
+                const float sgm = __builtin_amdgcn_rcpf(1.0f + __expf(-(p.slope * g)));
+                dg[y] = da * u * sgm * (1.0f + p.slope * g * (1.0f - sgm));
+                du[y] = da * g * sgm;
+            }
+            og[i] = pack2(dg[0], dg[1]);
+            ou[i] = pack2(du[0], du[1]);
+            v[2 * i] = lo_f(og[i]);
+            v[2 * i + 1] = hi_f(og[i]);
+            v[8 + 2 * i] = lo_f(ou[i]);
+            v[8 + 2 * i + 1] = hi_f(ou[i]);
+        }
+        if (store) {
+            uint16_t* o = p.v_out + r * p.K + c * 8;
+            *reinterpret_cast<uint4*>(o) = make_uint4(og[0], og[1], og[2], og[3]);
+            *reinterpret_cast<uint4*>(o + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 c0 = *reinterpret_cast<const float4*>(cs + h * F + c * 8);
+            const float4 c1 = *reinterpret_cast<const float4*>(cs + h * F + c * 8 + 4);
+            const float cf[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * h + i] *= cf[i];
+        }
+    }
+    if constexpr (MODE == Q_SCALED) {
+        const float4 c0 = *reinterpret_cast<const float4*>(cs + c * 8);
+        const float4 c1 = *reinterpret_cast<const float4*>(cs + c * 8 + 4);
+        const float cf[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= cf[i];
+    }
+}
+
+// Eight values to eight int8: t = v * c127 (127 times the row's power of two),
+// the corrected quotient t / top, then the sum with 1.5 * 2^23, whose rounding
+// is to the nearest even integer and whose low byte is that integer.
+__device__ __forceinline__ uint2 quant8(const float* v, float c127, float top, float inv) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * c127;
+        const float q0 = t * inv;
+        const float q = __builtin_fmaf(__builtin_fmaf(-q0, top, t), inv, q0);
+        b[i] = __builtin_bit_cast(uint32_t, q + 12582912.0f) & 0xffu;
+    }
+    return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
+}
+
+template <int MODE, int NC>   // NC = 0: any width, values computed twice
+__global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
+    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
+    constexpr int VALS = QuantUnit<MODE>::VALS;
+    constexpr bool SCALES = MODE == Q_SCALED || MODE == Q_DGLU;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = p.M;
+    if (p.offsets) {
+        for (int e = threadIdx.x; e <= p.E; e += 256) {
+            int64_t o = p.offsets[e];
+            o = o < 0 ? 0 : (o > p.M ? p.M : o);
+            s_off[e] = static_cast<int>(o);
+        }
+        __syncthreads();
+        lo = s_off[0];
+        hi = s_off[p.E];
+    }
+    const int units = p.K / VALS;
+    for (int64_t r = lo + static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6); r < hi;
+         r += static_cast<int64_t>(gridDim.x) * 4) {
+        const float* cs = nullptr;
+        if constexpr (SCALES)
+            cs = p.cs + static_cast<int64_t>(uni(find_expert(s_off, p.E, static_cast<int>(r)))) * p.cs_ld;
+        const bool keep = p.v_out != nullptr;
+        float v[NC ? NC : 1][VALS];
+        uint32_t m = 0;   // largest |v| as bits: a NaN is larger than infinity, which is larger than any number
+        if constexpr (NC > 0) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const int c = lane + 64 * j;
+                quant_unit<MODE>(p, r, cs, min(c, units - 1), v[j], keep && c < units);
+#pragma unroll
+                for (int i = 0; i < VALS; ++i)   // repeated last units do not change the maximum
+                    m = max(m, __builtin_bit_cast(uint32_t, v[j][i]) & 0x7fffffffu);
+            }
+        } else {
+            for (int c = lane; c < units; c += 64) {
+                quant_unit<MODE>(p, r, cs, c, v[0], keep);
+#pragma unroll
+                for (int i = 0; i < VALS; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[0][i]) & 0x7fffffffu);
+            }
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 64)));
+        float top = __builtin_bit_cast(float, m);
+        const bool fin = m < 0x7f800000u;
+        if (lane == 0) p.s[r] = fin ? top / 127.0f : __builtin_nanf("");
+        // a power of two that brings the row near one where it is far from it
+        const float pw = top < 0x1p-90f ? 0x1p64f : (top > 0x1p90f ? 0x1p-64f : 1.0f);
+        float c127 = 127.0f * pw;
+        top *= pw;
+        float inv = 1.0f / top;
+        const bool zero = m == 0 || !fin;
+        int8_t* qrow = p.q + r * p.ldq;
+        auto put = [&](int c, const float* u) {
+#pragma unroll
+            for (int h = 0; h < VALS / 8; ++h) {
+                uint2 o = quant8(u + 8 * h, c127, top, inv);
+                if (zero) o = make_uint2(0, 0);
+                *reinterpret_cast<uint2*>(qrow + (MODE == Q_DGLU ? h * (p.K / 2) : 0) + c * 8) = o;
+            }
+        };
+        if constexpr (NC > 0) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const int c = lane + 64 * j;
+                if (c < units) put(c, v[j]);
+            }
+        } else {
+            for (int c = lane; c < units; c += 64) {
+                quant_unit<MODE>(p, r, cs, c, v[0], false);
+                put(c, v[0]);
+            }
+        }
+        const int pad = (p.ldq - p.K) / 8;   // below 16
+        if (lane < pad) *reinterpret_cast<uint2*>(qrow + p.K + lane * 8) = make_uint2(0, 0);
+    }
+}
+
+// ---------------------------------------------------------------- packing
+__global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __restrict__ s, int E, int N, int K,
+                                 int transposed, int8_t* __restrict__ packed, float* __restrict__ scales, int ns) {
+    const int rows = transposed ? K : N, cont = transposed ? N : K;
+    const int64_t nb = (rows + I8_ROWS - 1) / I8_ROWS, ks = (cont + I8_PAD - 1) / I8_PAD * (I8_PAD / I8_STEP);
+    const int64_t total = static_cast<int64_t>(E) * nb * ks * 64;   // 16-byte operands
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    for (int64_t i = first; i < total; i += step) {
+        const int l = static_cast<int>(i & 63);
+        const int64_t blk = i >> 6;
+        const int st = static_cast<int>(blk % ks);
+        const int b = static_cast<int>(blk / ks % nb);
+        const int64_t e = blk / ks / nb;
+        const int row = b * I8_ROWS + (l & 31), c0 = st * I8_STEP + 16 * (l >> 5);
+        const int8_t* m = q + e * N * K;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (row < rows) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int c = c0 + j;
+                if (c < cont) {
+                    const int8_t x = transposed ? m[static_cast<int64_t>(c) * K + row] : m[static_cast<int64_t>(row) * K + c];
+                    w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(x)) << (8 * (j & 3));
+                }
+            }
+        }
+        *reinterpret_cast<uint4*>(packed + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    for (int64_t i = first; i < static_cast<int64_t>(E) * ns; i += step) {
+        const int64_t e = i / ns;
+        const int n = static_cast<int>(i - e * ns);
+        scales[i] = n < N ? s[e * N + n] : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------- product
+//
+// Items: up to 96 rows of one expert x 128 output columns; each of the four
+// waves owns one 32-column block over the whole summed dimension, its weights
+// one coalesced 1 KiB load a step and the token operands loaded straight from
+// the quantized rows.  The sums are exact in 32-bit integers.
+constexpr int I8_GROUP = 96;
+
+__device__ __forceinline__ int i8_groups(int m) { return (m + I8_GROUP - 1) / I8_GROUP; }
+
+// Exclusive prefix sums of count(rows of e) over the experts, and the clamped
+// offsets (256 threads; E <= GG_KMAX_EXPERTS).
+template <typename F>
+__device__ __forceinline__ void prefix_experts(const int64_t* __restrict__ offsets, int E, int M, int* s_off,
+                                               int* s_pre, F&& count) {
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+        int64_t o = offsets[e];
+        o = o < 0 ? 0 : (o > M ? M : o);
+        s_off[e] = static_cast<int>(o);
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x, per = (E + 63) / 64;
+        const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) sum += count(max(0, s_off[e + 1] - s_off[e]));
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(incl, d, 64);
+            if (lane >= d) incl += v;
+        }
+        int run = incl - sum;
+        for (int e = e0; e < e1; ++e) {
+            s_pre[e] = run;
+            run += count(max(0, s_off[e + 1] - s_off[e]));
+        }
+        if (lane == 63) s_pre[E] = incl;
+    }
+    __syncthreads();
+}
+
+template <int TB>
+__device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
+                                               int nb, int nblocks, int nsteps) {
+    constexpr int G = TB == 1 ? 8 : 4;   // steps loaded at a time
+    const int lane = threadIdx.x & 63;
+    const int8_t* wp = w + static_cast<int64_t>(min(nb, nblocks - 1)) * nsteps * 1024 + lane * 16;
+    const int8_t* tp[TB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * p.ldq + 16 * (lane >> 5);
+    i32x16 acc[TB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[i][x] = 0;
+    i32x4 wv[2][G], tv[2][G][TB];
+    auto load = [&](int buf, int g) {
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            const int st = min(g + u, nsteps - 1);
+            wv[buf][u] = *reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024);
+#pragma unroll
+            for (int i = 0; i < TB; ++i) tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + st * 32);
+        }
+    };
+    auto mma = [&](int buf, int g) {
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+            if (g + u < nsteps) {
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[buf][u], tv[buf][u][i], acc[i], 0, 0, 0);
+            }
+    };
+    load(0, 0);
+    for (int g = 0; g < nsteps; g += 2 * G) {
+        load(1, g + G);
+        mma(0, g);
+        load(0, g + 2 * G);
+        mma(1, g + G);
+    }
+    if (nb >= nblocks) return;
+    // lane holds token lane & 31 of each block and, in register 4q + x, column 8q + 4(lane >> 5) + x
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+        const int r = i * 32 + (lane & 31);
+        if (r >= rows) continue;
+        const float sr = p.s[row0 + r];
+        uint16_t* orow = p.out + static_cast<int64_t>(row0 + r) * p.N;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int n = nb * 32 + 8 * q + 4 * (lane >> 5);
+            if (n >= p.N) continue;
+            float y[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) y[x] = static_cast<float>(acc[i][4 * q + x]) * sr;
+            if (ws) {
+                const float4 c = *reinterpret_cast<const float4*>(ws + n);
+                y[0] *= c.x;
+                y[1] *= c.y;
+                y[2] *= c.z;
+                y[3] *= c.w;
+            }
+            *reinterpret_cast<uint2*>(orow + n) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
+    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
+    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
+    const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32;
+    const int items_n = (nblocks + 3) / 4;
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(m) * items_n; });
+    const int total = uni(s_pre[p.E]);
+    const int wave = uni(threadIdx.x >> 6);
+    for (int it = blockIdx.x; it < total; it += gridDim.x) {
+        const int e = uni(find_expert(s_pre, p.E, it));
+        const int local = it - uni(s_pre[e]);
+        const int grp = local / items_n, col = local - grp * items_n;
+        const int row0 = uni(s_off[e]) + grp * I8_GROUP;
+        const int rows = min(I8_GROUP, uni(s_off[e + 1]) - row0);
+        const int8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
+        const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
+        const int nb = col * 4 + wave;
+        if (rows <= 32) i8_stream_item<1>(p, w, ws, row0, rows, nb, nblocks, nsteps);
+        else if (rows <= 64) i8_stream_item<2>(p, w, ws, row0, rows, nb, nblocks, nsteps);
+        else i8_stream_item<3>(p, w, ws, row0, rows, nb, nblocks, nsteps);
+    }
+}
+
+// ---------------------------------------------------------------- launchers
+template <int MODE>
+static hipError_t launch_quant(const QuantParams& p, int num_cu, hipStream_t s) {
+    const int units = p.K / QuantUnit<MODE>::VALS;
+    const int64_t want = (static_cast<int64_t>(p.M) + 3) / 4, most = static_cast<int64_t>(num_cu) * 16;
+    const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(256);
+    if (units <= 64) hipLaunchKernelGGL((quant_rows_kernel<MODE, 1>), grid, block, 0, s, p);
+    else if (units <= 128) hipLaunchKernelGGL((quant_rows_kernel<MODE, 2>), grid, block, 0, s, p);
+    else if (units <= 256) hipLaunchKernelGGL((quant_rows_kernel<MODE, 4>), grid, block, 0, s, p);
+    else if (units <= 512 && MODE != Q_DGLU) hipLaunchKernelGGL((quant_rows_kernel<MODE, MODE == Q_DGLU ? 4 : 8>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((quant_rows_kernel<MODE, 0>), grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_quant_rows(QuantMode mode, const QuantParams& p, int num_cu, hipStream_t s) {
+    if (p.M <= 0) return hipSuccess;
+    switch (mode) {
+        case Q_PLAIN: return launch_quant<Q_PLAIN>(p, num_cu, s);
+        case Q_GLU: return launch_quant<Q_GLU>(p, num_cu, s);
+        case Q_SCALED: return launch_quant<Q_SCALED>(p, num_cu, s);
+        default: return launch_quant<Q_DGLU>(p, num_cu, s);
+    }
+}
+
+hipError_t launch_int8_pack(const int8_t* q, const float* s, int E, int N, int K, int transposed, int8_t* packed,
+                            hipStream_t stream) {
+    const int64_t rows = i8_rows_p(transposed ? K : N), cont = i8_cont_p(transposed ? N : K);
+    const int64_t bytes = E * rows * cont;
+    int64_t blocks = (bytes / 16 + 255) / 256;
+    if (blocks > 65536) blocks = 65536;
+    hipLaunchKernelGGL(int8_pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, q, s, E, N, K,
+                       transposed, packed, reinterpret_cast<float*>(packed + bytes), static_cast<int>(i8_cont_p(N)));
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
+    const int64_t items_n = (p.N + 127) / 128;
+    const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E)) * items_n;
+    const int64_t most = static_cast<int64_t>(num_cu) * 2;
+    hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace gg
