@@ -315,6 +315,42 @@ int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_
                   int64_t E, int64_t N, int64_t K, int activation, void* dh1_out,
                   void* workspace, size_t workspace_bytes, void* dx, hipStream_t stream);
 
+/* ---- Low-rank adapters of the experts (trainable; next to a frozen product).
+ *
+ * For an expert e with a_e [r][K] and b_e [N][r] (bf16), over its rows:
+ *
+ *   forward    u = bf16(x a_e^T) [rows][r]      y = bf16(base + scale u b_e^T) [rows][N]
+ *   backward   du = scale dy b_e                dx = bf16(base + du a_e) [rows][K]
+ *              da_e = du^T x [r][K] (fp32)      db_e = scale dy^T u [N][r] (fp32)
+ *
+ * base is the frozen product's y (forward) or dx (backward), or NULL for
+ * none; it may be the output itself.  Sums are fp32.  u is rounded to bf16
+ * once, where it is saved.  du is rounded to bf16 for dx (whose output is
+ * bf16) and kept to 16 bits of mantissa for da.  Every sum has a fixed order:
+ * equal calls give equal bits.  da and db are written for every expert
+ * (zeros without rows), or, with accumulate != 0, added to.
+ *
+ * x, u, y, dy, dx, a, b: DEVICE bf16; da, db: DEVICE fp32; 16-byte aligned.
+ * Limits: 1 <= E <= GG_MAX_EXPERTS; N and K positive multiples of 8 below
+ * 2^22; 1 <= r <= GG_ADAPTER_MAX_RANK; 0 <= M < 2^31.  Conventions as above. */
+#define GG_ADAPTER_MAX_RANK 64
+
+/* Forward: x [M][K], base [M][N] or NULL; writes u [M][r] and y [M][N].  One launch. */
+int gg_adapter_forward(const void* x, const int64_t* offsets, int64_t M, const void* a, const void* b,
+                       int64_t E, int64_t N, int64_t K, int64_t r, float scale, const void* base,
+                       void* u, void* y, hipStream_t stream);
+
+/* Bytes of the workspace of gg_adapter_backward. */
+size_t gg_adapter_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r);
+
+/* Backward: dy [M][N], x [M][K], u [M][r] (the forward's), base [M][K] or
+ * NULL; writes dx [M][K], da [E][r][K] and db [E][N][r].  M == 0 writes da
+ * and db only (zeros, or nothing with accumulate).  Four launches. */
+int gg_adapter_backward(const void* dy, const void* x, const void* u, const int64_t* offsets, int64_t M,
+                        const void* a, const void* b, int64_t E, int64_t N, int64_t K, int64_t r, float scale,
+                        const void* base, void* workspace, size_t workspace_bytes,
+                        void* dx, float* da, float* db, int accumulate, hipStream_t stream);
+
 /* ---- For callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid allocation).
  * gg_dgrad without a workspace argument: dH1 goes to a static device array

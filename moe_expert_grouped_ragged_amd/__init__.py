@@ -65,7 +65,8 @@ EXPORTED = ("gg_status_string", "gg_packed_bytes", "gg_dgrad_workspace_bytes", "
             "gg_frag_bytes", "gg_pack_frag", "gg_forward_fc2_frag", "gg_dgrad_noalloc",
             "gg_scale_rows", "gg_scale_rows_backward",
             "gg_int8_quantize_rows", "gg_int8_packed_bytes", "gg_int8_pack", "gg_int8_workspace_bytes",
-            "gg_int8_forward", "gg_int8_dgrad")
+            "gg_int8_forward", "gg_int8_dgrad",
+            "gg_adapter_forward", "gg_adapter_workspace_bytes", "gg_adapter_backward")
 
 
 def _load() -> ctypes.CDLL:
@@ -105,10 +106,16 @@ def _load() -> ctypes.CDLL:
     lib.gg_int8_workspace_bytes.restype = sz
     lib.gg_int8_forward.argtypes = [p, p, i64, p, i64, i64, i64, i32, p, p, sz, p, p]
     lib.gg_int8_dgrad.argtypes = [p, p, p, i64, p, i64, i64, i64, i32, p, p, sz, p, p]
+    f32 = ctypes.c_float
+    lib.gg_adapter_forward.argtypes = [p, p, i64, p, p, i64, i64, i64, i64, f32, p, p, p, p]
+    lib.gg_adapter_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.gg_adapter_workspace_bytes.restype = sz
+    lib.gg_adapter_backward.argtypes = [p, p, p, p, i64, p, p, i64, i64, i64, i64, f32, p, p, sz, p, p, p, i32, p]
     for name in ("gg_pack_weights", "gg_pack_frag", "gg_forward_fc1_swiglu", "gg_forward_fc2",
                  "gg_forward_fc2_frag", "gg_dgrad", "gg_round_bf16", "gg_forward_fc1_glu", "gg_dgrad_glu",
                  "gg_dgrad_recompute", "gg_dgrad_noalloc", "gg_scale_rows", "gg_scale_rows_backward",
-                 "gg_int8_quantize_rows", "gg_int8_pack", "gg_int8_forward", "gg_int8_dgrad"):
+                 "gg_int8_quantize_rows", "gg_int8_pack", "gg_int8_forward", "gg_int8_dgrad",
+                 "gg_adapter_forward", "gg_adapter_backward"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -689,6 +696,86 @@ def gg_int8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
                              _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                              dx.data_ptr(), _stream_ptr(stream, dev)), "gg_int8_dgrad")
     return dx, dh1_out
+
+
+ADAPTER_MAX_RANK = 64    # GG_ADAPTER_MAX_RANK of include/gg.h
+
+
+def adapter_workspace_bytes(M: int, E: int, N: int, K: int, r: int) -> int:
+    return int(lib.gg_adapter_workspace_bytes(M, E, N, K, r))
+
+
+def _adapter(x, offsets, a, b):
+    """The checked operands' sizes (M, E, N, K, r)."""
+    _bf16_cuda(x, "x")
+    _bf16_cuda(a, "a", device=x.device)
+    if x.dim() != 2 or a.dim() != 3 or a.shape[2] != x.shape[1]:
+        raise ValueError("x must be [M, K] and a [E, r, K]")
+    E, r, K = a.shape
+    _bf16_cuda(b, "b", device=x.device)
+    if b.dim() != 3 or b.shape[0] != E or b.shape[2] != r:
+        raise ValueError(f"b must be [E, N, r] with E={E}, r={r}, got {tuple(b.shape)}")
+    if not 1 <= r <= ADAPTER_MAX_RANK:
+        raise ValueError(f"the rank must be 1 .. {ADAPTER_MAX_RANK}, got {r}")
+    _offsets(offsets, E, x.device)
+    return x.shape[0], E, b.shape[1], K, r
+
+
+def gg_adapter_forward(x: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: float,
+                       base: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None,
+                       y: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                       ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Low-rank adapters: y = base + scale * (x a_e^T) b_e^T for the rows of
+    each expert -> (y [M, N], u = x a_e^T [M, r] for the backward).  a [E, r, K],
+    b [E, N, r], all bf16.  y may be base (in place)."""
+    M, E, N, K, r = _adapter(x, offsets, a, b)
+    dev = x.device
+    if base is not None:
+        _bf16_cuda(base, "base", shape=(M, N), device=dev)
+    if u is not None:
+        _bf16_cuda(u, "u", shape=(M, r), device=dev)
+    y = _out(y, (M, N), "y", dev)
+    u = _out(u, (M, r), "u", dev)
+    _check(lib.gg_adapter_forward(x.data_ptr(), offsets.data_ptr(), M, a.data_ptr(), b.data_ptr(), E, N, K, r, scale,
+                                  _ptr(base), u.data_ptr(), y.data_ptr(), _stream_ptr(stream, dev)),
+           "gg_adapter_forward")
+    return y, u
+
+
+def gg_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor,
+                        b: torch.Tensor, scale: float, base: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None, da: Optional[torch.Tensor] = None,
+                        db: Optional[torch.Tensor] = None, accumulate: bool = False,
+                        workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of gg_adapter_forward: (dx = base + du a_e [M, K] bf16, da
+    [E, r, K] float32, db [E, N, r] float32) with du = scale * dy b_e.  base is
+    the frozen product's input gradient (dx may be base).  accumulate: da and
+    db are given and added to."""
+    M, E, N, K, r = _adapter(x, offsets, a, b)
+    dev = x.device
+    _bf16_cuda(dy, "dy", shape=(M, N), device=dev)
+    _bf16_cuda(u, "u", shape=(M, r), device=dev)
+    if base is not None:
+        _bf16_cuda(base, "base", shape=(M, K), device=dev)
+    if accumulate and (da is None or db is None):
+        raise ValueError("accumulate needs da and db")
+    if da is not None:
+        _typed_cuda(da, torch.float32, "da", (E, r, K), dev)
+    if db is not None:
+        _typed_cuda(db, torch.float32, "db", (E, N, r), dev)
+    if dx is not None:
+        _bf16_cuda(dx, "dx", shape=(M, K), device=dev)
+    workspace = _workspace(workspace, adapter_workspace_bytes(M, E, N, K, r), dev)
+    dx = _out(dx, (M, K), "dx", dev)
+    da = torch.empty(E, r, K, dtype=torch.float32, device=dev) if da is None else da
+    db = torch.empty(E, N, r, dtype=torch.float32, device=dev) if db is None else db
+    _check(lib.gg_adapter_backward(dy.data_ptr(), x.data_ptr(), u.data_ptr(), offsets.data_ptr(), M, a.data_ptr(),
+                                   b.data_ptr(), E, N, K, r, scale, _ptr(base), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), dx.data_ptr(), da.data_ptr(),
+                                   db.data_ptr(), int(bool(accumulate)), _stream_ptr(stream, dev)),
+           "gg_adapter_backward")
+    return dx, da, db
 
 
 class ScaleRows(torch.autograd.Function):

@@ -15,8 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgg.so")
 
-SOURCES = ["gg_api.cpp", "gg_kernels.hip", "gg_noalloc.hip", "gg_int8_api.cpp", "gg_int8.hip"]
-HEADERS = ["gg_device.h", "gg_host.h", "gg_kernels.h", "gg_int8.h"]
+SOURCES = ["gg_api.cpp", "gg_kernels.hip", "gg_noalloc.hip", "gg_int8_api.cpp", "gg_int8.hip",
+           "gg_adapter_api.cpp", "gg_adapter.hip"]
+HEADERS = ["gg_device.h", "gg_host.h", "gg_kernels.h", "gg_int8.h", "gg_adapter.h"]
 
 # Packed-fp32 VALU ops are disabled for all device code.
 HIP_FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",

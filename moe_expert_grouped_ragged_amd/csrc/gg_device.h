@@ -1,6 +1,6 @@
 // Device helpers shared by the kernel files: bf16 conversion and packing,
-// memory waits and barriers, LDS-DMA copies, and the search of an expert in a
-// prefix sum.
+// memory waits and barriers, LDS-DMA copies, and the prefix sums over experts
+// that turn a work item's number into its expert.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -128,6 +128,55 @@ __device__ __forceinline__ void static_for(F&& f) {
         f(GrpTag<I>{});
         static_for<N, I + 1>(f);
     }
+}
+
+// Exclusive prefix sums of count(rows of e) over the experts, and the offsets
+// (every thread of the workgroup calls it).  The offsets are clamped into
+// [0, M] and made non-decreasing by a running maximum, so bad offsets cannot
+// count more rows than M.
+template <typename F>
+__device__ __forceinline__ void prefix_experts(const int64_t* __restrict__ offsets, int E, int M, int* s_off,
+                                               int* s_pre, F&& count) {
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+        int64_t o = offsets[e];
+        o = o < 0 ? 0 : (o > M ? M : o);
+        s_off[e] = static_cast<int>(o);
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x, per = E / 64 + 1;
+        const int e0 = min(E + 1, lane * per), e2 = min(E + 1, e0 + per), e1 = min(E, e2);
+        int top = 0;
+        for (int e = e0; e < e2; ++e) {
+            top = max(top, s_off[e]);
+            s_off[e] = top;
+        }
+        int before = __shfl_up(top, 1, 64);
+        if (lane == 0) before = 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(before, d, 64);
+            if (lane >= d) before = max(before, v);
+        }
+        for (int e = e0; e < e2; ++e) s_off[e] = max(s_off[e], before);
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the next lane's first offset
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) sum += count(s_off[e + 1] - s_off[e]);
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(incl, d, 64);
+            if (lane >= d) incl += v;
+        }
+        int run = incl - sum;
+        for (int e = e0; e < e1; ++e) {
+            s_pre[e] = run;
+            run += count(s_off[e + 1] - s_off[e]);
+        }
+        if (lane == 63) s_pre[E] = incl;
+    }
+    __syncthreads();
 }
 
 }  // namespace gg

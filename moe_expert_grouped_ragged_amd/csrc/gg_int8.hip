@@ -254,38 +254,6 @@ constexpr int I8_GROUP = 96;
 
 __device__ __forceinline__ int i8_groups(int m) { return (m + I8_GROUP - 1) / I8_GROUP; }
 
-// Exclusive prefix sums of count(rows of e) over the experts, and the clamped
-// offsets (256 threads; E <= GG_KMAX_EXPERTS).
-template <typename F>
-__device__ __forceinline__ void prefix_experts(const int64_t* __restrict__ offsets, int E, int M, int* s_off,
-                                               int* s_pre, F&& count) {
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-        int64_t o = offsets[e];
-        o = o < 0 ? 0 : (o > M ? M : o);
-        s_off[e] = static_cast<int>(o);
-    }
-    __syncthreads();
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x, per = (E + 63) / 64;
-        const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
-        int sum = 0;
-        for (int e = e0; e < e1; ++e) sum += count(max(0, s_off[e + 1] - s_off[e]));
-        int incl = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(incl, d, 64);
-            if (lane >= d) incl += v;
-        }
-        int run = incl - sum;
-        for (int e = e0; e < e1; ++e) {
-            s_pre[e] = run;
-            run += count(max(0, s_off[e + 1] - s_off[e]));
-        }
-        if (lane == 63) s_pre[E] = incl;
-    }
-    __syncthreads();
-}
-
 template <int TB>
 __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
                                                int nb, int nblocks, int nsteps) {
