@@ -326,7 +326,7 @@ int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_
  * base is the frozen product's y (forward) or dx (backward), or NULL for
  * none; it may be the output itself.  Sums are fp32.  u is rounded to bf16
  * once, where it is saved.  du is rounded to bf16 for dx (whose output is
- * bf16) and kept to 16 bits of mantissa for da.  Every sum has a fixed order:
+ * bf16) and kept whole, as three bf16 parts, for da.  Every sum has a fixed order:
  * equal calls give equal bits.  da and db are written for every expert
  * (zeros without rows), or, with accumulate != 0, added to.
  *

@@ -33,7 +33,7 @@ struct AdapterParams {
     int rows1, rows2;         // rows of a unit of the output-side and of the input-side kernel
     float* du_part;           // [chunks of N][blocks * 32][rp]: partial sums of du over the columns of a chunk
     uint16_t* du;             // [blocks][32][max(rp, 32)] bf16
-    uint16_t* du_t;           // [blocks][2][rp][32] bf16: du = high + low parts, transposed
+    uint16_t* du_t;           // [blocks][3][rp][32] bf16: du as the sum of three parts, transposed
     float* db_part;           // [slots1][N][r]: db of the units of experts with several
     float* da_part;           // [slots2][r][K]
     int64_t blocks;           // upper bound of the row blocks

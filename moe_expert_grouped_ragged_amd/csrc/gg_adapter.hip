@@ -209,8 +209,7 @@ __global__ __launch_bounds__(256) void adapter_forward_kernel(const AdapterParam
 //      columns.  It reads dy once and makes both products of it: db (summed
 //      over the rows in registers) and the chunk's part of du = scale dy b.
 //   2  du: the chunks' parts added in order, rounded to bf16 for dx, and kept
-//      as the sum of two bf16 values (16 bits of mantissa) for da, whose
-//      output is fp32.
+//      whole as the sum of three bf16 values for da, whose output is fp32.
 //   3  input side: a unit is up to rows2 rows of one expert x 512 columns of x:
 //      da (summed in registers) and dx = base + du a.
 //   4  experts with several units: their parts added in order; experts without
@@ -430,11 +429,15 @@ __global__ __launch_bounds__(256) void adapter_du_kernel(const AdapterParams p, 
         float v = 0.0f;
         for (int k = 0; k < chunks; ++k) v += src[static_cast<int64_t>(k) * p.blocks * AD_BLK * RP];
         v *= p.scale;
-        const uint16_t hi = f2bf(v), lo = f2bf(v - bf2f(hi));
+        const uint16_t hi = f2bf(v);
+        const float rest = v - bf2f(hi);
+        const uint16_t mid = f2bf(rest), lo = f2bf(rest - bf2f(mid));
         p.du[(blk * AD_BLK + row) * UW + c] = hi;
         if (RP < UW) p.du[(blk * AD_BLK + row) * UW + RP + c] = 0;
-        p.du_t[(blk * 2 * RP + c) * AD_BLK + row] = hi;
-        p.du_t[((blk * 2 + 1) * RP + c) * AD_BLK + row] = lo;
+        uint16_t* t = p.du_t + (blk * 3 * RP + c) * AD_BLK + row;
+        t[0] = hi;
+        t[RP * AD_BLK] = mid;
+        t[2 * RP * AD_BLK] = lo;
     }
 }
 
@@ -488,12 +491,12 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
                     if (p.base && rr < un.rows && c < K)
                         base[i][h][q] = ld16(p.base + static_cast<int64_t>(un.row0 + rr) * K + c);
                 }
-        bf16x8 dt[2][NT], dr[2][KS];
+        bf16x8 dt[3][NT], dr[2][KS];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 3; ++q)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                dt[q][j] = as_bf16x8(ld16(p.du_t + ((blk * 2 + q) * RP + 16 * j + l16) * AD_BLK + 8 * g));
+                dt[q][j] = as_bf16x8(ld16(p.du_t + ((blk * 3 + q) * RP + 16 * j + l16) * AD_BLK + 8 * g));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -506,10 +509,9 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                acc[c][j] = mfma16(as_bf16x8(tr[c]), dt[0][j], acc[c][j]);
-                acc[c][j] = mfma16(as_bf16x8(tr[c]), dt[1][j], acc[c][j]);
-            }
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int q = 2; q >= 0; --q) acc[c][j] = mfma16(as_bf16x8(tr[c]), dt[q][j], acc[c][j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll

@@ -53,7 +53,7 @@ Workspace workspace_of(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     };
     w.du_part = take(chunks * w.blocks * AD_BLK * rp * 4);
     w.du = take(w.blocks * AD_BLK * (rp < 32 ? 32 : rp) * 2);
-    w.du_t = take(w.blocks * AD_BLK * rp * 4);
+    w.du_t = take(w.blocks * AD_BLK * rp * 6);
     // an expert with m > rows has ceil(m / rows) < 2 m / rows parts
     w.db_part = take(M > w.rows1 ? 2 * M / w.rows1 * N * r * 4 : 0);
     w.da_part = take(M > w.rows2 ? 2 * M / w.rows2 * K * r * 4 : 0);

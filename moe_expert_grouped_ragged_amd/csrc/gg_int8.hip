@@ -12,6 +12,7 @@ namespace gg {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(16))) int i32x16;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 // ---------------------------------------------------------------- quantization
 //
@@ -246,13 +247,24 @@ __global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __re
 
 // ---------------------------------------------------------------- product
 //
-// Items: up to 96 rows of one expert x 128 output columns; each of the four
-// waves owns one 32-column block over the whole summed dimension, its weights
-// one coalesced 1 KiB load a step and the token operands loaded straight from
-// the quantized rows.  The sums are exact in 32-bit integers.
+// The sums are exact in 32-bit integers, so the two kernels below give the
+// same bits.  Rows that fill 256-row tiles (the last may be partial) run as
+// 256 x 256 tiles; at most 96 rows of an expert (all of a small one) run as
+// streaming items, which read each weight byte once for all of them.
+//
+// Streaming items: up to 96 rows of one expert x 128 output columns; each of
+// the four waves owns one 32-column block over the whole summed dimension, its
+// weights one coalesced 1 KiB load a step and the token operands loaded
+// straight from the quantized rows.
 constexpr int I8_GROUP = 96;
+constexpr int I8_TILE = 256;
 
 __device__ __forceinline__ int i8_groups(int m) { return (m + I8_GROUP - 1) / I8_GROUP; }
+// Rows of an expert that tiles cover.
+__device__ __forceinline__ int i8_tile_rows(int m) {
+    const int tail = m % I8_TILE;
+    return tail <= I8_GROUP ? m - tail : m;
+}
 
 template <int TB>
 __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
@@ -327,21 +339,237 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
     const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32;
     const int items_n = (nblocks + 3) / 4;
-    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(m) * items_n; });
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(p.tiles ? m - i8_tile_rows(m) : m) * items_n; });
     const int total = uni(s_pre[p.E]);
     const int wave = uni(threadIdx.x >> 6);
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
         const int e = uni(find_expert(s_pre, p.E, it));
         const int local = it - uni(s_pre[e]);
         const int grp = local / items_n, col = local - grp * items_n;
-        const int row0 = uni(s_off[e]) + grp * I8_GROUP;
-        const int rows = min(I8_GROUP, uni(s_off[e + 1]) - row0);
+        const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
+        const int row0 = lo + (p.tiles ? i8_tile_rows(hi - lo) : 0) + grp * I8_GROUP;
+        const int rows = min(I8_GROUP, hi - row0);
         const int8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
         const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
         const int nb = col * 4 + wave;
         if (rows <= 32) i8_stream_item<1>(p, w, ws, row0, rows, nb, nblocks, nsteps);
         else if (rows <= 64) i8_stream_item<2>(p, w, ws, row0, rows, nb, nblocks, nsteps);
         else i8_stream_item<3>(p, w, ws, row0, rows, nb, nblocks, nsteps);
+    }
+}
+
+// Tiles: 256 rows x 256 output columns by four waves, each 128 x 128 (4 x 4
+// accumulators of 32 x 32).  Rows and weights stream into a 4-slot LDS ring of
+// 64-byte stages by LDS-DMA, up to four stages ahead: 16 KiB of rows, 16-byte
+// chunk c of row r at c ^ ((r >> 2) & 3), and 16 KiB of weights as they lie in
+// the packed layout; fragment reads of both are free of bank conflicts.  Each
+// of a stage's two 32-byte steps is 16 matrix instructions a wave, while the
+// next step's eight fragments are read; the only barrier of a stage sits
+// before its second step, where the next stage has landed and every wave has
+// read the last fragments of this one, whose slot is refilled from there on.
+// The epilogue scales and rounds through a small staging area of its own, so
+// the next tile's first stages are already on their way.
+constexpr int I8_STAGE = 64, I8_SLOTS = 4;
+constexpr int I8_SLOT_BYTES = 2 * I8_TILE * I8_STAGE;
+constexpr int I8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf16
+
+__device__ __forceinline__ int acc_rd_i(int a) {
+    int v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+    return v;
+}
+
+__global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
+    __shared__ __attribute__((aligned(1024))) int8_t s_ring[I8_SLOTS * I8_SLOT_BYTES];
+    __shared__ __attribute__((aligned(16))) int8_t s_stg[4 * I8_STG_BYTES];
+    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
+    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
+    const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32, nstages = p.ldq / I8_STAGE;
+    const int tiles_n = (p.N + I8_TILE - 1) / I8_TILE;
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
+                   [&](int m) { return (i8_tile_rows(m) + I8_TILE - 1) / I8_TILE * tiles_n; });
+    const int n_tiles = uni(s_pre[p.E]);
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int wr = wave >> 1, wc = wave & 1;      // the wave's 128 rows and 128 columns
+    // consecutive tiles to the workgroups of one XCD, which share an L2
+    const int G = gridDim.x, b = blockIdx.x;
+    const int slot = (G % 8 == 0) ? (b & 7) * (G >> 3) + (b >> 3) : b;
+    const uint32_t ring = lds_addr(s_ring);
+
+    // what the copies of one tile read
+    const int8_t* t_base = nullptr;   // its first row
+    const int8_t* w_base = nullptr;   // its expert's matrix
+    uint32_t t_voff[4];               // this lane's chunks of rows 64 wave + 16 i ..
+    int wb[2];                        // this wave's two 32-column blocks
+    int e = 0, row0 = 0, rows = 0, col0 = 0;
+    auto setup = [&](int t) {
+        e = uni(find_expert(s_pre, p.E, t));
+        const int local = t - uni(s_pre[e]);
+        const int lo = uni(s_off[e]), m = i8_tile_rows(uni(s_off[e + 1]) - lo);
+        const int tiles_m = (m + I8_TILE - 1) / I8_TILE;
+        const int tm = local % tiles_m, tn = local / tiles_m;
+        row0 = lo + tm * I8_TILE;
+        rows = min(I8_TILE, m - tm * I8_TILE);
+        col0 = tn * I8_TILE;
+        t_base = p.q + static_cast<int64_t>(row0) * p.ldq;
+        w_base = p.w + static_cast<int64_t>(e) * p.w_stride;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 64 * wave + 16 * i + (lane >> 2);
+            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            t_voff[i] = static_cast<uint32_t>(min(r, rows - 1)) * p.ldq + 16 * c;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wb[i] = min(col0 / 32 + 2 * wave + i, nblocks - 1);
+    };
+    // half h of stage st (past the end: the last stage again, into a slot that is not read)
+    auto copy = [&](int st, int h) {
+        const int ss = min(st, nstages - 1);
+        const uint32_t dst = ring + (st & 3) * I8_SLOT_BYTES;
+#pragma unroll
+        for (int i = 2 * h; i < 2 * h + 2; ++i)
+            dma16(t_base + ss * I8_STAGE, t_voff[i], dst + (64 * wave + 16 * i) * I8_STAGE);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            dma16(w_base + (static_cast<int64_t>(wb[h]) * nsteps + 2 * ss + u) * 1024, lane * 16,
+                  dst + I8_TILE * I8_STAGE + ((2 * wave + h) * 2 + u) * 1024);
+    };
+
+    i32x16 acc[4][4];    // [row block][column block]
+    i32x4 tf[2][4], wf[2][4];
+    auto read = [&](int st, auto u_tag) {
+        constexpr int u = decltype(u_tag)::value;
+        const int8_t* sl = s_ring + (st & 3) * I8_SLOT_BYTES;
+        const int c = (2 * u + (lane >> 5)) ^ ((lane >> 2) & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            tf[u][i] = *reinterpret_cast<const i32x4*>(sl + (128 * wr + 32 * i + (lane & 31)) * I8_STAGE + 16 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            wf[u][j] = *reinterpret_cast<const i32x4*>(sl + I8_TILE * I8_STAGE + ((4 * wc + j) * 2 + u) * 1024 + lane * 16);
+    };
+    auto mma = [&](auto u_tag, auto first_tag) {
+        constexpr int u = decltype(u_tag)::value;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (decltype(first_tag)::value != 0)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], i32x16{}, 0, 0, 0);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], acc[i][j], 0, 0, 0);
+            }
+    };
+    // issue order of a step: a fragment read between every two matrix instructions
+    auto interleave = [&]() {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // two matrix instructions
+        }
+    };
+    auto stage = [&](int st, auto first_tag) {
+        read(st, GrpTag<1>{});
+        mma(GrpTag<0>{}, first_tag);
+        copy(st + 3, 1);
+        interleave();
+        // stage st + 1 has landed (the two after it may be under way), and
+        // every wave holds its last fragments of stage st
+        wait_vmcnt<16>();
+        block_barrier();
+        read(st + 1, GrpTag<0>{});
+        mma(GrpTag<1>{}, GrpTag<0>{});
+        copy(st + 4, 0);
+        interleave();
+    };
+    // the copies before a tile's first stage: 0 .. 2 and the first half of 3
+    auto prologue = [&]() {
+#pragma unroll
+        for (int st = 0; st < 3; ++st) {
+            copy(st, 0);
+            copy(st, 1);
+        }
+        copy(3, 0);
+    };
+
+    int t = slot;
+    if (t < n_tiles) {
+        setup(t);
+        prologue();
+    }
+    while (t < n_tiles) {
+        wait_vmcnt<20>();        // stage 0; whatever was issued after it may be under way
+        block_barrier();
+        read(0, GrpTag<0>{});
+        stage(0, GrpTag<1>{});
+        for (int st = 1; st < nstages - 1; ++st) stage(st, GrpTag<0>{});
+        // the scales of this tile, loaded during its last stage (nstages is even): lane holds, of
+        // block (i, j), row 32 i + (lane & 31) and columns 32 j + 8 q + 4 (lane >> 5) .. + 3
+        const int prow0 = row0, prows = rows, gc0 = col0 + 128 * wc;
+        const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
+        float sr[4];
+        f32x4 cs[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sr[i] = p.s[row0 + min(128 * wr + 32 * i + (lane & 31), rows - 1)];
+        if (ws) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    cs[j][q] = *reinterpret_cast<const f32x4*>(ws + min(gc0 + 32 * j + 8 * q + 4 * (lane >> 5), p.N - 4));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) cs[j][q] = f32x4{1.f, 1.f, 1.f, 1.f};
+        }
+        stage(nstages - 1, GrpTag<0>{});
+        t += G;
+        wait_vmcnt<0>();         // the scales, and the copies past the end
+        // held from here on, so that nothing waits for them behind the next tile's copies
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm volatile("" : "+v"(sr[i]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(cs[i][q]));
+        }
+        block_barrier();         // and every wave is done with the ring
+        if (t < n_tiles) {
+            setup(t);
+            prologue();
+        }
+        mfma_drain();
+        int opaque = 0;
+        asm volatile("" : "+s"(opaque));
+        const int ln = lane + opaque;
+        uint16_t* stg = reinterpret_cast<uint16_t*>(s_stg + wave * I8_STG_BYTES) + opaque;
+#pragma unroll
+        for (int jh = 0; jh < 2; ++jh)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // [32 rows][64 columns] (128-byte rows); 16-byte chunk c of row r at c ^ (r & 7)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const i32x16& a = acc[i][2 * jh + j];
+                        const float y0 = static_cast<float>(acc_rd_i(a[4 * q])) * sr[i] * cs[2 * jh + j][q][0];
+                        const float y1 = static_cast<float>(acc_rd_i(a[4 * q + 1])) * sr[i] * cs[2 * jh + j][q][1];
+                        const float y2 = static_cast<float>(acc_rd_i(a[4 * q + 2])) * sr[i] * cs[2 * jh + j][q][2];
+                        const float y3 = static_cast<float>(acc_rd_i(a[4 * q + 3])) * sr[i] * cs[2 * jh + j][q][3];
+                        const int rr = ln & 31, c = 4 * j + q;
+                        *reinterpret_cast<uint2*>(stg + rr * 64 + ((c ^ (rr & 7)) << 3) + 4 * (ln >> 5)) =
+                            make_uint2(pack2(y0, y1), pack2(y2, y3));
+                    }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rr = 8 * k + (ln >> 3), c = (ln & 7) ^ (rr & 7);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 64 + (ln & 7) * 8);
+                    const int gr = 128 * wr + 32 * i + rr, gc = gc0 + 64 * jh + 8 * c;
+                    if (gr < prows && gc < p.N)
+                        *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(prow0 + gr) * p.N + gc) = v;
+                }
+            }
     }
 }
 
@@ -381,10 +609,19 @@ hipError_t launch_int8_pack(const int8_t* q, const float* s, int E, int N, int K
 }
 
 hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
-    const int64_t items_n = (p.N + 127) / 128;
-    const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E)) * items_n;
+    // No expert of a batch of at most 96 rows has a tile.
+    Int8Params g = p;
+    g.tiles = p.M > I8_GROUP;
+    const int64_t few = p.M < p.E ? p.M : p.E;
+    if (g.tiles) {
+        const int64_t upper = (static_cast<int64_t>(p.M) / I8_TILE + few) * ((p.N + I8_TILE - 1) / I8_TILE);
+        hipLaunchKernelGGL(int8_tile_kernel, dim3(static_cast<unsigned>(upper < num_cu ? upper : num_cu)), dim3(256), 0, s, g);
+        const hipError_t st = hipGetLastError();
+        if (st != hipSuccess) return st;
+    }
+    const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + few) * ((p.N + 127) / 128);
     const int64_t most = static_cast<int64_t>(num_cu) * 2;
-    hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
     return hipGetLastError();
 }
 

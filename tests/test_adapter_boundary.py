@@ -12,9 +12,9 @@ def gg():
 
 
 def test_workspace(gg):
-    # 32-row blocks: du parts (fp32, one chunk of 1024 columns), du (bf16, 32 wide), du transposed (2 x bf16);
+    # 32-row blocks: du parts (fp32, one chunk of 1024 columns), du (bf16, 32 wide), du transposed (3 x bf16);
     # 100 rows of 3 experts make at most 100 // 32 + 3 blocks, and no expert has more than 256 rows
-    assert gg.adapter_workspace_bytes(100, 3, 64, 64, 16) == 6 * 32 * (16 * 4 + 32 * 2 + 16 * 4)
+    assert gg.adapter_workspace_bytes(100, 3, 64, 64, 16) == 6 * 32 * (16 * 4 + 32 * 2 + 16 * 6)
     assert gg.adapter_workspace_bytes(0, 3, 64, 64, 16) == 0
     for M, E, N, K, r in ((8, 0, 64, 64, 8), (8, 1, 60, 64, 8), (8, 1, 64, 4, 8), (8, 1, 64, 64, 0), (8, 1, 64, 64, 65)):
         assert gg.adapter_workspace_bytes(M, E, N, K, r) == 0
