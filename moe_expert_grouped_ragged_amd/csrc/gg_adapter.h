@@ -12,8 +12,11 @@ constexpr int AD_WCOLS = 128;    // columns a wavefront of the backward pass own
 
 // Rank padded to the matrix instruction's tiles: 16, 32 or 64.
 inline int ad_rank_p(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
-// Wavefronts of a workgroup of the output-side backward kernel (its columns / AD_WCOLS).
-inline int ad_waves(int rp) { return rp <= 32 ? 8 : 4; }
+// Wavefronts of a workgroup of the output-side backward kernel: at most (its
+// registers hold the columns' part of db), and at least; chunks of N columns.
+constexpr int ad_waves(int rp) { return rp <= 32 ? 8 : 4; }
+constexpr int ad_waves_min(int rp) { return ad_waves(rp) * 3 / 4; }
+inline int ad_chunks(int n, int rp) { return (n + ad_waves(rp) * AD_WCOLS - 1) / (ad_waves(rp) * AD_WCOLS); }
 
 struct AdapterParams {
     const uint16_t* x;        // [M][K]
@@ -37,6 +40,7 @@ struct AdapterParams {
     float* db_part;           // [slots1][N][r]: db of the units of experts with several
     float* da_part;           // [slots2][r][K]
     int64_t blocks;           // upper bound of the row blocks
+    int chunks1, chunks2;     // column chunks of the two kernels (set by the launcher)
 };
 
 hipError_t launch_adapter_forward(const AdapterParams& p, int num_cu, hipStream_t s);

@@ -19,111 +19,128 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 __device__ __forceinline__ bf16x8 as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8, v); }
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// Eight elements p[0], p[ld], ..., those at index >= n zero (n may be negative).
+// Eight elements p[0], p[ld], ..., of which the first n exist (p[0] is
+// readable in any case); the others are zero.  All eight loads are issued
+// without a branch between them.
 __device__ __forceinline__ uint4 gather8(const uint16_t* p, int64_t ld, int n) {
-    uint32_t w[4] = {0, 0, 0, 0};
+    uint32_t v[8];
+    const int top = max(n - 1, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[min(j, top) * ld];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (j < n) w[j >> 1] |= static_cast<uint32_t>(p[j * ld]) << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+        if (j >= n) v[j] = 0;
+    return make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
 }
 
 // ---------------------------------------------------------------- forward
 //
-// A workgroup owns up to 64 rows of one expert.  U = x a^T: the four waves
-// take 64-column groups of the rows in turn, each with all rows, and the
-// four partial sums meet in LDS in a fixed order; U is rounded to bf16 there
-// (it is saved and is the second product's operand).  Then each wave walks
-// 64-column tiles of y: the tile's columns are dealt to the instruction's
-// rows so that a lane ends up with 16 neighbouring columns of one token row,
-// and base and y move as whole 128-byte lines without passing through LDS.
-// With few row blocks the columns of y are split over workgroups, which each
-// compute U again.
+// A workgroup owns up to 64 rows of one expert, as up to four 16-row blocks.
+// U = x a^T: the four waves take 64-column groups of the rows in turn, each
+// with all rows, and the four partial sums meet in LDS in a fixed order; U is
+// rounded to bf16 there (it is saved and is the second product's operand).
+// Then each wave walks 64-column tiles of y: the tile's columns are dealt to
+// the instruction's rows so that a lane ends up with 16 neighbouring columns
+// of one token row, and base and y move as whole 128-byte lines without
+// passing through LDS.  With few row blocks the columns of y are split over
+// workgroups, which each compute U again.
 constexpr int AF_ROWS = 64;
 
+__device__ __forceinline__ uint4 and4(uint4 v, uint32_t m) { return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m); }
+
+// This wave's part of U for the NRB 16-row blocks from row0: groups wave,
+// wave + 4, ... of 64 columns, D of them loaded ahead while D are multiplied.
+// Lane: row 16 i + (lane & 15), ranks 16 j + 4 (lane >> 4) .. of acc[i][j].
+template <int NT, int NRB, int D>
+__device__ __forceinline__ void adapter_u(const AdapterParams& p, const uint16_t* ae, int row0, int rows, int wave,
+                                          f32x4 (&acc)[4][NT]) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+    const int K = p.K, groups = (K + 63) / 64;
+    const uint16_t* xr[NRB];
+    const uint16_t* ar[NT];
+#pragma unroll
+    for (int i = 0; i < NRB; ++i) xr[i] = p.x + static_cast<int64_t>(row0 + min(16 * i + l16, rows - 1)) * K;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) ar[j] = ae + static_cast<int64_t>(min(16 * j + l16, p.r - 1)) * K;
+    uint4 xv[2][D][2][NRB], av[2][D][2][NT];
+    // groups first, first + 4, ...; past the end of the columns both operands are zero
+    auto load = [&](int buf, int first) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int k = (first + 4 * d) * 64 + c * 32 + 8 * g;
+                const int kc = k < K ? k : 0;
+#pragma unroll
+                for (int i = 0; i < NRB; ++i) xv[buf][d][c][i] = ld16(xr[i] + kc);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) av[buf][d][c][j] = ld16(ar[j] + kc);
+            }
+    };
+    auto mma = [&](int buf, int first) {
+        if ((first + 4 * D - 3) * 64 > K) {
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t keep = (first + 4 * d) * 64 + c * 32 + 8 * g < K ? ~0u : 0u;
+#pragma unroll
+                    for (int i = 0; i < NRB; ++i) xv[buf][d][c][i] = and4(xv[buf][d][c][i], keep);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) av[buf][d][c][j] = and4(av[buf][d][c][j], keep);
+                }
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < NRB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        acc[i][j] = mfma16(as_bf16x8(av[buf][d][c][j]), as_bf16x8(xv[buf][d][c][i]), acc[i][j]);
+    };
+    int at = wave;
+    if (at < groups) load(0, at);
+    for (; at < groups; at += 8 * D) {
+        if (at + 4 * D < groups) load(1, at + 4 * D);
+        mma(0, at);
+        if (at + 4 * D < groups) {
+            if (at + 8 * D < groups) load(0, at + 8 * D);
+            mma(1, at + 4 * D);
+        }
+    }
+}
+
 template <int RP>
-__global__ __launch_bounds__(256) void adapter_forward_kernel(const AdapterParams p) {
+__global__ __launch_bounds__(256, 2) void adapter_forward_kernel(const AdapterParams p) {
     constexpr int NT = RP / 16;                  // rank tiles
     constexpr int UW = RP < 32 ? 32 : RP;        // U's width as an operand (zero-padded)
     constexpr int KS = UW / 32;
-    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
-    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
-    __shared__ float s_part[4][AF_ROWS][RP + 4];
+    __shared__ __attribute__((aligned(16))) float s_part[4][AF_ROWS][RP + 4];
     __shared__ __attribute__((aligned(16))) uint16_t s_u[AF_ROWS][UW + 8];
-    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [](int m) { return (m + AF_ROWS - 1) / AF_ROWS; });
-    const int blk = blockIdx.x;
-    if (blk >= uni(s_pre[p.E])) return;
-    const int e = uni(find_expert(s_pre, p.E, blk));
-    const int row0 = uni(s_off[e]) + (blk - uni(s_pre[e])) * AF_ROWS;
-    const int rows = min(AF_ROWS, uni(s_off[e + 1]) - row0);
+    const ExpertItem<1> it = find_item<1>(p.offsets, p.E, p.M, blockIdx.x,
+                                          [](int m) { return Counts<1>{{(m + AF_ROWS - 1) / AF_ROWS}}; });
+    if (it.e < 0) return;
+    const int e = it.e;
+    const int row0 = it.lo + (static_cast<int>(blockIdx.x) - it.before[0]) * AF_ROWS;
+    const int rows = min(AF_ROWS, it.hi - row0);
     const int nrb = (rows + 15) / 16;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4;
-    const int K = p.K, N = p.N, r = p.r;
-    const uint16_t* ae = p.a + static_cast<int64_t>(e) * r * K;
-    const uint16_t* be = p.b + static_cast<int64_t>(e) * N * r;
+    const int N = p.N, r = p.r;
+    const uint16_t* ae = p.a + static_cast<int64_t>(e) * r * p.K;
 
-    // ---- U
+    // ---- U: fewer row blocks leave registers for more columns in flight
     {
-        const uint16_t* xr[4];
-        const uint16_t* ar[NT];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xr[i] = p.x + static_cast<int64_t>(row0 + min(16 * i + l16, rows - 1)) * K;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) ar[j] = ae + static_cast<int64_t>(min(16 * j + l16, r - 1)) * K;
         f32x4 acc[4][NT];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        uint4 xv[2][2][4], av[2][2][NT];
-        const int groups = (K + 63) / 64;
-        auto load = [&](int buf, int grp) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int k = grp * 64 + c * 32 + 8 * g;
-                const bool in = k < K;
-                const int kc = in ? k : 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < nrb) xv[buf][c][i] = ld16(xr[i] + kc);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) av[buf][c][j] = ld16(ar[j] + kc);
-                if (grp * 64 + 64 > K) {   // past the end both operands are zero
-                    const uint32_t keep = in ? ~0u : 0u;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        xv[buf][c][i] = make_uint4(xv[buf][c][i].x & keep, xv[buf][c][i].y & keep, xv[buf][c][i].z & keep,
-                                                   xv[buf][c][i].w & keep);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        av[buf][c][j] = make_uint4(av[buf][c][j].x & keep, av[buf][c][j].y & keep, av[buf][c][j].z & keep,
-                                                   av[buf][c][j].w & keep);
-                }
-            }
-        };
-        auto mma = [&](int buf) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < nrb) {
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            acc[i][j] = mfma16(as_bf16x8(av[buf][c][j]), as_bf16x8(xv[buf][c][i]), acc[i][j]);
-                    }
-        };
-        int grp = wave;
-        if (grp < groups) load(0, grp);
-        for (; grp < groups; grp += 8) {
-            if (grp + 4 < groups) load(1, grp + 4);
-            mma(0);
-            if (grp + 4 < groups) {
-                if (grp + 8 < groups) load(0, grp + 8);
-                mma(1);
-            }
-        }
-        // lane: row 16 i + l16, ranks 16 j + 4 g ..
+        if (nrb == 1) adapter_u<NT, 1, NT == 1 ? 4 : (NT == 2 ? 2 : 1)>(p, ae, row0, rows, wave, acc);
+        else if (nrb == 2) adapter_u<NT, 2, NT <= 2 ? 2 : 1>(p, ae, row0, rows, wave, acc);
+        else adapter_u<NT, 4, 1>(p, ae, row0, rows, wave, acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -131,7 +148,7 @@ __global__ __launch_bounds__(256) void adapter_forward_kernel(const AdapterParam
                 if (i < nrb) *reinterpret_cast<f32x4*>(&s_part[wave][16 * i + l16][16 * j + 4 * g]) = acc[i][j];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < AF_ROWS * UW; i += 256) {
+    for (int i = threadIdx.x; i < 16 * nrb * UW; i += 256) {
         const int row = i / UW, c = i % UW;
         float v = 0.0f;
         if (row < rows && c < r)
@@ -147,8 +164,19 @@ __global__ __launch_bounds__(256) void adapter_forward_kernel(const AdapterParam
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) uo[i][k] = *reinterpret_cast<const bf16x8*>(&s_u[16 * i + l16][32 * k + 8 * g]);
-    const bool r8 = (r & 7) == 0;
+        for (int k = 0; k < KS; ++k)
+            if (i < nrb) uo[i][k] = *reinterpret_cast<const bf16x8*>(&s_u[16 * i + l16][32 * k + 8 * g]);
+    // b's rows are 2 r bytes apart: a 16-byte load may start anywhere and may reach into the next
+    // row, whose values are cleared, but not past the tensor's end
+    const uint16_t* be = p.b + static_cast<int64_t>(e) * N * r;
+    const uint16_t* bend = p.b + static_cast<int64_t>(p.E) * N * r;
+    uint4 bmask[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        const int n = r - 32 * k - 8 * g;     // ranks of this lane's eight that exist
+        auto word = [&](int w) { return n >= 2 * w + 2 ? ~0u : (n == 2 * w + 1 ? 0xffffu : 0u); };
+        bmask[k] = make_uint4(word(0), word(1), word(2), word(3));
+    }
     const int tiles = (N + 63) / 64;
     const int per = (tiles + gridDim.y - 1) / gridDim.y;
     const int t1 = min(tiles, static_cast<int>(blockIdx.y + 1) * per);
@@ -170,8 +198,16 @@ __global__ __launch_bounds__(256) void adapter_forward_kernel(const AdapterParam
             for (int k = 0; k < KS; ++k) {
                 const int c0 = 32 * k + 8 * g;
                 const uint16_t* src = be + static_cast<int64_t>(c) * r + c0;
-                if (r8) bv[t][k] = c0 < r ? ld16(src) : make_uint4(0, 0, 0, 0);
-                else bv[t][k] = gather8(src, 1, r - c0);
+                bv[t][k] = make_uint4(0, 0, 0, 0);
+                if (c0 < r) {
+                    if (src + 8 <= bend) {
+                        __builtin_memcpy(&bv[t][k], src, 16);
+                        bv[t][k] = make_uint4(bv[t][k].x & bmask[k].x, bv[t][k].y & bmask[k].y, bv[t][k].z & bmask[k].z,
+                                              bv[t][k].w & bmask[k].w);
+                    } else {
+                        bv[t][k] = gather8(src, 1, r - c0);
+                    }
+                }
             }
         }
 #pragma unroll
@@ -240,37 +276,35 @@ struct AdapterUnit {
     int e, row0, rows, blk0, slot;
 };
 
-// The schedule in LDS: units, 32-row blocks and part slots before each expert.
-struct AdapterSchedule {
-    int off[GG_KMAX_EXPERTS + 1], unit[GG_KMAX_EXPERTS + 1], blk[GG_KMAX_EXPERTS + 1], slot[GG_KMAX_EXPERTS + 1];
-};
-
-__device__ __forceinline__ void build_units(const AdapterParams& p, int unit_rows, AdapterSchedule& s) {
-    prefix_experts(p.offsets, p.E, p.M, s.off, s.unit, [&](int m) { return (m + unit_rows - 1) / unit_rows; });
-    prefix_experts(p.offsets, p.E, p.M, s.off, s.blk, [&](int m) { return (m + AD_BLK - 1) / AD_BLK; });
-    prefix_experts(p.offsets, p.E, p.M, s.off, s.slot,
-                   [&](int m) { return m > unit_rows ? (m + unit_rows - 1) / unit_rows : 0; });
-}
-
-__device__ __forceinline__ AdapterUnit unit_at(const AdapterParams& p, int unit_rows, const AdapterSchedule& s, int i) {
+// Unit i of the list of units of unit_rows rows (e = -1 past its end).
+__device__ __forceinline__ AdapterUnit find_unit(const AdapterParams& p, int unit_rows, int i) {
+    const ExpertItem<3> it = find_item<3>(p.offsets, p.E, p.M, i, [&](int m) {
+        const int units = (m + unit_rows - 1) / unit_rows;
+        return Counts<3>{{units, (m + AD_BLK - 1) / AD_BLK, units > 1 ? units : 0}};
+    });
+    const int part = i - it.before[0];
     AdapterUnit u;
-    u.e = uni(find_expert(s.unit, p.E, i));
-    const int part = i - uni(s.unit[u.e]);
-    const int lo = uni(s.off[u.e]), hi = uni(s.off[u.e + 1]);
-    u.row0 = lo + part * unit_rows;
-    u.rows = min(unit_rows, hi - u.row0);
-    u.blk0 = uni(s.blk[u.e]) + part * (unit_rows / AD_BLK);
-    u.slot = hi - lo > unit_rows ? uni(s.slot[u.e]) + part : -1;
+    u.e = it.e;
+    u.row0 = it.lo + part * unit_rows;
+    u.rows = min(unit_rows, it.hi - u.row0);
+    u.blk0 = it.before[1] + part * (unit_rows / AD_BLK);
+    u.slot = it.hi - it.lo > unit_rows ? it.before[2] + part : -1;
     return u;
 }
 
-// Eight rows 8 g + t of the 32-row block at `row`, columns c .. c+7 (`in`: those exist); rows past `rows` are zero.
-__device__ __forceinline__ void load_rows8(const uint16_t* m, int64_t ld, int row0, int row, int rows, int c, bool in,
-                                           uint4 (&v)[8]) {
+// 16 bytes at a wave-uniform base and a 32-bit byte offset of this lane.
+__device__ __forceinline__ uint4 ld16_at(const uint16_t* base, uint32_t bytes) {
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + bytes);
+}
+
+// Eight rows 8 g + t of the 32-row block at `block` (its first row, of row
+// length ld), of which `left` rows exist (later ones repeat the last), columns
+// c .. c + 7.  No branches: a load behind a branch would make the compiler
+// wait for every load before the next use of any.
+__device__ __forceinline__ void load_rows8(const uint16_t* block, int ld, int left, int c, uint4 (&v)[8]) {
     const int g = (threadIdx.x & 63) >> 4;
-    const uint16_t* base = m + static_cast<int64_t>(row0) * ld + (in ? c : 0);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) v[t] = ld16(base + static_cast<int64_t>(min(row + 8 * g + t, rows - 1)) * ld);
+    for (int t = 0; t < 8; ++t) v[t] = ld16_at(block, static_cast<uint32_t>(min(8 * g + t, left - 1) * ld + c) * 2);
 }
 __device__ __forceinline__ void mask_rows8(int row, int rows, bool in, uint4 (&v)[8]) {
     const int g = (threadIdx.x & 63) >> 4;
@@ -281,82 +315,119 @@ __device__ __forceinline__ void mask_rows8(int row, int rows, bool in, uint4 (&v
     }
 }
 
+// A wave's registers for the token rows are refilled for the next block as
+// soon as they are consumed, so that 8 KiB a wave are on their way for most of
+// the time.
 template <int RP>
-__global__ __launch_bounds__(RP <= 32 ? 512 : 256) void adapter_dy_kernel(const AdapterParams p) {
-    constexpr int NW = RP <= 32 ? 8 : 4;
+__global__ __launch_bounds__(ad_waves(RP) * 64) void adapter_dy_kernel(const AdapterParams p) {
+    constexpr int NW = ad_waves(RP);
     constexpr int NT = RP / 16;
-    __shared__ AdapterSchedule s;
     // each wave's 32 x 128 tile of dy; 16-byte chunk c of row i at c ^ (i & 15)
     __shared__ __attribute__((aligned(16))) uint16_t s_dy[NW][AD_BLK * AD_WCOLS];
-    __shared__ __attribute__((aligned(16))) uint16_t s_ut[2][RP][AD_BLK + 8];    // U^T of a block
-    __shared__ float s_du[2][NW][AD_BLK][RP + 4];                                // the waves' parts of du
-    build_units(p, p.rows1, s);
-    if (static_cast<int>(blockIdx.x) >= uni(s.unit[p.E])) return;
-    const AdapterUnit un = unit_at(p, p.rows1, s, blockIdx.x);
+    __shared__ __attribute__((aligned(16))) uint16_t s_u[2][AD_BLK * RP];                      // U of a block
+    __shared__ __attribute__((aligned(16))) float s_du[2][NW][AD_BLK][RP + 4];                 // the waves' parts of du
+    const int chunk = blockIdx.x % p.chunks1;   // neighbouring workgroups share rows
+    const AdapterUnit un = find_unit(p, p.rows1, blockIdx.x / p.chunks1);
+    if (un.e < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int nw = blockDim.x / 64, nthreads = blockDim.x;
     const int l16 = lane & 15, g = lane >> 4;
     const int N = p.N, r = p.r;
-    const int c0 = (blockIdx.y * NW + wave) * AD_WCOLS;
-    const int cl = c0 + 8 * l16;                  // the lane's columns
-    const bool in = cl < N;
+    const int c0 = (chunk * nw + wave) * AD_WCOLS;
+    const bool in = c0 + 8 * l16 < N;
+    const int cl = in ? c0 + 8 * l16 : 0;         // the lane's columns
     const bool whole = c0 + AD_WCOLS <= N;
     const uint16_t* be = p.b + static_cast<int64_t>(un.e) * N * r;
     const uint16_t* ue = p.u + static_cast<int64_t>(un.row0) * r;
 
-    bf16x8 bw[4][NT];   // b as the operand of du: rank 16 j + l16, columns c0 + 32 k + 8 g ..
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int c = c0 + 32 * k + 8 * g, rr = 16 * j + l16;
-            bw[k][j] = as_bf16x8(gather8(be + static_cast<int64_t>(c) * r + rr, r, rr < r ? N - c : 0));
-        }
-    f32x4 acc[8][NT];
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[c][j] = f32x4{0, 0, 0, 0};
-
-    constexpr int UPT = AD_BLK * RP / (NW * 64);   // U elements a thread stages
-    uint16_t uv[UPT];
+    // U of a block is 32 r values in a row: 16 bytes a thread, from any 2-byte boundary.  A load that would
+    // reach past the tensor's end takes its values one by one.
+    constexpr int UPT = (AD_BLK * RP / 8 + ad_waves_min(RP) * 64 - 1) / (ad_waves_min(RP) * 64);
+    const uint16_t* uend = p.u + static_cast<int64_t>(p.M) * r;
+    uint4 uv[UPT];
     auto load_u = [&](int row) {
+        const uint16_t* from = ue + static_cast<int64_t>(row) * r;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-            const int el = tid + i * NW * 64, rr = el / RP, c = el % RP;
-            uv[i] = row + rr < un.rows && c < r ? ue[static_cast<int64_t>(row + rr) * r + c] : 0;
+            const int el = (tid + i * nthreads) * 8;
+            if (el >= AD_BLK * r) continue;
+            const int64_t have = uend - (from + el);
+            if (have >= 8) __builtin_memcpy(&uv[i], from + el, 16);
+            else uv[i] = gather8(have > 0 ? from + el : ue, 1, static_cast<int>(have));
         }
     };
     auto put_u = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-            const int el = tid + i * NW * 64;
-            s_ut[buf][el % RP][el / RP] = uv[i];
+            const int el = (tid + i * nthreads) * 8;
+            if (el < AD_BLK * r) *reinterpret_cast<uint4*>(&s_u[buf][el]) = uv[i];
         }
     };
-    uint4 cur[8], nxt[8];
-    load_rows8(p.dy, N, un.row0, 0, un.rows, cl, in, cur);
-    load_u(0);
-    put_u(0);
-    __syncthreads();
-    int buf = 0;
-    for (int row = 0; row < un.rows; row += AD_BLK, buf ^= 1) {
-        const bool more = row + AD_BLK < un.rows;
-        if (more) {
-            load_rows8(p.dy, N, un.row0, row + AD_BLK, un.rows, cl, in, nxt);
-            load_u(row + AD_BLK);
-        }
-        if (!whole || row + AD_BLK > un.rows) mask_rows8(row, un.rows, in, cur);
-        uint16_t* tile = s_dy[wave];
+    // U as the operand of db: rank 16 j + l16 (a rank past r gives columns that are not kept), rows 8 g ..
+    auto read_u = [&](int buf, int j, int left) {
+        uint32_t w[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int rr = 8 * g + t;
-            *reinterpret_cast<uint4*>(tile + rr * AD_WCOLS + ((l16 ^ (rr & 15)) << 3)) = cur[t];
+        for (int i = 0; i < 8; ++i) {
+            w[i] = s_u[buf][(8 * g + i) * r + 16 * j + l16];
+            if (left < AD_BLK && 8 * g + i >= left) w[i] = 0;     // rows past the end: not U's
         }
-        uint4 tr[8];
-        transpose8(cur, tr);
+        return as_bf16x8(make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16)));
+    };
+    uint4 t[8];
+    bf16x8 bw[4][NT];   // b as the operand of du: rank 16 j + l16, columns c0 + 32 k + 8 g ..
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const bf16x8 ut = *reinterpret_cast<const bf16x8*>(&s_ut[buf][16 * j + l16][8 * g]);
+            const int c = c0 + 32 * k + 8 * g, rr = 16 * j + l16;
+            bw[k][j] = as_bf16x8(gather8(be + static_cast<int64_t>(min(c, N - 1)) * r + min(rr, r - 1), r, rr < r ? N - c : 0));
+        }
+        if (NT * (k + 1) % 4 == 0) __builtin_amdgcn_sched_barrier(0);   // 32 loads at a time
+    }
+    load_u(0);
+    const uint16_t* dy0 = p.dy + static_cast<int64_t>(un.row0) * N;
+    load_rows8(dy0, N, un.rows, cl, t);
+    f32x4 acc[8][NT];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[c][j] = f32x4{0, 0, 0, 0};
+    put_u(0);
+    __syncthreads();
+
+    // the waves' parts of du of the block at `row`, added up and stored
+    auto store_du = [&](int row, int buf) {
+        float* part = p.du_part + ((static_cast<int64_t>(chunk) * p.blocks + un.blk0 + row / AD_BLK) * AD_BLK) * RP;
+        for (int i = tid; i < AD_BLK * RP / 4; i += nthreads) {
+            const int rr = i / (RP / 4), c = i % (RP / 4) * 4;
+            f32x4 sum = *reinterpret_cast<const f32x4*>(&s_du[buf][0][rr][c]);
+            for (int w = 1; w < nw; ++w) sum += *reinterpret_cast<const f32x4*>(&s_du[buf][w][rr][c]);
+            *reinterpret_cast<f32x4*>(part + rr * RP + c) = sum;
+        }
+    };
+    const int last = (un.rows - 1) / AD_BLK * AD_BLK;
+    int buf = 0;
+    for (int row = 0; row < un.rows; row += AD_BLK, buf ^= 1) {
+        if (!whole || row + AD_BLK > un.rows) mask_rows8(row, un.rows, in, t);
+        uint16_t* tile = s_dy[wave];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int rr = 8 * g + i;
+            *reinterpret_cast<uint4*>(tile + rr * AD_WCOLS + ((l16 ^ (rr & 15)) << 3)) = t[i];
+        }
+        uint4 tr[8];
+        transpose8(t, tr);
+        // Memory operations complete in order: the stores go out before the next loads, whose
+        // wait (above, in the next block) would otherwise be for the stores too.
+        if (row > 0) store_du(row - AD_BLK, buf ^ 1);
+        const int ahead = min(row + AD_BLK, last);
+        load_u(ahead);
+        __builtin_amdgcn_sched_barrier(0);   // t is free: nothing of the refill moves above
+        load_rows8(dy0 + static_cast<int64_t>(ahead) * N, N, un.rows - ahead, cl, t);
+        __builtin_amdgcn_sched_barrier(0);   // nor does it wait for what follows
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const bf16x8 ut = read_u(buf, j, un.rows - row);
 #pragma unroll
             for (int c = 0; c < 8; ++c) acc[c][j] = mfma16(as_bf16x8(tr[c]), ut, acc[c][j]);
         }
@@ -380,19 +451,12 @@ __global__ __launch_bounds__(RP <= 32 ? 512 : 256) void adapter_dy_kernel(const 
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 *reinterpret_cast<f32x4*>(&s_du[buf][wave][16 * h + l16][16 * j + 4 * g]) = du[h][j];
-        if (more) put_u(buf ^ 1);
-        __syncthreads();   // the waves' parts are in; the next block's go to the other buffers
-        float* part = p.du_part + ((static_cast<int64_t>(blockIdx.y) * p.blocks + un.blk0 + row / AD_BLK) * AD_BLK) * RP;
-        for (int i = tid; i < AD_BLK * RP / 4; i += NW * 64) {
-            const int rr = i / (RP / 4), c = i % (RP / 4) * 4;
-            f32x4 sum = *reinterpret_cast<const f32x4*>(&s_du[buf][0][rr][c]);
-#pragma unroll
-            for (int w = 1; w < NW; ++w) sum += *reinterpret_cast<const f32x4*>(&s_du[buf][w][rr][c]);
-            *reinterpret_cast<f32x4*>(part + rr * RP + c) = sum;
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) cur[t] = nxt[t];
+        put_u(buf ^ 1);
+        // The waves' parts are in; the next block's go to the other buffers.  Only LDS is
+        // handed over here, so the rows on their way are not waited for.
+        block_barrier();
     }
+    store_du(last, buf ^ 1);
     // lane: rank 16 j + l16, columns c0 + 8 (4 g + x) + c
     const bool direct = un.slot < 0;
     float* out = direct ? p.db + static_cast<int64_t>(un.e) * N * r : p.db_part + static_cast<int64_t>(un.slot) * N * r;
@@ -412,32 +476,52 @@ __global__ __launch_bounds__(RP <= 32 ? 512 : 256) void adapter_dy_kernel(const 
             }
 }
 
-// du of every block from its parts, in chunk order; rows past an expert's end are zero already.
+// du of every block from its parts, in chunk order; rows past an expert's end
+// are zero already.  A workgroup takes 1024 or more values at a time, read as
+// they lie (rank fastest) and written so and transposed.
 template <int RP>
-__global__ __launch_bounds__(256) void adapter_du_kernel(const AdapterParams p, int chunks) {
+__global__ __launch_bounds__(256) void adapter_du_kernel(const AdapterParams p) {
     constexpr int UW = RP < 32 ? 32 : RP;
+    constexpr int VALS = AD_BLK * RP;                     // values of a block
+    constexpr int NB = VALS < 1024 ? 1024 / VALS : 1;     // blocks at a time
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
     __shared__ int s_blk[GG_KMAX_EXPERTS + 1];
+    __shared__ __attribute__((aligned(16))) uint16_t s_t[3][NB * RP][AD_BLK + 8];
     prefix_experts(p.offsets, p.E, p.M, s_off, s_blk, [](int m) { return (m + AD_BLK - 1) / AD_BLK; });
-    const int64_t total = static_cast<int64_t>(uni(s_blk[p.E])) * AD_BLK * RP;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        // consecutive threads take consecutive rows of one rank, so that the transposed stores are contiguous
-        const int64_t blk = i / (AD_BLK * RP);
-        const int w = static_cast<int>(i % (AD_BLK * RP)), c = w / AD_BLK, row = w % AD_BLK;
-        const float* src = p.du_part + (blk * AD_BLK + row) * RP + c;
-        float v = 0.0f;
-        for (int k = 0; k < chunks; ++k) v += src[static_cast<int64_t>(k) * p.blocks * AD_BLK * RP];
-        v *= p.scale;
-        const uint16_t hi = f2bf(v);
-        const float rest = v - bf2f(hi);
-        const uint16_t mid = f2bf(rest), lo = f2bf(rest - bf2f(mid));
-        p.du[(blk * AD_BLK + row) * UW + c] = hi;
-        if (RP < UW) p.du[(blk * AD_BLK + row) * UW + RP + c] = 0;
-        uint16_t* t = p.du_t + (blk * 3 * RP + c) * AD_BLK + row;
-        t[0] = hi;
-        t[RP * AD_BLK] = mid;
-        t[2 * RP * AD_BLK] = lo;
+    const int total = uni(s_blk[p.E]);
+    for (int blk = blockIdx.x * NB; blk < total; blk += gridDim.x * NB) {
+#pragma unroll
+        for (int i = 0; i < NB * VALS / 1024; ++i) {
+            const int v4 = (i * 256 + threadIdx.x) * 4, nb = v4 / VALS, row = v4 % VALS / RP, c = v4 % RP;
+            if (blk + nb >= total) continue;
+            const float* src = p.du_part + static_cast<int64_t>(blk) * VALS + v4;
+            f32x4 v = {0, 0, 0, 0};
+            for (int k = 0; k < p.chunks1; ++k)
+                v += *reinterpret_cast<const f32x4*>(src + static_cast<int64_t>(k) * p.blocks * VALS);
+            uint32_t hi[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float d = v[x] * p.scale;
+                hi[x] = f2bf(d);
+                const float rest = d - bf2f(hi[x]);
+                const uint16_t mid = f2bf(rest);
+                s_t[0][nb * RP + c + x][row] = static_cast<uint16_t>(hi[x]);
+                s_t[1][nb * RP + c + x][row] = mid;
+                s_t[2][nb * RP + c + x][row] = f2bf(rest - bf2f(mid));
+            }
+            uint16_t* d = p.du + ((static_cast<int64_t>(blk) + nb) * AD_BLK + row) * UW + c;
+            *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            if (RP < UW) *reinterpret_cast<uint2*>(d + RP) = make_uint2(0, 0);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < NB * 3 * RP * AD_BLK / 8; i += 256) {
+            const int nb = i / (3 * RP * AD_BLK / 8), w = i % (3 * RP * AD_BLK / 8);
+            const int q = w / (RP * AD_BLK / 8), c = w / (AD_BLK / 8) % RP, row = w % (AD_BLK / 8) * 8;
+            if (blk + nb < total)
+                *reinterpret_cast<uint4*>(p.du_t + (((static_cast<int64_t>(blk) + nb) * 3 + q) * RP + c) * AD_BLK + row) =
+                    *reinterpret_cast<const uint4*>(&s_t[q][nb * RP + c][row]);
+        }
+        __syncthreads();
     }
 }
 
@@ -446,101 +530,136 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
     constexpr int NT = RP / 16;
     constexpr int UW = RP < 32 ? 32 : RP;
     constexpr int KS = UW / 32;
-    __shared__ AdapterSchedule s;
-    build_units(p, p.rows2, s);
-    if (static_cast<int>(blockIdx.x) >= uni(s.unit[p.E])) return;
-    const AdapterUnit un = unit_at(p, p.rows2, s, blockIdx.x);
+    // a as the operand of dx, for each wave: tile t of 64-column half h, ranks 32 k + 8 g ..
+    __shared__ __attribute__((aligned(16))) uint4 s_aw[4][2][4][KS][64];
+    const int chunk = blockIdx.x % p.chunks2;
+    const AdapterUnit un = find_unit(p, p.rows2, blockIdx.x / p.chunks2);
+    if (un.e < 0) return;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4;
     const int K = p.K, r = p.r;
-    const int c0 = (blockIdx.y * 4 + wave) * AD_WCOLS;
-    if (c0 >= K) return;
-    const int cl = c0 + 8 * l16;
-    const bool in = cl < K, whole = c0 + AD_WCOLS <= K;
+    const int c0 = (chunk * 4 + wave) * AD_WCOLS;
+    if (c0 >= K) return;                        // no barrier below: each wave keeps to its own part of LDS
+    const bool in = c0 + 8 * l16 < K, whole = c0 + AD_WCOLS <= K;
+    const int cl = in ? c0 + 8 * l16 : 0;
     const uint16_t* ae = p.a + static_cast<int64_t>(un.e) * r * K;
 
-    // a as the operand of dx: tile t of 64-column half h, ranks 32 k + 8 g ..
-    bf16x8 aw[2][4][KS];
+    uint4 x[8], base[2][2][2];
+    bf16x8 dt[3][NT], dr[2][KS];
+    const uint16_t* x0 = p.x + static_cast<int64_t>(un.row0) * K;
+    // without a base its place is taken by x, cleared: the loads stay the same
+    const uint16_t* base0 = (p.base ? p.base : p.x) + static_cast<int64_t>(un.row0) * K;
+    const uint32_t keep = p.base ? ~0u : 0u;
+    auto load_base = [&](int row) {
+        const uint16_t* from = base0 + static_cast<int64_t>(row) * K;
 #pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // columns past K: x's first ones instead, whose results are not stored
+                const int c = c0 + 64 * h + 16 * g, rr = min(16 * i + l16, un.rows - row - 1) * K;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    base[i][h][q] = ld16_at(from, static_cast<uint32_t>(rr + (c + 8 * q < K ? c + 8 * q : 0)) * 2);
+            }
+    };
+    auto load_dt = [&](int row) {
+        const uint16_t* from = p.du_t + (static_cast<int64_t>(un.blk0) + row / AD_BLK) * 3 * RP * AD_BLK;
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                dt[q][j] = as_bf16x8(ld16_at(from, ((q * RP + 16 * j + l16) * AD_BLK + 8 * g) * 2));
+    };
+    auto load_dr = [&](int row) {
+        const uint16_t* from = p.du + (static_cast<int64_t>(un.blk0) + row / AD_BLK) * AD_BLK * UW;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) dr[i][k] = as_bf16x8(ld16_at(from, ((16 * i + l16) * UW + 32 * k + 8 * g) * 2));
+    };
+#pragma unroll 1
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const int c = c0 + 64 * h + 16 * (l16 >> 2) + 4 * t + (l16 & 3), rr = 32 * k + 8 * g;
-                aw[h][t][k] = as_bf16x8(gather8(ae + static_cast<int64_t>(rr) * K + c, K, c < K ? r - rr : 0));
+                s_aw[wave][h][t][k][lane] = gather8(ae + static_cast<int64_t>(min(rr, r - 1)) * K + min(c, K - 1), K, c < K ? r - rr : 0);
             }
+    load_rows8(x0, K, un.rows, cl, x);
+    load_dt(0);
+    load_base(0);
+    load_dr(0);
     f32x4 acc[8][NT];
 #pragma unroll
     for (int c = 0; c < 8; ++c)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[c][j] = f32x4{0, 0, 0, 0};
-    uint4 cur[8], nxt[8];
-    load_rows8(p.x, K, un.row0, 0, un.rows, cl, in, cur);
+
+    const int last = (un.rows - 1) / AD_BLK * AD_BLK;
     for (int row = 0; row < un.rows; row += AD_BLK) {
-        const int64_t blk = un.blk0 + row / AD_BLK;
-        uint4 base[2][2][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int rr = row + 16 * i + l16, c = c0 + 64 * h + 16 * g + 8 * q;
-                    base[i][h][q] = make_uint4(0, 0, 0, 0);
-                    if (p.base && rr < un.rows && c < K)
-                        base[i][h][q] = ld16(p.base + static_cast<int64_t>(un.row0 + rr) * K + c);
-                }
-        bf16x8 dt[3][NT], dr[2][KS];
-#pragma unroll
-        for (int q = 0; q < 3; ++q)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                dt[q][j] = as_bf16x8(ld16(p.du_t + ((blk * 3 + q) * RP + 16 * j + l16) * AD_BLK + 8 * g));
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-                dr[i][k] = as_bf16x8(ld16(p.du + (blk * AD_BLK + 16 * i + l16) * UW + 32 * k + 8 * g));
-        if (row + AD_BLK < un.rows) load_rows8(p.x, K, un.row0, row + AD_BLK, un.rows, cl, in, nxt);
-        if (!whole || row + AD_BLK > un.rows) mask_rows8(row, un.rows, in, cur);
+        const int ahead = min(row + AD_BLK, last);
+        if (!whole || row + AD_BLK > un.rows) mask_rows8(row, un.rows, in, x);
         uint4 tr[8];
-        transpose8(cur, tr);
+        transpose8(x, tr);
+        __builtin_amdgcn_sched_barrier(0);   // x is free: nothing of the refill moves above
+        load_rows8(x0 + static_cast<int64_t>(ahead) * K, K, un.rows - ahead, cl, x);
+        __builtin_amdgcn_sched_barrier(0);   // nor does it wait for what follows
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int q = 2; q >= 0; --q) acc[c][j] = mfma16(as_bf16x8(tr[c]), dt[q][j], acc[c][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        load_dt(ahead);
+        int at = lane;
+        asm volatile("" : "+v"(at));         // a's operands are read anew in every block, not held
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 aw[4][KS];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) aw[t][k] = as_bf16x8(s_aw[wave][h][t][k][at]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 f32x4 d[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     d[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) d[t] = mfma16(aw[h][t][k], dr[i][k], d[t]);
+                    for (int k = 0; k < KS; ++k) d[t] = mfma16(aw[t][k], dr[i][k], d[t]);
                 }
-                const int rr = row + 16 * i + l16;
-                if (rr >= un.rows) continue;
-                uint16_t* orow = p.out + static_cast<int64_t>(un.row0 + rr) * K + c0 + 64 * h + 16 * g;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    if (c0 + 64 * h + 16 * g + 8 * q >= K) continue;
-                    const uint32_t bw[4] = {base[i][h][q].x, base[i][h][q].y, base[i][h][q].z, base[i][h][q].w};
+                    const uint4 bs = and4(base[i][h][q], keep);
+                    const uint32_t bw[4] = {bs.x, bs.y, bs.z, bs.w};
                     uint32_t o[4];
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         const f32x4& dd = d[2 * q + (m >> 1)];
                         o[m] = pack2(lo_f(bw[m]) + dd[2 * (m & 1)], hi_f(bw[m]) + dd[2 * (m & 1) + 1]);
                     }
-                    *reinterpret_cast<uint4*>(orow + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+                    base[i][h][q] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
+        }
+        // base now holds dx
+        uint16_t* to = p.out + static_cast<int64_t>(un.row0 + row) * K + c0;
+        const uint32_t at0 = static_cast<uint32_t>(l16 * K + 16 * g);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) cur[t] = nxt[t];
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (row + 16 * i + l16 < un.rows && c0 + 64 * h + 16 * g + 8 * q < K)
+                        *reinterpret_cast<uint4*>(to + 16 * i * K + (at0 + 64 * h + 8 * q)) = base[i][h][q];
+        __builtin_amdgcn_sched_barrier(0);
+        load_dr(ahead);
+        load_base(ahead);
     }
     // lane: rank 16 j + l16, columns c0 + 8 (4 g + x) + 0 .. 7
     const bool direct = un.slot < 0;
@@ -600,8 +719,8 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(const AdapterParams p
 template <int RP>
 static hipError_t forward_of(const AdapterParams& p, int num_cu, hipStream_t s) {
     const int64_t blocks = static_cast<int64_t>(p.M) / AF_ROWS + (p.M < p.E ? p.M : p.E);
-    // two workgroups for each CU where the rows alone give fewer, down to 256 columns each
-    int64_t split = 2 * static_cast<int64_t>(num_cu) / blocks;
+    // four workgroups for each CU where the rows alone give fewer, down to 256 columns each
+    int64_t split = 4 * static_cast<int64_t>(num_cu) / blocks;
     const int64_t most = (p.N + 255) / 256;
     split = split < 1 ? 1 : (split > most ? most : split);
     hipLaunchKernelGGL((adapter_forward_kernel<RP>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(split)),
@@ -618,23 +737,24 @@ hipError_t launch_adapter_forward(const AdapterParams& p, int num_cu, hipStream_
 }
 
 template <int RP>
-static hipError_t backward_of(const AdapterParams& p, int num_cu, hipStream_t s) {
+static hipError_t backward_of(AdapterParams p, int num_cu, hipStream_t s) {
     const int64_t few = p.M < p.E ? p.M : p.E;
-    const int cols = ad_waves(RP) * AD_WCOLS;
-    const int chunks = (p.N + cols - 1) / cols;
+    p.chunks1 = ad_chunks(p.N, RP);
+    p.chunks2 = (p.K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS);
+    // the columns of dy spread evenly over its chunks
+    const int parts = (p.N + AD_WCOLS - 1) / AD_WCOLS, even = (parts + p.chunks1 - 1) / p.chunks1;
+    const int waves = even > ad_waves_min(RP) ? even : ad_waves_min(RP);
     hipError_t st;
     if (p.M > 0) {
-        hipLaunchKernelGGL((adapter_dy_kernel<RP>),
-                           dim3(static_cast<unsigned>(p.M / p.rows1 + few), static_cast<unsigned>(chunks)),
-                           dim3(ad_waves(RP) * 64), 0, s, p);
+        hipLaunchKernelGGL((adapter_dy_kernel<RP>), dim3(static_cast<unsigned>((p.M / p.rows1 + few) * p.chunks1)),
+                           dim3(static_cast<unsigned>(waves) * 64), 0, s, p);
         if ((st = hipGetLastError()) != hipSuccess) return st;
-        const int64_t want = p.blocks * AD_BLK * RP / 256, most = static_cast<int64_t>(num_cu) * 8;
-        hipLaunchKernelGGL((adapter_du_kernel<RP>), dim3(static_cast<unsigned>(want < most ? want : most)), dim3(256), 0, s, p,
-                           chunks);
-        if ((st = hipGetLastError()) != hipSuccess) return st;
-        hipLaunchKernelGGL((adapter_dx_kernel<RP>),
-                           dim3(static_cast<unsigned>(p.M / p.rows2 + few), static_cast<unsigned>((p.K + 511) / 512)), dim3(256),
+        const int64_t most = static_cast<int64_t>(num_cu) * 6;
+        hipLaunchKernelGGL((adapter_du_kernel<RP>), dim3(static_cast<unsigned>(p.blocks < most ? p.blocks : most)), dim3(256),
                            0, s, p);
+        if ((st = hipGetLastError()) != hipSuccess) return st;
+        hipLaunchKernelGGL((adapter_dx_kernel<RP>), dim3(static_cast<unsigned>((p.M / p.rows2 + few) * p.chunks2)),
+                           dim3(256), 0, s, p);
         if ((st = hipGetLastError()) != hipSuccess) return st;
     }
     const int64_t width = p.N > p.K ? p.N : p.K, gx = (width * p.r / 4 + 1023) / 1024;

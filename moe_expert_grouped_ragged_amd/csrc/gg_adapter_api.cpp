@@ -41,7 +41,7 @@ struct Workspace {
 Workspace workspace_of(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     Workspace w{};
     const int64_t rp = ad_rank_p(static_cast<int>(r));
-    const int64_t cols = ad_waves(static_cast<int>(rp)) * AD_WCOLS, chunks = (N + cols - 1) / cols;
+    const int64_t chunks = ad_chunks(static_cast<int>(N), static_cast<int>(rp));
     w.rows1 = unit_rows(M, chunks);
     w.rows2 = unit_rows(M, (K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS));
     w.blocks = M / AD_BLK + (M < E ? M : E);

@@ -130,53 +130,135 @@ __device__ __forceinline__ void static_for(F&& f) {
     }
 }
 
-// Exclusive prefix sums of count(rows of e) over the experts, and the offsets
-// (every thread of the workgroup calls it).  The offsets are clamped into
-// [0, M] and made non-decreasing by a running maximum, so bad offsets cannot
-// count more rows than M.
+// Inclusive scan over the 64 lanes (v >= 0; op: sum or maximum) by the DPP
+// row shifts and row broadcasts, without LDS.
+template <typename Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr:1
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));   // row_shr:2
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));   // row_shr:4
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));   // row_shr:8
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast:15 into rows 1 and 3
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));   // row_bcast:31 into rows 2 and 3
+    return v;
+}
+// The value of the lane before (0 in lane 0), given an inclusive scan's values.
+__device__ __forceinline__ int lane_before(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x138, 0xf, 0xf, false);       // wave_shr:1
+}
+
+// Offsets of a chunk of 256 experts, four a lane (o[j]: first row of expert
+// base + 4 lane + j, o[4]: its successor's), clamped into [0, M] and made
+// non-decreasing by a running maximum (`top` carries it between chunks), so
+// that bad offsets cannot count more rows than M.  Experts past E have no rows.
+constexpr int EXPERT_CHUNK = 256;
+__device__ __forceinline__ void load_offsets(const int64_t* __restrict__ offsets, int E, int M, int base, int& top,
+                                             int (&o)[5]) {
+    const int e0 = base + 4 * (threadIdx.x & 63);
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+        const int64_t v = offsets[min(e0 + j, E)];
+        o[j] = static_cast<int>(v < 0 ? 0 : (v > M ? M : v));
+    }
+#pragma unroll
+    for (int j = 1; j < 5; ++j) o[j] = max(o[j], o[j - 1]);
+    const int incl = wave_scan(o[4], [](int a, int b) { return max(a, b); });
+    const int before = max(lane_before(incl), top);
+#pragma unroll
+    for (int j = 0; j < 5; ++j) o[j] = max(o[j], before);
+    top = max(top, __builtin_amdgcn_readlane(incl, 63));
+}
+
+// Exclusive prefix sums of count(rows of e) over the experts, and the offsets,
+// into LDS (every thread of the workgroup calls it).
 template <typename F>
 __device__ __forceinline__ void prefix_experts(const int64_t* __restrict__ offsets, int E, int M, int* s_off,
                                                int* s_pre, F&& count) {
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-        int64_t o = offsets[e];
-        o = o < 0 ? 0 : (o > M ? M : o);
-        s_off[e] = static_cast<int>(o);
-    }
-    __syncthreads();
     if (threadIdx.x < 64) {
-        const int lane = threadIdx.x, per = E / 64 + 1;
-        const int e0 = min(E + 1, lane * per), e2 = min(E + 1, e0 + per), e1 = min(E, e2);
-        int top = 0;
-        for (int e = e0; e < e2; ++e) {
-            top = max(top, s_off[e]);
-            s_off[e] = top;
-        }
-        int before = __shfl_up(top, 1, 64);
-        if (lane == 0) before = 0;
+        int top = 0, sum = 0;
+        for (int base = 0; base <= E; base += EXPERT_CHUNK) {
+            int o[5], c[4];
+            load_offsets(offsets, E, M, base, top, o);
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(before, d, 64);
-            if (lane >= d) before = max(before, v);
-        }
-        for (int e = e0; e < e2; ++e) s_off[e] = max(s_off[e], before);
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the next lane's first offset
-        int sum = 0;
-        for (int e = e0; e < e1; ++e) sum += count(s_off[e + 1] - s_off[e]);
-        int incl = sum;
+            for (int j = 0; j < 4; ++j) c[j] = count(o[j + 1] - o[j]);
+            const int incl = wave_scan(c[0] + c[1] + c[2] + c[3], [](int a, int b) { return a + b; });
+            int run = sum + lane_before(incl);
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(incl, d, 64);
-            if (lane >= d) incl += v;
+            for (int j = 0; j < 4; ++j) {
+                const int e = base + 4 * threadIdx.x + j;
+                if (e <= E) {
+                    s_off[e] = o[j];
+                    s_pre[e] = run;
+                }
+                run += c[j];
+            }
+            sum += __builtin_amdgcn_readlane(incl, 63);
         }
-        int run = incl - sum;
-        for (int e = e0; e < e1; ++e) {
-            s_pre[e] = run;
-            run += count(s_off[e + 1] - s_off[e]);
-        }
-        if (lane == 63) s_pre[E] = incl;
     }
     __syncthreads();
+}
+
+// The expert that owns item `target` of a list with count(rows)[0] items for
+// each expert, its rows [lo, hi), and the sums of the NC counts over the
+// experts before it; e = -1 past the end of the list.  Every wave finds it by
+// itself, in registers, in the order of the offsets.
+template <int NC>
+struct ExpertItem {
+    int e, lo, hi, before[NC];
+};
+template <int NC>
+struct Counts {
+    int c[NC];
+};
+template <int NC, typename F>
+__device__ __forceinline__ ExpertItem<NC> find_item(const int64_t* __restrict__ offsets, int E, int M, int target,
+                                                    F&& count) {
+    ExpertItem<NC> item;
+    item.e = -1;
+    int top = 0, sum[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) sum[k] = 0;
+    for (int base = 0; base < E; base += EXPERT_CHUNK) {
+        int o[5], run[NC];
+        Counts<NC> c[4];
+        load_offsets(offsets, E, M, base, top, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = count(o[j + 1] - o[j]);
+        int total[NC];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const int incl = wave_scan(c[0].c[k] + c[1].c[k] + c[2].c[k] + c[3].c[k], [](int a, int b) { return a + b; });
+            run[k] = sum[k] + lane_before(incl);
+            total[k] = __builtin_amdgcn_readlane(incl, 63);
+        }
+        if (target < sum[0] + total[0]) {
+            // the lane's expert that holds the target, if any (counts are zero or more, so it is unique)
+            int at = -1;
+            ExpertItem<NC> mine = {};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (run[0] <= target && target < run[0] + c[j].c[0]) {
+                    at = j;
+                    mine.lo = o[j];
+                    mine.hi = o[j + 1];
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) mine.before[k] = run[k];
+                }
+#pragma unroll
+                for (int k = 0; k < NC; ++k) run[k] += c[j].c[k];
+            }
+            const int lane = __builtin_ctzll(__ballot(at >= 0));
+            item.e = base + 4 * lane + __builtin_amdgcn_readlane(at, lane);
+            item.lo = __builtin_amdgcn_readlane(mine.lo, lane);
+            item.hi = __builtin_amdgcn_readlane(mine.hi, lane);
+#pragma unroll
+            for (int k = 0; k < NC; ++k) item.before[k] = __builtin_amdgcn_readlane(mine.before[k], lane);
+            return item;
+        }
+#pragma unroll
+        for (int k = 0; k < NC; ++k) sum[k] += total[k];
+    }
+    return item;
 }
 
 }  // namespace gg
