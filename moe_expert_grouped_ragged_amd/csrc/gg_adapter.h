@@ -12,11 +12,13 @@ constexpr int AD_WCOLS = 128;    // columns a wavefront of the backward pass own
 
 // Rank padded to the matrix instruction's tiles: 16, 32 or 64.
 inline int ad_rank_p(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
-// Wavefronts of a workgroup of the output-side backward kernel: at most (its
-// registers hold the columns' part of db), and at least; chunks of N columns.
-constexpr int ad_waves(int rp) { return rp <= 32 ? 8 : 4; }
-constexpr int ad_waves_min(int rp) { return ad_waves(rp) * 3 / 4; }
-inline int ad_chunks(int n, int rp) { return (n + ad_waves(rp) * AD_WCOLS - 1) / (ad_waves(rp) * AD_WCOLS); }
+// Column groups (AD_WCOLS each) of a workgroup of the output-side backward
+// kernel: at most (its registers hold the columns' part of db), and at least;
+// wavefronts that share a group, 32 ranks each; chunks of N columns.
+constexpr int ad_groups(int rp) { return rp <= 32 ? 8 : 4; }
+constexpr int ad_groups_min(int rp) { return ad_groups(rp) * 3 / 4; }
+constexpr int ad_split(int rp) { return rp <= 32 ? 1 : 2; }
+inline int ad_chunks(int n, int rp) { return (n + ad_groups(rp) * AD_WCOLS - 1) / (ad_groups(rp) * AD_WCOLS); }
 
 struct AdapterParams {
     const uint16_t* x;        // [M][K]

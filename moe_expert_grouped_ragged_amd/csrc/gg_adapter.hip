@@ -35,25 +35,26 @@ __device__ __forceinline__ uint4 gather8(const uint16_t* p, int64_t ld, int n) {
 
 // ---------------------------------------------------------------- forward
 //
-// A workgroup owns up to 64 rows of one expert, as up to four 16-row blocks.
-// U = x a^T: the four waves take 64-column groups of the rows in turn, each
-// with all rows, and the four partial sums meet in LDS in a fixed order; U is
-// rounded to bf16 there (it is saved and is the second product's operand).
-// Then each wave walks 64-column tiles of y: the tile's columns are dealt to
-// the instruction's rows so that a lane ends up with 16 neighbouring columns
-// of one token row, and base and y move as whole 128-byte lines without
-// passing through LDS.  With few row blocks the columns of y are split over
-// workgroups, which each compute U again.
-constexpr int AF_ROWS = 64;
+// A workgroup owns up to 16 RB rows of one expert, as 16-row blocks (RB = 4,
+// or 2 with twice the waves where the experts have few rows).  U = x a^T: the
+// waves take 64-column groups of the rows in turn, each with all rows, and
+// their partial sums meet in LDS in a fixed order; U is rounded to bf16 there
+// (it is saved and is the second product's operand).
+// Then each wave walks 128-column tiles of y: the columns are dealt to the
+// eight instructions of a tile so that a lane ends up with 8 neighbouring
+// columns of four token rows, and base and y move as 256-byte row segments of
+// 16 lanes without passing through LDS.  With few row blocks the columns of y
+// are split over workgroups, which each compute U again.
+constexpr int af_waves(int rb) { return rb == 2 ? 8 : 4; }
 
 __device__ __forceinline__ uint4 and4(uint4 v, uint32_t m) { return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m); }
 
 // This wave's part of U for the NRB 16-row blocks from row0: groups wave,
-// wave + 4, ... of 64 columns, D of them loaded ahead while D are multiplied.
+// wave + W, ... of 64 columns, D of them loaded ahead while D are multiplied.
 // Lane: row 16 i + (lane & 15), ranks 16 j + 4 (lane >> 4) .. of acc[i][j].
-template <int NT, int NRB, int D>
+template <int NT, int NRB, int D, int W, int MAXB>
 __device__ __forceinline__ void adapter_u(const AdapterParams& p, const uint16_t* ae, int row0, int rows, int wave,
-                                          f32x4 (&acc)[4][NT]) {
+                                          f32x4 (&acc)[MAXB][NT]) {
     const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
     const int K = p.K, groups = (K + 63) / 64;
     const uint16_t* xr[NRB];
@@ -63,13 +64,13 @@ __device__ __forceinline__ void adapter_u(const AdapterParams& p, const uint16_t
 #pragma unroll
     for (int j = 0; j < NT; ++j) ar[j] = ae + static_cast<int64_t>(min(16 * j + l16, p.r - 1)) * K;
     uint4 xv[2][D][2][NRB], av[2][D][2][NT];
-    // groups first, first + 4, ...; past the end of the columns both operands are zero
+    // groups first, first + W, ...; past the end of the columns both operands are zero
     auto load = [&](int buf, int first) {
 #pragma unroll
         for (int d = 0; d < D; ++d)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int k = (first + 4 * d) * 64 + c * 32 + 8 * g;
+                const int k = (first + W * d) * 64 + c * 32 + 8 * g;
                 const int kc = k < K ? k : 0;
 #pragma unroll
                 for (int i = 0; i < NRB; ++i) xv[buf][d][c][i] = ld16(xr[i] + kc);
@@ -78,12 +79,12 @@ __device__ __forceinline__ void adapter_u(const AdapterParams& p, const uint16_t
             }
     };
     auto mma = [&](int buf, int first) {
-        if ((first + 4 * D - 3) * 64 > K) {
+        if ((first + W * (D - 1) + 1) * 64 > K) {
 #pragma unroll
             for (int d = 0; d < D; ++d)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint32_t keep = (first + 4 * d) * 64 + c * 32 + 8 * g < K ? ~0u : 0u;
+                    const uint32_t keep = (first + W * d) * 64 + c * 32 + 8 * g < K ? ~0u : 0u;
 #pragma unroll
                     for (int i = 0; i < NRB; ++i) xv[buf][d][c][i] = and4(xv[buf][d][c][i], keep);
 #pragma unroll
@@ -102,22 +103,23 @@ __device__ __forceinline__ void adapter_u(const AdapterParams& p, const uint16_t
     };
     int at = wave;
     if (at < groups) load(0, at);
-    for (; at < groups; at += 8 * D) {
-        if (at + 4 * D < groups) load(1, at + 4 * D);
+    for (; at < groups; at += 2 * W * D) {
+        if (at + W * D < groups) load(1, at + W * D);
         mma(0, at);
-        if (at + 4 * D < groups) {
-            if (at + 8 * D < groups) load(0, at + 8 * D);
-            mma(1, at + 4 * D);
+        if (at + W * D < groups) {
+            if (at + 2 * W * D < groups) load(0, at + 2 * W * D);
+            mma(1, at + W * D);
         }
     }
 }
 
-template <int RP>
-__global__ __launch_bounds__(256, 2) void adapter_forward_kernel(const AdapterParams p) {
+template <int RP, int RB>
+__global__ __launch_bounds__(af_waves(RB) * 64, 2) void adapter_forward_kernel(const AdapterParams p) {
+    constexpr int W = af_waves(RB), AF_ROWS = 16 * RB;
     constexpr int NT = RP / 16;                  // rank tiles
     constexpr int UW = RP < 32 ? 32 : RP;        // U's width as an operand (zero-padded)
     constexpr int KS = UW / 32;
-    __shared__ __attribute__((aligned(16))) float s_part[4][AF_ROWS][RP + 4];
+    __shared__ __attribute__((aligned(16))) float s_part[W][AF_ROWS][RP + 4];
     __shared__ __attribute__((aligned(16))) uint16_t s_u[AF_ROWS][UW + 8];
     const ExpertItem<1> it = find_item<1>(p.offsets, p.E, p.M, blockIdx.x,
                                           [](int m) { return Counts<1>{{(m + AF_ROWS - 1) / AF_ROWS}}; });
@@ -133,26 +135,28 @@ __global__ __launch_bounds__(256, 2) void adapter_forward_kernel(const AdapterPa
 
     // ---- U: fewer row blocks leave registers for more columns in flight
     {
-        f32x4 acc[4][NT];
+        f32x4 acc[RB][NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        if (nrb == 1) adapter_u<NT, 1, NT == 1 ? 4 : (NT == 2 ? 2 : 1)>(p, ae, row0, rows, wave, acc);
-        else if (nrb == 2) adapter_u<NT, 2, NT <= 2 ? 2 : 1>(p, ae, row0, rows, wave, acc);
-        else adapter_u<NT, 4, 1>(p, ae, row0, rows, wave, acc);
+        if (nrb == 1) adapter_u<NT, 1, NT == 1 ? 2 : 1, W>(p, ae, row0, rows, wave, acc);
+        else if (RB == 2 || nrb == 2) adapter_u<NT, 2, 1, W>(p, ae, row0, rows, wave, acc);
+        else adapter_u<NT, RB, 1, W>(p, ae, row0, rows, wave, acc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 if (i < nrb) *reinterpret_cast<f32x4*>(&s_part[wave][16 * i + l16][16 * j + 4 * g]) = acc[i][j];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * nrb * UW; i += 256) {
+    for (int i = threadIdx.x; i < 16 * nrb * UW; i += W * 64) {
         const int row = i / UW, c = i % UW;
         float v = 0.0f;
-        if (row < rows && c < r)
-            v = (s_part[0][row][c] + s_part[1][row][c]) + (s_part[2][row][c] + s_part[3][row][c]);
+        if (row < rows && c < r) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) v += s_part[w][row][c];
+        }
         const uint16_t h = f2bf(v);
         s_u[row][c] = h;
         if (row < rows && c < r && blockIdx.y == 0) p.u[static_cast<int64_t>(row0 + row) * r + c] = h;
@@ -160,9 +164,10 @@ __global__ __launch_bounds__(256, 2) void adapter_forward_kernel(const AdapterPa
     __syncthreads();
 
     // ---- y
-    bf16x8 uo[4][KS];
+    constexpr int HB = RP == 64 && RB == 4 ? 1 : RB;   // row blocks whose base is held at a time (registers)
+    bf16x8 uo[RB][KS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
             if (i < nrb) uo[i][k] = *reinterpret_cast<const bf16x8*>(&s_u[16 * i + l16][32 * k + 8 * g]);
@@ -177,23 +182,28 @@ __global__ __launch_bounds__(256, 2) void adapter_forward_kernel(const AdapterPa
         auto word = [&](int w) { return n >= 2 * w + 2 ? ~0u : (n == 2 * w + 1 ? 0xffffu : 0u); };
         bmask[k] = make_uint4(word(0), word(1), word(2), word(3));
     }
-    const int tiles = (N + 63) / 64;
-    const int per = (tiles + gridDim.y - 1) / gridDim.y;
+    const int tiles = (N + 127) / 128;
+    const int per = (tiles + gridDim.y - 1) / gridDim.y;   // a multiple of W but for few tiles
     const int t1 = min(tiles, static_cast<int>(blockIdx.y + 1) * per);
-    for (int ct = blockIdx.y * per + wave; ct < t1; ct += 4) {
-        const int n0 = ct * 64 + 16 * g;            // the lane's 16 columns
-        uint4 bv[4][KS], base[4][2];
+    for (int ct = blockIdx.y * per + wave; ct < t1; ct += W) {
+        const int n0 = ct * 128 + 8 * l16;          // the lane's 8 columns of rows 16 i + 4 g + x
+        const bool in = n0 < N;
+        uint4 bv[8][KS], base[HB][4];
+        auto load_base = [&](int first) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < HB; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                base[i][h] = make_uint4(0, 0, 0, 0);
-                if (p.base && 16 * i + l16 < rows && n0 + 8 * h < N)
-                    base[i][h] = ld16(p.base + static_cast<int64_t>(row0 + 16 * i + l16) * N + n0 + 8 * h);
-            }
+                for (int x = 0; x < 4; ++x) {
+                    base[i][x] = make_uint4(0, 0, 0, 0);
+                    if (p.base && first + i < nrb)
+                        base[i][x] = ld16_nt(
+                            p.base + static_cast<int64_t>(row0 + min(16 * (first + i) + 4 * g + x, rows - 1)) * N + (in ? n0 : 0));
+                }
+        };
+        load_base(0);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int c = min(ct * 64 + 16 * (l16 >> 2) + 4 * t + (l16 & 3), N - 1);
+        for (int t = 0; t < 8; ++t) {
+            const int c = min(n0 + t, N - 1);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const int c0 = 32 * k + 8 * g;
@@ -211,28 +221,26 @@ __global__ __launch_bounds__(256, 2) void adapter_forward_kernel(const AdapterPa
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RB; ++i) {
             if (i >= nrb) continue;
-            f32x4 d[4];
+            if (HB < RB && i > 0) load_base(i);
+            f32x4 d[8];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < 8; ++t) {
                 d[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) d[t] = mfma16(as_bf16x8(bv[t][k]), uo[i][k], d[t]);
+                for (int k = 0; k < KS; ++k) d[t] = mfma16(uo[i][k], as_bf16x8(bv[t][k]), d[t]);
             }
-            if (16 * i + l16 >= rows) continue;
-            uint16_t* yrow = p.out + static_cast<int64_t>(row0 + 16 * i + l16) * N + n0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (n0 + 8 * h >= N) continue;
-                const uint32_t bw[4] = {base[i][h].x, base[i][h].y, base[i][h].z, base[i][h].w};
+            for (int x = 0; x < 4; ++x) {
+                const int row = 16 * i + 4 * g + x;
+                const uint32_t bw[4] = {base[i % HB][x].x, base[i % HB][x].y, base[i % HB][x].z, base[i % HB][x].w};
                 uint32_t o[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4& dd = d[2 * h + (q >> 1)];
-                    o[q] = pack2(lo_f(bw[q]) + p.scale * dd[2 * (q & 1)], hi_f(bw[q]) + p.scale * dd[2 * (q & 1) + 1]);
-                }
-                *reinterpret_cast<uint4*>(yrow + 8 * h) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int q = 0; q < 4; ++q)
+                    o[q] = pack2(lo_f(bw[q]) + p.scale * d[2 * q][x], hi_f(bw[q]) + p.scale * d[2 * q + 1][x]);
+                if (in && row < rows)
+                    st16_nt(p.out + static_cast<int64_t>(row0 + row) * N + n0, make_uint4(o[0], o[1], o[2], o[3]));
             }
         }
     }
@@ -297,52 +305,58 @@ __device__ __forceinline__ uint4 ld16_at(const uint16_t* base, uint32_t bytes) {
     return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + bytes);
 }
 
-// Eight rows 8 g + t of the 32-row block at `block` (its first row, of row
+__device__ __forceinline__ uint4 ld16_nt_at(const uint16_t* base, uint32_t bytes) {
+    return ld16_nt(reinterpret_cast<const char*>(base) + bytes);
+}
+
+// Rows r0 .. r0 + R - 1 of the 32-row block at `block` (its first row, of row
 // length ld), of which `left` rows exist (later ones repeat the last), columns
 // c .. c + 7.  No branches: a load behind a branch would make the compiler
 // wait for every load before the next use of any.
-__device__ __forceinline__ void load_rows8(const uint16_t* block, int ld, int left, int c, uint4 (&v)[8]) {
-    const int g = (threadIdx.x & 63) >> 4;
+template <int R>
+__device__ __forceinline__ void load_rows(const uint16_t* block, int ld, int r0, int left, int c, uint4 (&v)[R]) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) v[t] = ld16_at(block, static_cast<uint32_t>(min(8 * g + t, left - 1) * ld + c) * 2);
+    for (int t = 0; t < R; ++t) v[t] = ld16_nt_at(block, static_cast<uint32_t>(min(r0 + t, left - 1) * ld + c) * 2);
 }
-__device__ __forceinline__ void mask_rows8(int row, int rows, bool in, uint4 (&v)[8]) {
-    const int g = (threadIdx.x & 63) >> 4;
+// Rows past `left`, and columns that do not exist, are zero.
+template <int R>
+__device__ __forceinline__ void mask_rows(int r0, int left, bool in, uint4 (&v)[R]) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const uint32_t keep = in && row + 8 * g + t < rows ? ~0u : 0u;
-        v[t] = make_uint4(v[t].x & keep, v[t].y & keep, v[t].z & keep, v[t].w & keep);
-    }
+    for (int t = 0; t < R; ++t) v[t] = and4(v[t], in && r0 + t < left ? ~0u : 0u);
 }
 
 // A wave's registers for the token rows are refilled for the next block as
 // soon as they are consumed, so that 8 KiB a wave are on their way for most of
 // the time.
 template <int RP>
-__global__ __launch_bounds__(ad_waves(RP) * 64) void adapter_dy_kernel(const AdapterParams p) {
-    constexpr int NW = ad_waves(RP);
-    constexpr int NT = RP / 16;
-    // each wave's 32 x 128 tile of dy; 16-byte chunk c of row i at c ^ (i & 15)
-    __shared__ __attribute__((aligned(16))) uint16_t s_dy[NW][AD_BLK * AD_WCOLS];
+__global__ __launch_bounds__(ad_groups(RP) * ad_split(RP) * 64) void adapter_dy_kernel(const AdapterParams p) {
+    constexpr int RS = ad_split(RP), NG = ad_groups(RP);
+    constexpr int NT = RP / 16 / RS;             // rank tiles of a wave
+    constexpr int MIN_THREADS = ad_groups_min(RP) * RS * 64;
+    // each column group's 32 x 128 tile of dy; 16-byte chunk c of row i at c ^ (i & 15).  Two for groups of
+    // two waves, which each bring half of the next block's rows while they compute.
+    __shared__ __attribute__((aligned(16))) uint16_t s_dy[RS][NG][AD_BLK * AD_WCOLS];
     __shared__ __attribute__((aligned(16))) uint16_t s_u[2][AD_BLK * RP];                      // U of a block
-    __shared__ __attribute__((aligned(16))) float s_du[2][NW][AD_BLK][RP + 4];                 // the waves' parts of du
+    __shared__ __attribute__((aligned(16))) float s_du[2][NG][AD_BLK][RP + 4];   // the groups' parts of du
     const int chunk = blockIdx.x % p.chunks1;   // neighbouring workgroups share rows
     const AdapterUnit un = find_unit(p, p.rows1, blockIdx.x / p.chunks1);
     if (un.e < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-    const int nw = blockDim.x / 64, nthreads = blockDim.x;
+    const int nthreads = blockDim.x, ng = nthreads / (64 * RS);
+    const int grp = wave / RS, r0 = wave % RS * (RP / RS);   // the wave's columns and first rank
     const int l16 = lane & 15, g = lane >> 4;
     const int N = p.N, r = p.r;
-    const int c0 = (chunk * nw + wave) * AD_WCOLS;
+    const int c0 = (chunk * ng + grp) * AD_WCOLS;
     const bool in = c0 + 8 * l16 < N;
     const int cl = in ? c0 + 8 * l16 : 0;         // the lane's columns
     const bool whole = c0 + AD_WCOLS <= N;
     const uint16_t* be = p.b + static_cast<int64_t>(un.e) * N * r;
+    const uint16_t* dy0 = p.dy + static_cast<int64_t>(un.row0) * N;
     const uint16_t* ue = p.u + static_cast<int64_t>(un.row0) * r;
 
     // U of a block is 32 r values in a row: 16 bytes a thread, from any 2-byte boundary.  A load that would
     // reach past the tensor's end takes its values one by one.
-    constexpr int UPT = (AD_BLK * RP / 8 + ad_waves_min(RP) * 64 - 1) / (ad_waves_min(RP) * 64);
+    constexpr int UPT = (AD_BLK * RP / 8 + MIN_THREADS - 1) / MIN_THREADS;
     const uint16_t* uend = p.u + static_cast<int64_t>(p.M) * r;
     uint4 uv[UPT];
     auto load_u = [&](int row) {
@@ -368,31 +382,45 @@ __global__ __launch_bounds__(ad_waves(RP) * 64) void adapter_dy_kernel(const Ada
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[i] = s_u[buf][(8 * g + i) * r + 16 * j + l16];
+            w[i] = s_u[buf][(8 * g + i) * r + r0 + 16 * j + l16];
             if (left < AD_BLK && 8 * g + i >= left) w[i] = 0;     // rows past the end: not U's
         }
         return as_bf16x8(make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16)));
     };
-    uint4 t[8];
+    constexpr int TR = 8 / RS;                   // of each 32-row block a lane loads rows rl .. rl + TR - 1
+    const int rl = 8 * g + wave % RS * TR;
+    uint4 t[TR];
+    auto load_t = [&](int row) { load_rows<TR>(dy0 + static_cast<int64_t>(row) * N, N, rl, un.rows - row, cl, t); };
+    auto put_t = [&](int row, int buf) {
+        if (!whole || row + AD_BLK > un.rows) mask_rows<TR>(rl, un.rows - row, in, t);
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+            *reinterpret_cast<uint4*>(&s_dy[buf % RS][grp][(rl + i) * AD_WCOLS + ((l16 ^ ((rl + i) & 15)) << 3)]) = t[i];
+    };
+    load_u(0);
+    load_t(0);
     bf16x8 bw[4][NT];   // b as the operand of du: rank 16 j + l16, columns c0 + 32 k + 8 g ..
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int c = c0 + 32 * k + 8 * g, rr = 16 * j + l16;
+            const int c = c0 + 32 * k + 8 * g, rr = r0 + 16 * j + l16;
             bw[k][j] = as_bf16x8(gather8(be + static_cast<int64_t>(min(c, N - 1)) * r + min(rr, r - 1), r, rr < r ? N - c : 0));
         }
         if (NT * (k + 1) % 4 == 0) __builtin_amdgcn_sched_barrier(0);   // 32 loads at a time
     }
-    load_u(0);
-    const uint16_t* dy0 = p.dy + static_cast<int64_t>(un.row0) * N;
-    load_rows8(dy0, N, un.rows, cl, t);
     f32x4 acc[8][NT];
 #pragma unroll
     for (int c = 0; c < 8; ++c)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[c][j] = f32x4{0, 0, 0, 0};
     put_u(0);
+    const int last = (un.rows - 1) / AD_BLK * AD_BLK;
+    if constexpr (RS > 1) {
+        put_t(0, 0);
+        load_u(min(AD_BLK, last));
+        load_t(min(AD_BLK, last));
+    }
     __syncthreads();
 
     // the waves' parts of du of the block at `row`, added up and stored
@@ -401,30 +429,34 @@ __global__ __launch_bounds__(ad_waves(RP) * 64) void adapter_dy_kernel(const Ada
         for (int i = tid; i < AD_BLK * RP / 4; i += nthreads) {
             const int rr = i / (RP / 4), c = i % (RP / 4) * 4;
             f32x4 sum = *reinterpret_cast<const f32x4*>(&s_du[buf][0][rr][c]);
-            for (int w = 1; w < nw; ++w) sum += *reinterpret_cast<const f32x4*>(&s_du[buf][w][rr][c]);
+            for (int w = 1; w < ng; ++w) sum += *reinterpret_cast<const f32x4*>(&s_du[buf][w][rr][c]);
             *reinterpret_cast<f32x4*>(part + rr * RP + c) = sum;
         }
     };
-    const int last = (un.rows - 1) / AD_BLK * AD_BLK;
     int buf = 0;
     for (int row = 0; row < un.rows; row += AD_BLK, buf ^= 1) {
-        if (!whole || row + AD_BLK > un.rows) mask_rows8(row, un.rows, in, t);
-        uint16_t* tile = s_dy[wave];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int rr = 8 * g + i;
-            *reinterpret_cast<uint4*>(tile + rr * AD_WCOLS + ((l16 ^ (rr & 15)) << 3)) = t[i];
-        }
-        uint4 tr[8];
-        transpose8(t, tr);
-        // Memory operations complete in order: the stores go out before the next loads, whose
-        // wait (above, in the next block) would otherwise be for the stores too.
-        if (row > 0) store_du(row - AD_BLK, buf ^ 1);
         const int ahead = min(row + AD_BLK, last);
-        load_u(ahead);
-        __builtin_amdgcn_sched_barrier(0);   // t is free: nothing of the refill moves above
-        load_rows8(dy0 + static_cast<int64_t>(ahead) * N, N, un.rows - ahead, cl, t);
-        __builtin_amdgcn_sched_barrier(0);   // nor does it wait for what follows
+        uint4 tr[8];
+        const uint16_t* tile = s_dy[buf % RS][grp];
+        if constexpr (RS == 1) {
+            put_t(row, buf);
+            transpose8(t, tr);
+        } else {
+            uint4 rows8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                rows8[i] = *reinterpret_cast<const uint4*>(tile + (8 * g + i) * AD_WCOLS + ((l16 ^ ((8 * g + i) & 15)) << 3));
+            transpose8(rows8, tr);
+        }
+        // Memory operations complete in order: the stores go out before the next loads, whose
+        // wait (in the next block) would otherwise be for the stores too.
+        if (row > 0) store_du(row - AD_BLK, buf ^ 1);
+        if constexpr (RS == 1) {
+            load_u(ahead);
+            __builtin_amdgcn_sched_barrier(0);   // t is free: nothing of the refill moves above
+            load_t(ahead);
+            __builtin_amdgcn_sched_barrier(0);   // nor does it wait for what follows
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const bf16x8 ut = read_u(buf, j, un.rows - row);
@@ -450,8 +482,15 @@ __global__ __launch_bounds__(ad_waves(RP) * 64) void adapter_dy_kernel(const Ada
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                *reinterpret_cast<f32x4*>(&s_du[buf][wave][16 * h + l16][16 * j + 4 * g]) = du[h][j];
+                *reinterpret_cast<f32x4*>(&s_du[buf][grp][16 * h + l16][r0 + 16 * j + 4 * g]) = du[h][j];
         put_u(buf ^ 1);
+        if constexpr (RS > 1) {
+            // the next block's rows into the other tile, and the loads of the one after it
+            put_t(ahead, buf ^ 1);
+            const int after = min(row + 2 * AD_BLK, last);
+            load_u(after);
+            load_t(after);
+        }
         // The waves' parts are in; the next block's go to the other buffers.  Only LDS is
         // handed over here, so the rows on their way are not waited for.
         block_barrier();
@@ -467,7 +506,7 @@ __global__ __launch_bounds__(ad_waves(RP) * 64) void adapter_dy_kernel(const Ada
         for (int c = 0; c < 8; ++c)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int n = c0 + 8 * (4 * g + x) + c, rr = 16 * j + l16;
+                const int n = c0 + 8 * (4 * g + x) + c, rr = r0 + 16 * j + l16;
                 if (n < N && rr < r) {
                     float* o = out + static_cast<int64_t>(n) * r + rr;
                     const float v = p.scale * acc[c][j][x];
@@ -530,8 +569,8 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
     constexpr int NT = RP / 16;
     constexpr int UW = RP < 32 ? 32 : RP;
     constexpr int KS = UW / 32;
-    // a as the operand of dx, for each wave: tile t of 64-column half h, ranks 32 k + 8 g ..
-    __shared__ __attribute__((aligned(16))) uint4 s_aw[4][2][4][KS][64];
+    // a as the operand of dx, for each wave: columns c0 + 8 l16 + t, ranks 32 k + 8 g ..
+    __shared__ __attribute__((aligned(16))) uint4 s_aw[4][8][KS][64];
     const int chunk = blockIdx.x % p.chunks2;
     const AdapterUnit un = find_unit(p, p.rows2, blockIdx.x / p.chunks2);
     if (un.e < 0) return;
@@ -544,24 +583,19 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
     const int cl = in ? c0 + 8 * l16 : 0;
     const uint16_t* ae = p.a + static_cast<int64_t>(un.e) * r * K;
 
-    uint4 x[8], base[2][2][2];
+    uint4 x[8], base[2][4];
     bf16x8 dt[3][NT], dr[2][KS];
     const uint16_t* x0 = p.x + static_cast<int64_t>(un.row0) * K;
     // without a base its place is taken by x, cleared: the loads stay the same
     const uint16_t* base0 = (p.base ? p.base : p.x) + static_cast<int64_t>(un.row0) * K;
     const uint32_t keep = p.base ? ~0u : 0u;
-    auto load_base = [&](int row) {
+    auto load_base = [&](int row) {   // rows 16 i + 4 g + x of the block at `row`
         const uint16_t* from = base0 + static_cast<int64_t>(row) * K;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // columns past K: x's first ones instead, whose results are not stored
-                const int c = c0 + 64 * h + 16 * g, rr = min(16 * i + l16, un.rows - row - 1) * K;
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    base[i][h][q] = ld16_at(from, static_cast<uint32_t>(rr + (c + 8 * q < K ? c + 8 * q : 0)) * 2);
-            }
+            for (int x = 0; x < 4; ++x)
+                base[i][x] = ld16_nt_at(from, static_cast<uint32_t>(min(16 * i + 4 * g + x, un.rows - row - 1) * K + cl) * 2);
     };
     auto load_dt = [&](int row) {
         const uint16_t* from = p.du_t + (static_cast<int64_t>(un.blk0) + row / AD_BLK) * 3 * RP * AD_BLK;
@@ -578,19 +612,17 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
 #pragma unroll
             for (int k = 0; k < KS; ++k) dr[i][k] = as_bf16x8(ld16_at(from, ((16 * i + l16) * UW + 32 * k + 8 * g) * 2));
     };
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int c = c0 + 64 * h + 16 * (l16 >> 2) + 4 * t + (l16 & 3), rr = 32 * k + 8 * g;
-                s_aw[wave][h][t][k][lane] = gather8(ae + static_cast<int64_t>(min(rr, r - 1)) * K + min(c, K - 1), K, c < K ? r - rr : 0);
-            }
-    load_rows8(x0, K, un.rows, cl, x);
+    load_rows<8>(x0, K, 8 * g, un.rows, cl, x);
     load_dt(0);
     load_base(0);
     load_dr(0);
+#pragma unroll 4
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int rr = 32 * k + 8 * g;
+            s_aw[wave][t][k][lane] = gather8(ae + static_cast<int64_t>(min(rr, r - 1)) * K + cl + t, K, in ? r - rr : 0);
+        }
     f32x4 acc[8][NT];
 #pragma unroll
     for (int c = 0; c < 8; ++c)
@@ -600,12 +632,11 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
     const int last = (un.rows - 1) / AD_BLK * AD_BLK;
     for (int row = 0; row < un.rows; row += AD_BLK) {
         const int ahead = min(row + AD_BLK, last);
-        if (!whole || row + AD_BLK > un.rows) mask_rows8(row, un.rows, in, x);
+        if (!whole || row + AD_BLK > un.rows) mask_rows<8>(8 * g, un.rows - row, in, x);
         uint4 tr[8];
         transpose8(x, tr);
         __builtin_amdgcn_sched_barrier(0);   // x is free: nothing of the refill moves above
-        load_rows8(x0 + static_cast<int64_t>(ahead) * K, K, un.rows - ahead, cl, x);
-        __builtin_amdgcn_sched_barrier(0);   // nor does it wait for what follows
+        load_rows<8>(x0 + static_cast<int64_t>(ahead) * K, K, 8 * g, un.rows - ahead, cl, x);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
@@ -616,47 +647,34 @@ __global__ __launch_bounds__(256) void adapter_dx_kernel(const AdapterParams p) 
         load_dt(ahead);
         int at = lane;
         asm volatile("" : "+v"(at));         // a's operands are read anew in every block, not held
+        f32x4 d[2][8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            bf16x8 aw[4][KS];
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int i = 0; i < 2; ++i) d[i][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) aw[t][k] = as_bf16x8(s_aw[wave][h][t][k][at]);
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f32x4 d[4];
+            for (int k = 0; k < KS; ++k) {
+                const bf16x8 aw = as_bf16x8(s_aw[wave][t][k][at]);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    d[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) d[t] = mfma16(aw[t][k], dr[i][k], d[t]);
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint4 bs = and4(base[i][h][q], keep);
-                    const uint32_t bw[4] = {bs.x, bs.y, bs.z, bs.w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const f32x4& dd = d[2 * q + (m >> 1)];
-                        o[m] = pack2(lo_f(bw[m]) + dd[2 * (m & 1)], hi_f(bw[m]) + dd[2 * (m & 1) + 1]);
-                    }
-                    base[i][h][q] = make_uint4(o[0], o[1], o[2], o[3]);
-                }
+                for (int i = 0; i < 2; ++i) d[i][t] = mfma16(dr[i][k], aw, d[i][t]);
             }
-        }
-        // base now holds dx
-        uint16_t* to = p.out + static_cast<int64_t>(un.row0 + row) * K + c0;
-        const uint32_t at0 = static_cast<uint32_t>(l16 * K + 16 * g);
+        uint16_t* to = p.out + static_cast<int64_t>(un.row0 + row) * K;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int x = 0; x < 4; ++x) {
+                const uint4 bs = and4(base[i][x], keep);
+                const uint32_t bw[4] = {bs.x, bs.y, bs.z, bs.w};
+                uint32_t o[4];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (row + 16 * i + l16 < un.rows && c0 + 64 * h + 16 * g + 8 * q < K)
-                        *reinterpret_cast<uint4*>(to + 16 * i * K + (at0 + 64 * h + 8 * q)) = base[i][h][q];
+                for (int q = 0; q < 4; ++q)
+                    o[q] = pack2(lo_f(bw[q]) + d[i][2 * q][x], hi_f(bw[q]) + d[i][2 * q + 1][x]);
+                const int rr = 16 * i + 4 * g + x;
+                if (in && row + rr < un.rows)
+                    st16_nt(to + static_cast<uint32_t>(rr * K + cl), make_uint4(o[0], o[1], o[2], o[3]));
+            }
         __builtin_amdgcn_sched_barrier(0);
         load_dr(ahead);
         load_base(ahead);
@@ -708,7 +726,16 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(const AdapterParams p
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size;
          i += static_cast<int64_t>(gridDim.x) * 1024) {
         f32x4 v = {0, 0, 0, 0};
-        for (int k = 0; k < n; ++k) v += *reinterpret_cast<const f32x4*>(part + (s0 + k) * size + i);
+        const float* at = part + s0 * size + i;
+        int k = 0;
+        for (; k + 4 <= n; k += 4) {
+            f32x4 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const f32x4*>(at + (k + q) * size);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v += w[q];
+        }
+        for (; k < n; ++k) v += *reinterpret_cast<const f32x4*>(at + k * size);
         f32x4* o = reinterpret_cast<f32x4*>(out + i);
         if (p.accumulate) v += *o;
         *o = v;
@@ -716,16 +743,25 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(const AdapterParams p
 }
 
 // ---------------------------------------------------------------- launchers
+template <int RP, int RB>
+static hipError_t forward_rows(const AdapterParams& p, int num_cu, hipStream_t s) {
+    constexpr int W = af_waves(RB);
+    const int64_t blocks = static_cast<int64_t>(p.M) / (16 * RB) + (p.M < p.E ? p.M : p.E);
+    // sixteen waves for each CU where the rows alone give fewer, down to one tile a wave
+    const int64_t tiles = (p.N + 127) / 128;
+    int64_t split = 16 / W * static_cast<int64_t>(num_cu) / blocks;
+    split = split < 1 ? 1 : split;
+    const int64_t per = ((tiles + split - 1) / split + W - 1) / W * W;
+    hipLaunchKernelGGL((adapter_forward_kernel<RP, RB>),
+                       dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((tiles + per - 1) / per)), dim3(W * 64), 0, s,
+                       p);
+    return hipGetLastError();
+}
+
+// Small blocks where the experts have at most 48 rows each on average.
 template <int RP>
 static hipError_t forward_of(const AdapterParams& p, int num_cu, hipStream_t s) {
-    const int64_t blocks = static_cast<int64_t>(p.M) / AF_ROWS + (p.M < p.E ? p.M : p.E);
-    // four workgroups for each CU where the rows alone give fewer, down to 256 columns each
-    int64_t split = 4 * static_cast<int64_t>(num_cu) / blocks;
-    const int64_t most = (p.N + 255) / 256;
-    split = split < 1 ? 1 : (split > most ? most : split);
-    hipLaunchKernelGGL((adapter_forward_kernel<RP>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(split)),
-                       dim3(256), 0, s, p);
-    return hipGetLastError();
+    return p.M <= 48 * static_cast<int64_t>(p.E) ? forward_rows<RP, 2>(p, num_cu, s) : forward_rows<RP, 4>(p, num_cu, s);
 }
 
 hipError_t launch_adapter_forward(const AdapterParams& p, int num_cu, hipStream_t s) {
@@ -743,11 +779,11 @@ static hipError_t backward_of(AdapterParams p, int num_cu, hipStream_t s) {
     p.chunks2 = (p.K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS);
     // the columns of dy spread evenly over its chunks
     const int parts = (p.N + AD_WCOLS - 1) / AD_WCOLS, even = (parts + p.chunks1 - 1) / p.chunks1;
-    const int waves = even > ad_waves_min(RP) ? even : ad_waves_min(RP);
+    const int groups = even > ad_groups_min(RP) ? even : ad_groups_min(RP);
     hipError_t st;
     if (p.M > 0) {
         hipLaunchKernelGGL((adapter_dy_kernel<RP>), dim3(static_cast<unsigned>((p.M / p.rows1 + few) * p.chunks1)),
-                           dim3(static_cast<unsigned>(waves) * 64), 0, s, p);
+                           dim3(static_cast<unsigned>(groups * ad_split(RP)) * 64), 0, s, p);
         if ((st = hipGetLastError()) != hipSuccess) return st;
         const int64_t most = static_cast<int64_t>(num_cu) * 6;
         hipLaunchKernelGGL((adapter_du_kernel<RP>), dim3(static_cast<unsigned>(p.blocks < most ? p.blocks : most)), dim3(256),
@@ -757,8 +793,8 @@ static hipError_t backward_of(AdapterParams p, int num_cu, hipStream_t s) {
                            dim3(256), 0, s, p);
         if ((st = hipGetLastError()) != hipSuccess) return st;
     }
-    const int64_t width = p.N > p.K ? p.N : p.K, gx = (width * p.r / 4 + 1023) / 1024;
-    hipLaunchKernelGGL(adapter_join_kernel, dim3(static_cast<unsigned>(gx < 16 ? gx : 16), 2, static_cast<unsigned>(p.E)),
+    const int64_t width = p.N > p.K ? p.N : p.K, gx = (width * p.r / 4 + 511) / 512;
+    hipLaunchKernelGGL(adapter_join_kernel, dim3(static_cast<unsigned>(gx < 64 ? gx : 64), 2, static_cast<unsigned>(p.E)),
                        dim3(256), 0, s, p);
     return hipGetLastError();
 }

