@@ -133,6 +133,57 @@ __global__ __launch_bounds__(af_waves(RB) * 64, 2) void adapter_forward_kernel(c
     const int N = p.N, r = p.r;
     const uint16_t* ae = p.a + static_cast<int64_t>(e) * r * p.K;
 
+    // b's rows are 2 r bytes apart: a 16-byte load may start anywhere and may reach into the next
+    // row, whose values are cleared, but not past the tensor's end
+    const uint16_t* be = p.b + static_cast<int64_t>(e) * N * r;
+    const uint16_t* bend = p.b + static_cast<int64_t>(p.E) * N * r;
+    uint4 bmask[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        const int n = r - 32 * k - 8 * g;     // ranks of this lane's eight that exist
+        auto word = [&](int w) { return n >= 2 * w + 2 ? ~0u : (n == 2 * w + 1 ? 0xffffu : 0u); };
+        bmask[k] = make_uint4(word(0), word(1), word(2), word(3));
+    }
+    const int tiles = (N + 127) / 128;
+    const int per = (tiles + gridDim.y - 1) / gridDim.y;   // a multiple of W but for few tiles
+    const int t1 = min(tiles, static_cast<int>(blockIdx.y + 1) * per);
+    int ct = blockIdx.y * per + wave;
+    // Small blocks keep one tile's operands ahead, the first of them from before U: with little else
+    // in flight, a wave's time is the latency of its loads.
+    constexpr int HB = RP == 64 && RB == 4 ? 1 : RB;   // row blocks whose base is held at a time (registers)
+    constexpr bool AHEAD = RB == 2 && RP <= 32;
+    uint4 bv[AHEAD ? 2 : 1][8][KS], base[AHEAD ? 2 : 1][HB][4];
+    auto load_base = [&](int buf, int tile, int first) {   // rows 16 i + 4 g + x, columns 128 tile + 8 l16 ..
+        const int n0 = tile * 128 + 8 * l16;
+#pragma unroll
+        for (int i = 0; i < HB; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                base[buf][i][x] = make_uint4(0, 0, 0, 0);
+                if (p.base && first + i < nrb)
+                    base[buf][i][x] = ld16_nt(p.base + static_cast<int64_t>(row0 + min(16 * (first + i) + 4 * g + x, rows - 1)) * N +
+                                              (n0 < N ? n0 : 0));
+            }
+    };
+    auto load_tile = [&](int buf, int tile) {
+        load_base(buf, tile, 0);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int c = min(tile * 128 + 8 * l16 + t, N - 1);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const int c0 = 32 * k + 8 * g;
+                const uint16_t* src = be + static_cast<int64_t>(c) * r + c0;
+                bv[buf][t][k] = make_uint4(0, 0, 0, 0);
+                if (c0 < r) {
+                    if (src + 8 <= bend) __builtin_memcpy(&bv[buf][t][k], src, 16);
+                    else bv[buf][t][k] = gather8(src, 1, r - c0);
+                }
+            }
+        }
+    };
+    if (AHEAD && ct < t1) load_tile(0, ct);
+
     // ---- U: fewer row blocks leave registers for more columns in flight
     {
         f32x4 acc[RB][NT];
@@ -140,7 +191,7 @@ __global__ __launch_bounds__(af_waves(RB) * 64, 2) void adapter_forward_kernel(c
         for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        if (nrb == 1) adapter_u<NT, 1, NT == 1 ? 2 : 1, W>(p, ae, row0, rows, wave, acc);
+        if (nrb == 1) adapter_u<NT, 1, NT == 1 ? 4 : (NT == 2 ? 2 : 1), W>(p, ae, row0, rows, wave, acc);
         else if (RB == 2 || nrb == 2) adapter_u<NT, 2, 1, W>(p, ae, row0, rows, wave, acc);
         else adapter_u<NT, RB, 1, W>(p, ae, row0, rows, wave, acc);
 #pragma unroll
@@ -164,84 +215,58 @@ __global__ __launch_bounds__(af_waves(RB) * 64, 2) void adapter_forward_kernel(c
     __syncthreads();
 
     // ---- y
-    constexpr int HB = RP == 64 && RB == 4 ? 1 : RB;   // row blocks whose base is held at a time (registers)
     bf16x8 uo[RB][KS];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
             if (i < nrb) uo[i][k] = *reinterpret_cast<const bf16x8*>(&s_u[16 * i + l16][32 * k + 8 * g]);
-    // b's rows are 2 r bytes apart: a 16-byte load may start anywhere and may reach into the next
-    // row, whose values are cleared, but not past the tensor's end
-    const uint16_t* be = p.b + static_cast<int64_t>(e) * N * r;
-    const uint16_t* bend = p.b + static_cast<int64_t>(p.E) * N * r;
-    uint4 bmask[KS];
+    auto do_tile = [&](int buf, int tile) {
+        const int n0 = tile * 128 + 8 * l16;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-        const int n = r - 32 * k - 8 * g;     // ranks of this lane's eight that exist
-        auto word = [&](int w) { return n >= 2 * w + 2 ? ~0u : (n == 2 * w + 1 ? 0xffffu : 0u); };
-        bmask[k] = make_uint4(word(0), word(1), word(2), word(3));
-    }
-    const int tiles = (N + 127) / 128;
-    const int per = (tiles + gridDim.y - 1) / gridDim.y;   // a multiple of W but for few tiles
-    const int t1 = min(tiles, static_cast<int>(blockIdx.y + 1) * per);
-    for (int ct = blockIdx.y * per + wave; ct < t1; ct += W) {
-        const int n0 = ct * 128 + 8 * l16;          // the lane's 8 columns of rows 16 i + 4 g + x
-        const bool in = n0 < N;
-        uint4 bv[8][KS], base[HB][4];
-        auto load_base = [&](int first) {
-#pragma unroll
-            for (int i = 0; i < HB; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    base[i][x] = make_uint4(0, 0, 0, 0);
-                    if (p.base && first + i < nrb)
-                        base[i][x] = ld16_nt(
-                            p.base + static_cast<int64_t>(row0 + min(16 * (first + i) + 4 * g + x, rows - 1)) * N + (in ? n0 : 0));
-                }
-        };
-        load_base(0);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int c = min(n0 + t, N - 1);
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                const int c0 = 32 * k + 8 * g;
-                const uint16_t* src = be + static_cast<int64_t>(c) * r + c0;
-                bv[t][k] = make_uint4(0, 0, 0, 0);
-                if (c0 < r) {
-                    if (src + 8 <= bend) {
-                        __builtin_memcpy(&bv[t][k], src, 16);
-                        bv[t][k] = make_uint4(bv[t][k].x & bmask[k].x, bv[t][k].y & bmask[k].y, bv[t][k].z & bmask[k].z,
-                                              bv[t][k].w & bmask[k].w);
-                    } else {
-                        bv[t][k] = gather8(src, 1, r - c0);
-                    }
-                }
+                uint4& v = bv[buf][t][k];
+                v = make_uint4(v.x & bmask[k].x, v.y & bmask[k].y, v.z & bmask[k].z, v.w & bmask[k].w);
             }
-        }
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
             if (i >= nrb) continue;
-            if (HB < RB && i > 0) load_base(i);
+            if (HB < RB && i > 0) load_base(buf, tile, i);
             f32x4 d[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 d[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) d[t] = mfma16(uo[i][k], as_bf16x8(bv[t][k]), d[t]);
+                for (int k = 0; k < KS; ++k) d[t] = mfma16(uo[i][k], as_bf16x8(bv[buf][t][k]), d[t]);
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int row = 16 * i + 4 * g + x;
-                const uint32_t bw[4] = {base[i % HB][x].x, base[i % HB][x].y, base[i % HB][x].z, base[i % HB][x].w};
+                const uint4 bs = base[buf][i % HB][x];
+                const uint32_t bw[4] = {bs.x, bs.y, bs.z, bs.w};
                 uint32_t o[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     o[q] = pack2(lo_f(bw[q]) + p.scale * d[2 * q][x], hi_f(bw[q]) + p.scale * d[2 * q + 1][x]);
-                if (in && row < rows)
+                if (n0 < N && row < rows)
                     st16_nt(p.out + static_cast<int64_t>(row0 + row) * N + n0, make_uint4(o[0], o[1], o[2], o[3]));
             }
+        }
+    };
+    if constexpr (AHEAD) {
+        for (; ct < t1; ct += 2 * W) {
+            if (ct + W < t1) load_tile(1, ct + W);
+            do_tile(0, ct);
+            if (ct + W >= t1) break;
+            if (ct + 2 * W < t1) load_tile(0, ct + 2 * W);
+            do_tile(1, ct + W);
+        }
+    } else {
+        for (; ct < t1; ct += W) {
+            load_tile(0, ct);
+            do_tile(0, ct);
         }
     }
 }
