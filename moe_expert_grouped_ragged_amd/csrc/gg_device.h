@@ -131,6 +131,14 @@ __device__ __forceinline__ int find_expert(const int* s_pre, int E, int t) {
     return lo;
 }
 
+// The same by a whole wave: every lane looks at every 64th expert.
+__device__ __forceinline__ int find_expert_wave(const int* s_pre, int E, int t) {
+    int below = 0;   // experts with s_pre <= t, which come first
+    for (int e = threadIdx.x & 63; e - static_cast<int>(threadIdx.x & 63) < E; e += 64)
+        below += __builtin_popcountll(__ballot(e < E && s_pre[min(e, E - 1)] <= t));
+    return below - 1;
+}
+
 template <int V> struct GrpTag { static constexpr int value = V; };
 // f(GrpTag<0>{}), ..., f(GrpTag<N - 1>{}): a loop over compile-time indices.
 template <int N, int I = 0, typename F>

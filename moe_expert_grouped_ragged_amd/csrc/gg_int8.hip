@@ -343,7 +343,7 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
     const int total = uni(s_pre[p.E]);
     const int wave = uni(threadIdx.x >> 6);
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
-        const int e = uni(find_expert(s_pre, p.E, it));
+        const int e = uni(find_expert_wave(s_pre, p.E, it));
         const int local = it - uni(s_pre[e]);
         const int grp = local / items_n, col = local - grp * items_n;
         const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
@@ -365,10 +365,12 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
 // the packed layout; fragment reads of both are free of bank conflicts.  Each
 // of a stage's two 32-byte steps is 16 matrix instructions a wave, while the
 // next step's eight fragments are read; the only barrier of a stage sits
-// before its second step, where the next stage has landed and every wave has
+// in its second step, where the next stage has landed and every wave has
 // read the last fragments of this one, whose slot is refilled from there on.
 // The epilogue scales and rounds through a small staging area of its own, so
-// the next tile's first stages are already on their way.
+// the next tile's first four stages are already on their way, and the waits of
+// those stages leave the epilogue's stores outstanding: memory operations
+// complete in order, and the stores were issued after the copies.
 constexpr int I8_STAGE = 64, I8_SLOTS = 4;
 constexpr int I8_SLOT_BYTES = 2 * I8_TILE * I8_STAGE;
 constexpr int I8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf16
@@ -379,6 +381,7 @@ __device__ __forceinline__ int acc_rd_i(int a) {
     return v;
 }
 
+template <bool SCALED>   // whether the output columns have scales
 __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
     __shared__ __attribute__((aligned(1024))) int8_t s_ring[I8_SLOTS * I8_SLOT_BYTES];
     __shared__ __attribute__((aligned(16))) int8_t s_stg[4 * I8_STG_BYTES];
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
     int wb[2];                        // this wave's two 32-column blocks
     int e = 0, row0 = 0, rows = 0, col0 = 0;
     auto setup = [&](int t) {
-        e = uni(find_expert(s_pre, p.E, t));
+        e = uni(find_expert_wave(s_pre, p.E, t));
         const int local = t - uni(s_pre[e]);
         const int lo = uni(s_off[e]), m = i8_tile_rows(uni(s_off[e + 1]) - lo);
         const int tiles_m = (m + I8_TILE - 1) / I8_TILE;
@@ -422,154 +425,205 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) wb[i] = min(col0 / 32 + 2 * wave + i, nblocks - 1);
     };
-    // half h of stage st (past the end: the last stage again, into a slot that is not read)
-    auto copy = [&](int st, int h) {
-        const int ss = min(st, nstages - 1);
+    // One of the eight copies of a stage that this wave issues (nothing past the last stage).
+    auto piece = [&](int st, auto i_tag) {
+        constexpr int i = decltype(i_tag)::value;
+        if (st >= nstages) return;
         const uint32_t dst = ring + (st & 3) * I8_SLOT_BYTES;
-#pragma unroll
-        for (int i = 2 * h; i < 2 * h + 2; ++i)
-            dma16(t_base + ss * I8_STAGE, t_voff[i], dst + (64 * wave + 16 * i) * I8_STAGE);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            dma16(w_base + (static_cast<int64_t>(wb[h]) * nsteps + 2 * ss + u) * 1024, lane * 16,
+        if constexpr (i < 4) {
+            dma16(t_base + st * I8_STAGE, t_voff[i], dst + (64 * wave + 16 * i) * I8_STAGE);
+        } else {
+            constexpr int h = (i - 4) >> 1, u = i & 1;
+            dma16(w_base + (static_cast<int64_t>(wb[h]) * nsteps + 2 * st + u) * 1024, lane * 16,
                   dst + I8_TILE * I8_STAGE + ((2 * wave + h) * 2 + u) * 1024);
+        }
     };
 
     i32x16 acc[4][4];    // [row block][column block]
     i32x4 tf[2][4], wf[2][4];
-    auto read = [&](int st, auto u_tag) {
+    auto read_t = [&](int st, auto u_tag) {
         constexpr int u = decltype(u_tag)::value;
         const int8_t* sl = s_ring + (st & 3) * I8_SLOT_BYTES;
         const int c = (2 * u + (lane >> 5)) ^ ((lane >> 2) & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             tf[u][i] = *reinterpret_cast<const i32x4*>(sl + (128 * wr + 32 * i + (lane & 31)) * I8_STAGE + 16 * c);
+    };
+    auto read_w = [&](int st, auto u_tag) {
+        constexpr int u = decltype(u_tag)::value;
+        const int8_t* sl = s_ring + (st & 3) * I8_SLOT_BYTES;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             wf[u][j] = *reinterpret_cast<const i32x4*>(sl + I8_TILE * I8_STAGE + ((4 * wc + j) * 2 + u) * 1024 + lane * 16);
     };
-    auto mma = [&](auto u_tag, auto first_tag) {
-        constexpr int u = decltype(u_tag)::value;
+    // the four matrix instructions of row block i in step u; the tile's first step starts its sums from zero
+    auto mma = [&](auto u_tag, auto i_tag, auto first_tag) {
+        constexpr int u = decltype(u_tag)::value, i = decltype(i_tag)::value;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (decltype(first_tag)::value != 0)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], i32x16{}, 0, 0, 0);
-                else
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], acc[i][j], 0, 0, 0);
-            }
-    };
-    // issue order of a step: a fragment read between every two matrix instructions
-    auto interleave = [&]() {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // two matrix instructions
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (decltype(first_tag)::value != 0)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], i32x16{}, 0, 0, 0);
+            else
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], acc[i][j], 0, 0, 0);
         }
     };
-    auto stage = [&](int st, auto first_tag) {
-        read(st, GrpTag<1>{});
-        mma(GrpTag<0>{}, first_tag);
-        copy(st + 3, 1);
-        interleave();
-        // stage st + 1 has landed (the two after it may be under way), and
-        // every wave holds its last fragments of stage st
-        wait_vmcnt<16>();
-        block_barrier();
-        read(st + 1, GrpTag<0>{});
-        mma(GrpTag<1>{}, GrpTag<0>{});
-        copy(st + 4, 0);
-        interleave();
+    auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
+    // Waits until at most n copies and stores issued after those of the stage that is needed are outstanding.
+    auto wait_after = [&](int n) {
+        if (n >= 48) wait_vmcnt<48>();
+        else if (n >= 40) wait_vmcnt<40>();
+        else if (n >= 32) wait_vmcnt<32>();
+        else if (n >= 16) wait_vmcnt<16>();
+        else if (n >= 8) wait_vmcnt<8>();
+        else wait_vmcnt<0>();
     };
-    // the copies before a tile's first stage: 0 .. 2 and the first half of 3
+    // Stage st: two steps of four groups of four matrix instructions, each
+    // group followed by one copy; the next step's fragments are read during
+    // the first groups of a step.  stores: what the last tile's epilogue
+    // issued behind the copies of stages 0 .. 3, at least.
+    auto stage = [&](int st, int stores, auto first_tag, auto last_tag) {
+        const int c3 = decltype(first_tag)::value != 0 ? nstages : st + 3;    // the prologue brought stage 3
+        read_w(st, GrpTag<1>{});
+        mma(GrpTag<0>{}, GrpTag<0>{}, first_tag);
+        piece(c3, GrpTag<3>{});
+        fence();
+        read_t(st, GrpTag<1>{});
+        mma(GrpTag<0>{}, GrpTag<1>{}, first_tag);
+        piece(c3, GrpTag<4>{});
+        fence();
+        mma(GrpTag<0>{}, GrpTag<2>{}, first_tag);
+        piece(c3, GrpTag<5>{});
+        fence();
+        mma(GrpTag<0>{}, GrpTag<3>{}, first_tag);
+        piece(c3, GrpTag<6>{});
+        fence();
+        mma(GrpTag<1>{}, GrpTag<0>{}, GrpTag<0>{});
+        piece(c3, GrpTag<7>{});
+        fence();
+        if constexpr (decltype(last_tag)::value == 0) {
+            // stage st + 1 has landed, and every wave holds its last fragments of stage st, whose slot
+            // is refilled from here on
+            wait_after(8 * min(nstages - 2 - st, 2) + (st < 3 ? stores : 0));
+            block_barrier();
+            read_w(st + 1, GrpTag<0>{});
+            mma(GrpTag<1>{}, GrpTag<1>{}, GrpTag<0>{});
+            piece(st + 4, GrpTag<0>{});
+            fence();
+            read_t(st + 1, GrpTag<0>{});
+            mma(GrpTag<1>{}, GrpTag<2>{}, GrpTag<0>{});
+            piece(st + 4, GrpTag<1>{});
+            fence();
+            mma(GrpTag<1>{}, GrpTag<3>{}, GrpTag<0>{});
+            piece(st + 4, GrpTag<2>{});
+            fence();
+        } else {
+            static_for<3>([&](auto i) { mma(GrpTag<1>{}, GrpTag<decltype(i)::value + 1>{}, GrpTag<0>{}); });
+        }
+    };
+    // the copies before a tile's first stage: the ring's four stages
     auto prologue = [&]() {
-#pragma unroll
-        for (int st = 0; st < 3; ++st) {
-            copy(st, 0);
-            copy(st, 1);
-        }
-        copy(3, 0);
+        for (int st = 0; st < I8_SLOTS; ++st) static_for<8>([&](auto i) { piece(st, i); });
     };
 
-    int t = slot;
+    int t = slot, stores = 0;
     if (t < n_tiles) {
         setup(t);
         prologue();
     }
     while (t < n_tiles) {
-        wait_vmcnt<20>();        // stage 0; whatever was issued after it may be under way
+        wait_after(8 * min(nstages - 1, 2) + stores);        // stage 0 (of the two after it at most)
         block_barrier();
-        read(0, GrpTag<0>{});
-        stage(0, GrpTag<1>{});
-        for (int st = 1; st < nstages - 1; ++st) stage(st, GrpTag<0>{});
+        read_w(0, GrpTag<0>{});
+        read_t(0, GrpTag<0>{});
+        stage(0, stores, GrpTag<1>{}, GrpTag<0>{});
+        for (int st = 1; st < nstages - 1; ++st) stage(st, stores, GrpTag<0>{}, GrpTag<0>{});
         // the scales of this tile, loaded during its last stage (nstages is even): lane holds, of
         // block (i, j), row 32 i + (lane & 31) and columns 32 j + 8 q + 4 (lane >> 5) .. + 3
         const int prow0 = row0, prows = rows, gc0 = col0 + 128 * wc;
-        const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
         float sr[4];
-        f32x4 cs[4][4];
+        f32x4 cs[SCALED ? 4 : 1][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sr[i] = p.s[row0 + min(128 * wr + 32 * i + (lane & 31), rows - 1)];
-        if (ws) {
+        if constexpr (SCALED) {
+            const float* ws = p.ws + static_cast<int64_t>(e) * p.ws_ld;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     cs[j][q] = *reinterpret_cast<const f32x4*>(ws + min(gc0 + 32 * j + 8 * q + 4 * (lane >> 5), p.N - 4));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) cs[j][q] = f32x4{1.f, 1.f, 1.f, 1.f};
         }
-        stage(nstages - 1, GrpTag<0>{});
+        stage(nstages - 1, stores, GrpTag<0>{}, GrpTag<1>{});
         t += G;
-        wait_vmcnt<0>();         // the scales, and the copies past the end
+        wait_vmcnt<0>();         // the scales
         // held from here on, so that nothing waits for them behind the next tile's copies
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             asm volatile("" : "+v"(sr[i]));
+            if constexpr (SCALED) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(cs[i][q]));
+                for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(cs[i][q]));
+            }
         }
         block_barrier();         // and every wave is done with the ring
         if (t < n_tiles) {
             setup(t);
             prologue();
         }
+        // All 32 stores of a wave are issued where the tile is full; a store whose lanes all lie outside may be
+        // skipped, so a partial tile counts as none.
+        stores = prows == I8_TILE && gc0 - 128 * wc + I8_TILE <= p.N ? 32 : 0;
         mfma_drain();
         int opaque = 0;
         asm volatile("" : "+s"(opaque));
         const int ln = lane + opaque;
         uint16_t* stg = reinterpret_cast<uint16_t*>(s_stg + wave * I8_STG_BYTES) + opaque;
+        // Eight blocks of 32 rows x 64 columns go through the staging area, [32 rows][64 columns] with 16-byte
+        // chunk c of row r at c ^ (r & 7); the arithmetic of a block covers the LDS round trip of the last.
+        auto scaled = [&](auto b_tag, uint2 (&v)[8]) {
+            constexpr int i = decltype(b_tag)::value & 3, jh = decltype(b_tag)::value >> 2;
 #pragma unroll
-        for (int jh = 0; jh < 2; ++jh)
+            for (int c = 0; c < 8; ++c) {
+                const int j = 2 * jh + (c >> 2), q = c & 3;
+                const i32x16& a = acc[i][j];
+                float y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // [32 rows][64 columns] (128-byte rows); 16-byte chunk c of row r at c ^ (r & 7)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const i32x16& a = acc[i][2 * jh + j];
-                        const float y0 = static_cast<float>(acc_rd_i(a[4 * q])) * sr[i] * cs[2 * jh + j][q][0];
-                        const float y1 = static_cast<float>(acc_rd_i(a[4 * q + 1])) * sr[i] * cs[2 * jh + j][q][1];
-                        const float y2 = static_cast<float>(acc_rd_i(a[4 * q + 2])) * sr[i] * cs[2 * jh + j][q][2];
-                        const float y3 = static_cast<float>(acc_rd_i(a[4 * q + 3])) * sr[i] * cs[2 * jh + j][q][3];
-                        const int rr = ln & 31, c = 4 * j + q;
-                        *reinterpret_cast<uint2*>(stg + rr * 64 + ((c ^ (rr & 7)) << 3) + 4 * (ln >> 5)) =
-                            make_uint2(pack2(y0, y1), pack2(y2, y3));
-                    }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int rr = 8 * k + (ln >> 3), c = (ln & 7) ^ (rr & 7);
-                    const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 64 + (ln & 7) * 8);
-                    const int gr = 128 * wr + 32 * i + rr, gc = gc0 + 64 * jh + 8 * c;
-                    if (gr < prows && gc < p.N)
-                        *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(prow0 + gr) * p.N + gc) = v;
+                for (int x = 0; x < 4; ++x) {
+                    y[x] = static_cast<float>(acc_rd_i(a[4 * q + x])) * sr[i];
+                    if constexpr (SCALED) y[x] *= cs[j][q][x];
                 }
+                v[c] = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
             }
+        };
+        auto put = [&](const uint2 (&v)[8]) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int rr = ln & 31;
+                *reinterpret_cast<uint2*>(stg + rr * 64 + ((c ^ (rr & 7)) << 3) + 4 * (ln >> 5)) = v[c];
+            }
+        };
+        uint2 vals[8];
+        scaled(GrpTag<0>{}, vals);
+        put(vals);
+        static_for<8>([&](auto b_tag) {
+            constexpr int b = decltype(b_tag)::value, i = b & 3, jh = b >> 2;
+            if constexpr (b < 7) scaled(GrpTag<b + 1>{}, vals);
+            uint4 out[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                out[k] = *reinterpret_cast<const uint4*>(stg + (8 * k + (ln >> 3)) * 64 + (ln & 7) * 8);
+            if constexpr (b < 7) put(vals);
+            // lane: row 8 k + (ln >> 3), 16-byte chunk (ln & 7) ^ (ln >> 3)
+            const int gc = gc0 + 64 * jh + 8 * ((ln & 7) ^ (ln >> 3)), gr = 128 * wr + 32 * i + (ln >> 3);
+            uint16_t* to = p.out + static_cast<int64_t>(prow0 + gr) * p.N + gc;
+            if (stores) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) st16_nt(to + static_cast<int64_t>(8 * k) * p.N, out[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (gr + 8 * k < prows && gc < p.N) st16_nt(to + static_cast<int64_t>(8 * k) * p.N, out[k]);
+            }
+        });
     }
 }
 
@@ -615,7 +669,9 @@ hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
     const int64_t few = p.M < p.E ? p.M : p.E;
     if (g.tiles) {
         const int64_t upper = (static_cast<int64_t>(p.M) / I8_TILE + few) * ((p.N + I8_TILE - 1) / I8_TILE);
-        hipLaunchKernelGGL(int8_tile_kernel, dim3(static_cast<unsigned>(upper < num_cu ? upper : num_cu)), dim3(256), 0, s, g);
+        const dim3 grid(static_cast<unsigned>(upper < num_cu ? upper : num_cu));
+        if (p.ws) hipLaunchKernelGGL((int8_tile_kernel<true>), grid, dim3(256), 0, s, g);
+        else hipLaunchKernelGGL((int8_tile_kernel<false>), grid, dim3(256), 0, s, g);
         const hipError_t st = hipGetLastError();
         if (st != hipSuccess) return st;
     }
