@@ -50,7 +50,7 @@ struct Int8Params {
     int ldq;
     int M, E, N;             // N: output columns, a multiple of 8
     uint16_t* out;           // [M][N]
-    int tiles;               // whether large experts run as tiles (set by the launcher)
+    int tile;                // rows of a tile, or 0: no tiles (set by the launcher)
 };
 
 hipError_t launch_quant_rows(QuantMode mode, const QuantParams& p, int num_cu, hipStream_t s);

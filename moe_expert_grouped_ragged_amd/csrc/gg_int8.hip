@@ -247,22 +247,24 @@ __global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __re
 
 // ---------------------------------------------------------------- product
 //
-// The sums are exact in 32-bit integers, so the two kernels below give the
-// same bits.  Rows that fill 256-row tiles (the last may be partial) run as
-// 256 x 256 tiles; at most 96 rows of an expert (all of a small one) run as
-// streaming items, which read each weight byte once for all of them.
+// The sums are exact in 32-bit integers, so the kernels below give the same
+// bits.  The rows of a large expert run as tiles (the last may be partial);
+// a remainder of few rows (all rows of a small expert) runs as streaming
+// items, which read each weight byte once for all of them.
 //
 // Streaming items: up to 96 rows of one expert x 128 output columns; each of
 // the four waves owns one 32-column block over the whole summed dimension, its
 // weights one coalesced 1 KiB load a step and the token operands loaded
 // straight from the quantized rows.
 constexpr int I8_GROUP = 96;
-constexpr int I8_TILE = 256;
 
 __device__ __forceinline__ int i8_groups(int m) { return (m + I8_GROUP - 1) / I8_GROUP; }
-// Rows of an expert that tiles cover.
-__device__ __forceinline__ int i8_tile_rows(int m) {
-    const int tail = m % I8_TILE;
+// Rows of an expert that tiles of `tile` rows cover (0: there are no tiles).  256-row tiles leave a remainder
+// of at most 96 rows; 128-row tiles, which run where there is little work, take all of an expert or nothing.
+__device__ __forceinline__ int i8_tile_rows(int m, int tile) {
+    if (tile == 0) return 0;
+    if (tile == 128) return m <= 64 ? 0 : m;
+    const int tail = m % tile;
     return tail <= I8_GROUP ? m - tail : m;
 }
 
@@ -286,7 +288,7 @@ __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t
 #pragma unroll
         for (int u = 0; u < G; ++u) {
             const int st = min(g + u, nsteps - 1);
-            wv[buf][u] = *reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024);
+            wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024));
 #pragma unroll
             for (int i = 0; i < TB; ++i) tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + st * 32);
         }
@@ -339,7 +341,7 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
     const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32;
     const int items_n = (nblocks + 3) / 4;
-    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(p.tiles ? m - i8_tile_rows(m) : m) * items_n; });
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(m - i8_tile_rows(m, p.tile)) * items_n; });
     const int total = uni(s_pre[p.E]);
     const int wave = uni(threadIdx.x >> 6);
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
@@ -347,7 +349,7 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
         const int local = it - uni(s_pre[e]);
         const int grp = local / items_n, col = local - grp * items_n;
         const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
-        const int row0 = lo + (p.tiles ? i8_tile_rows(hi - lo) : 0) + grp * I8_GROUP;
+        const int row0 = lo + i8_tile_rows(hi - lo, p.tile) + grp * I8_GROUP;
         const int rows = min(I8_GROUP, hi - row0);
         const int8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
         const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
@@ -358,21 +360,25 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
     }
 }
 
-// Tiles: 256 rows x 256 output columns by four waves, each 128 x 128 (4 x 4
-// accumulators of 32 x 32).  Rows and weights stream into a 4-slot LDS ring of
-// 64-byte stages by LDS-DMA, up to four stages ahead: 16 KiB of rows, 16-byte
-// chunk c of row r at c ^ ((r >> 2) & 3), and 16 KiB of weights as they lie in
+// Tiles: 64 B rows x 64 B output columns by four waves, each 32 B x 32 B, as
+// B x B accumulators of 32 x 32.  B = 4 (256 x 256) fills the accumulation
+// registers; B = 2 (128 x 128) gives four times the tiles where there would
+// be fewer large ones than CUs (777 rows, K 1048, N 2056: 20 us with B = 4,
+// see launch_int8_gemm).
+// Rows and weights stream into an LDS ring (128 KiB: four stages, or eight)
+// of 64-byte stages by LDS-DMA, all but one of them ahead: the rows, 16-byte
+// chunk c of row r at c ^ ((r >> 2) & 3), and the weights as they lie in
 // the packed layout; fragment reads of both are free of bank conflicts.  Each
-// of a stage's two 32-byte steps is 16 matrix instructions a wave, while the
-// next step's eight fragments are read; the only barrier of a stage sits
+// of a stage's two 32-byte steps is B x B matrix instructions a wave, while the
+// next step's 2 B fragments are read; the only barrier of a stage sits
 // in its second step, where the next stage has landed and every wave has
 // read the last fragments of this one, whose slot is refilled from there on.
 // The epilogue scales and rounds through a small staging area of its own, so
-// the next tile's first four stages are already on their way, and the waits of
+// the next tile's first stages are already on their way, and the waits of
 // those stages leave the epilogue's stores outstanding: memory operations
 // complete in order, and the stores were issued after the copies.
-constexpr int I8_STAGE = 64, I8_SLOTS = 4;
-constexpr int I8_SLOT_BYTES = 2 * I8_TILE * I8_STAGE;
+constexpr int I8_STAGE = 64;
+constexpr int I8_RING = 128 * 1024;
 constexpr int I8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf16
 
 __device__ __forceinline__ int acc_rd_i(int a) {
@@ -381,19 +387,22 @@ __device__ __forceinline__ int acc_rd_i(int a) {
     return v;
 }
 
-template <bool SCALED>   // whether the output columns have scales
+template <int B, bool SCALED>   // SCALED: the output columns have scales
 __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
-    __shared__ __attribute__((aligned(1024))) int8_t s_ring[I8_SLOTS * I8_SLOT_BYTES];
+    constexpr int TILE = 64 * B;                            // rows, and columns
+    constexpr int SLOT_BYTES = 2 * TILE * I8_STAGE, SLOTS = I8_RING / SLOT_BYTES;
+    constexpr int P = 2 * B;                                // copies a wave issues for a stage
+    __shared__ __attribute__((aligned(1024))) int8_t s_ring[I8_RING];
     __shared__ __attribute__((aligned(16))) int8_t s_stg[4 * I8_STG_BYTES];
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
     const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32, nstages = p.ldq / I8_STAGE;
-    const int tiles_n = (p.N + I8_TILE - 1) / I8_TILE;
+    const int tiles_n = (p.N + TILE - 1) / TILE;
     prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
-                   [&](int m) { return (i8_tile_rows(m) + I8_TILE - 1) / I8_TILE * tiles_n; });
+                   [&](int m) { return (i8_tile_rows(m, TILE) + TILE - 1) / TILE * tiles_n; });
     const int n_tiles = uni(s_pre[p.E]);
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-    const int wr = wave >> 1, wc = wave & 1;      // the wave's 128 rows and 128 columns
+    const int wr = wave >> 1, wc = wave & 1;      // the wave's rows and columns
     // consecutive tiles to the workgroups of one XCD, which share an L2
     const int G = gridDim.x, b = blockIdx.x;
     const int slot = (G % 8 == 0) ? (b & 7) * (G >> 3) + (b >> 3) : b;
@@ -402,65 +411,65 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
     // what the copies of one tile read
     const int8_t* t_base = nullptr;   // its first row
     const int8_t* w_base = nullptr;   // its expert's matrix
-    uint32_t t_voff[4];               // this lane's chunks of rows 64 wave + 16 i ..
-    int wb[2];                        // this wave's two 32-column blocks
+    uint32_t t_voff[B];               // this lane's chunks of rows 16 B wave + 16 i ..
+    int wb[B / 2];                    // this wave's 32-column blocks
     int e = 0, row0 = 0, rows = 0, col0 = 0;
     auto setup = [&](int t) {
         e = uni(find_expert_wave(s_pre, p.E, t));
         const int local = t - uni(s_pre[e]);
-        const int lo = uni(s_off[e]), m = i8_tile_rows(uni(s_off[e + 1]) - lo);
-        const int tiles_m = (m + I8_TILE - 1) / I8_TILE;
+        const int lo = uni(s_off[e]), m = i8_tile_rows(uni(s_off[e + 1]) - lo, TILE);
+        const int tiles_m = (m + TILE - 1) / TILE;
         const int tm = local % tiles_m, tn = local / tiles_m;
-        row0 = lo + tm * I8_TILE;
-        rows = min(I8_TILE, m - tm * I8_TILE);
-        col0 = tn * I8_TILE;
+        row0 = lo + tm * TILE;
+        rows = min(TILE, m - tm * TILE);
+        col0 = tn * TILE;
         t_base = p.q + static_cast<int64_t>(row0) * p.ldq;
         w_base = p.w + static_cast<int64_t>(e) * p.w_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 64 * wave + 16 * i + (lane >> 2);
+        for (int i = 0; i < B; ++i) {
+            const int r = 16 * B * wave + 16 * i + (lane >> 2);
             const int c = (lane & 3) ^ ((r >> 2) & 3);
             t_voff[i] = static_cast<uint32_t>(min(r, rows - 1)) * p.ldq + 16 * c;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wb[i] = min(col0 / 32 + 2 * wave + i, nblocks - 1);
+        for (int i = 0; i < B / 2; ++i) wb[i] = min(col0 / 32 + B / 2 * wave + i, nblocks - 1);
     };
-    // One of the eight copies of a stage that this wave issues (nothing past the last stage).
+    // One of the P copies of a stage that this wave issues (nothing past the last stage).
     auto piece = [&](int st, auto i_tag) {
         constexpr int i = decltype(i_tag)::value;
         if (st >= nstages) return;
-        const uint32_t dst = ring + (st & 3) * I8_SLOT_BYTES;
-        if constexpr (i < 4) {
-            dma16(t_base + st * I8_STAGE, t_voff[i], dst + (64 * wave + 16 * i) * I8_STAGE);
+        const uint32_t dst = ring + (st & (SLOTS - 1)) * SLOT_BYTES;
+        if constexpr (i < B) {
+            dma16(t_base + st * I8_STAGE, t_voff[i], dst + (16 * B * wave + 16 * i) * I8_STAGE);
         } else {
-            constexpr int h = (i - 4) >> 1, u = i & 1;
+            constexpr int h = (i - B) >> 1, u = i & 1;
             dma16(w_base + (static_cast<int64_t>(wb[h]) * nsteps + 2 * st + u) * 1024, lane * 16,
-                  dst + I8_TILE * I8_STAGE + ((2 * wave + h) * 2 + u) * 1024);
+                  dst + TILE * I8_STAGE + ((B / 2 * wave + h) * 2 + u) * 1024);
         }
     };
 
-    i32x16 acc[4][4];    // [row block][column block]
-    i32x4 tf[2][4], wf[2][4];
+    i32x16 acc[B][B];    // [row block][column block]
+    i32x4 tf[2][B], wf[2][B];
     auto read_t = [&](int st, auto u_tag) {
         constexpr int u = decltype(u_tag)::value;
-        const int8_t* sl = s_ring + (st & 3) * I8_SLOT_BYTES;
+        const int8_t* sl = s_ring + (st & (SLOTS - 1)) * SLOT_BYTES;
         const int c = (2 * u + (lane >> 5)) ^ ((lane >> 2) & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            tf[u][i] = *reinterpret_cast<const i32x4*>(sl + (128 * wr + 32 * i + (lane & 31)) * I8_STAGE + 16 * c);
+        for (int i = 0; i < B; ++i)
+            tf[u][i] = *reinterpret_cast<const i32x4*>(sl + (32 * B * wr + 32 * i + (lane & 31)) * I8_STAGE + 16 * c);
     };
     auto read_w = [&](int st, auto u_tag) {
         constexpr int u = decltype(u_tag)::value;
-        const int8_t* sl = s_ring + (st & 3) * I8_SLOT_BYTES;
+        const int8_t* sl = s_ring + (st & (SLOTS - 1)) * SLOT_BYTES;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            wf[u][j] = *reinterpret_cast<const i32x4*>(sl + I8_TILE * I8_STAGE + ((4 * wc + j) * 2 + u) * 1024 + lane * 16);
+        for (int j = 0; j < B; ++j)
+            wf[u][j] = *reinterpret_cast<const i32x4*>(sl + TILE * I8_STAGE + ((B * wc + j) * 2 + u) * 1024 + lane * 16);
     };
-    // the four matrix instructions of row block i in step u; the tile's first step starts its sums from zero
+    // the B matrix instructions of row block i in step u; the tile's first step starts its sums from zero
     auto mma = [&](auto u_tag, auto i_tag, auto first_tag) {
         constexpr int u = decltype(u_tag)::value, i = decltype(i_tag)::value;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < B; ++j) {
             if constexpr (decltype(first_tag)::value != 0)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][j], tf[u][i], i32x16{}, 0, 0, 0);
             else
@@ -470,59 +479,57 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
     auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
     // Waits until at most n copies and stores issued after those of the stage that is needed are outstanding.
     auto wait_after = [&](int n) {
-        if (n >= 48) wait_vmcnt<48>();
-        else if (n >= 40) wait_vmcnt<40>();
-        else if (n >= 32) wait_vmcnt<32>();
+        if (n >= 60) wait_vmcnt<60>();
+        else if (n >= 52) wait_vmcnt<52>();
+        else if (n >= 44) wait_vmcnt<44>();
+        else if (n >= 36) wait_vmcnt<36>();
+        else if (n >= 28) wait_vmcnt<28>();
+        else if (n >= 24) wait_vmcnt<24>();
+        else if (n >= 20) wait_vmcnt<20>();
         else if (n >= 16) wait_vmcnt<16>();
+        else if (n >= 12) wait_vmcnt<12>();
         else if (n >= 8) wait_vmcnt<8>();
+        else if (n >= 4) wait_vmcnt<4>();
         else wait_vmcnt<0>();
     };
-    // Stage st: two steps of four groups of four matrix instructions, each
-    // group followed by one copy; the next step's fragments are read during
-    // the first groups of a step.  stores: what the last tile's epilogue
-    // issued behind the copies of stages 0 .. 3, at least.
-    auto stage = [&](int st, int stores, auto first_tag, auto last_tag) {
-        const int c3 = decltype(first_tag)::value != 0 ? nstages : st + 3;    // the prologue brought stage 3
-        read_w(st, GrpTag<1>{});
-        mma(GrpTag<0>{}, GrpTag<0>{}, first_tag);
-        piece(c3, GrpTag<3>{});
-        fence();
-        read_t(st, GrpTag<1>{});
-        mma(GrpTag<0>{}, GrpTag<1>{}, first_tag);
-        piece(c3, GrpTag<4>{});
-        fence();
-        mma(GrpTag<0>{}, GrpTag<2>{}, first_tag);
-        piece(c3, GrpTag<5>{});
-        fence();
-        mma(GrpTag<0>{}, GrpTag<3>{}, first_tag);
-        piece(c3, GrpTag<6>{});
-        fence();
+    // Stage st: two steps of B groups of B matrix instructions, each group
+    // followed by one copy; the next step's fragments are read during the
+    // first groups of a step.  behind: the stores and loads issued behind the
+    // copies of the prologue's stages, at least.
+    auto stage = [&](int st, int behind, auto first_tag, auto last_tag) {
+        const int c1 = decltype(first_tag)::value != 0 ? nstages : st + SLOTS - 1;    // the prologue brought that stage
+        static_for<B>([&](auto it) {
+            constexpr int i = decltype(it)::value;
+            if constexpr (i == 0) read_w(st, GrpTag<1>{});
+            if constexpr (i == 1) read_t(st, GrpTag<1>{});
+            mma(GrpTag<0>{}, it, first_tag);
+            piece(c1, GrpTag<B - 1 + i>{});
+            fence();
+        });
         mma(GrpTag<1>{}, GrpTag<0>{}, GrpTag<0>{});
-        piece(c3, GrpTag<7>{});
+        piece(c1, GrpTag<P - 1>{});
         fence();
         if constexpr (decltype(last_tag)::value == 0) {
             // stage st + 1 has landed, and every wave holds its last fragments of stage st, whose slot
             // is refilled from here on
-            wait_after(8 * min(nstages - 2 - st, 2) + (st < 3 ? stores : 0));
+            wait_after(P * min(nstages - 2 - st, SLOTS - 2) + (st < SLOTS - 1 ? behind : 0));
             block_barrier();
-            read_w(st + 1, GrpTag<0>{});
-            mma(GrpTag<1>{}, GrpTag<1>{}, GrpTag<0>{});
-            piece(st + 4, GrpTag<0>{});
-            fence();
-            read_t(st + 1, GrpTag<0>{});
-            mma(GrpTag<1>{}, GrpTag<2>{}, GrpTag<0>{});
-            piece(st + 4, GrpTag<1>{});
-            fence();
-            mma(GrpTag<1>{}, GrpTag<3>{}, GrpTag<0>{});
-            piece(st + 4, GrpTag<2>{});
-            fence();
-        } else {
-            static_for<3>([&](auto i) { mma(GrpTag<1>{}, GrpTag<decltype(i)::value + 1>{}, GrpTag<0>{}); });
         }
+        static_for<B - 1>([&](auto it) {
+            constexpr int i = decltype(it)::value;
+            if constexpr (decltype(last_tag)::value == 0) {
+                if constexpr (i == 0) read_w(st + 1, GrpTag<0>{});
+                if constexpr (i == (B > 2 ? 1 : 0)) read_t(st + 1, GrpTag<0>{});
+            }
+            mma(GrpTag<1>{}, GrpTag<i + 1>{}, GrpTag<0>{});
+            if constexpr (decltype(last_tag)::value == 0) piece(st + SLOTS, it);
+            fence();
+        });
     };
-    // the copies before a tile's first stage: the ring's four stages
+    constexpr int SCALE_LOADS = SCALED ? B + 4 * B : B;
+    // the copies before a tile's first stage: the whole ring's
     auto prologue = [&]() {
-        for (int st = 0; st < I8_SLOTS; ++st) static_for<8>([&](auto i) { piece(st, i); });
+        for (int st = 0; st < SLOTS; ++st) static_for<P>([&](auto i) { piece(st, i); });
     };
 
     int t = slot, stores = 0;
@@ -531,33 +538,34 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
         prologue();
     }
     while (t < n_tiles) {
-        wait_after(8 * min(nstages - 1, 2) + stores);        // stage 0 (of the two after it at most)
+        wait_after(P * min(nstages - 1, SLOTS - 1) + stores);        // stage 0
         block_barrier();
-        read_w(0, GrpTag<0>{});
-        read_t(0, GrpTag<0>{});
-        stage(0, stores, GrpTag<1>{}, GrpTag<0>{});
-        for (int st = 1; st < nstages - 1; ++st) stage(st, stores, GrpTag<0>{}, GrpTag<0>{});
-        // the scales of this tile, loaded during its last stage (nstages is even): lane holds, of
+        // the scales of this tile, for its epilogue: lane holds, of
         // block (i, j), row 32 i + (lane & 31) and columns 32 j + 8 q + 4 (lane >> 5) .. + 3
-        const int prow0 = row0, prows = rows, gc0 = col0 + 128 * wc;
-        float sr[4];
-        f32x4 cs[SCALED ? 4 : 1][4];
+        const int prow0 = row0, prows = rows, gc0 = col0 + 32 * B * wc;
+        float sr[B];
+        f32x4 cs[SCALED ? B : 1][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sr[i] = p.s[row0 + min(128 * wr + 32 * i + (lane & 31), rows - 1)];
+        for (int i = 0; i < B; ++i) sr[i] = p.s[row0 + min(32 * B * wr + 32 * i + (lane & 31), rows - 1)];
         if constexpr (SCALED) {
             const float* ws = p.ws + static_cast<int64_t>(e) * p.ws_ld;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < B; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     cs[j][q] = *reinterpret_cast<const f32x4*>(ws + min(gc0 + 32 * j + 8 * q + 4 * (lane >> 5), p.N - 4));
         }
-        stage(nstages - 1, stores, GrpTag<0>{}, GrpTag<1>{});
+        const int behind = stores + SCALE_LOADS;
+        read_w(0, GrpTag<0>{});
+        read_t(0, GrpTag<0>{});
+        stage(0, behind, GrpTag<1>{}, GrpTag<0>{});
+        for (int st = 1; st < nstages - 1; ++st) stage(st, behind, GrpTag<0>{}, GrpTag<0>{});
+        stage(nstages - 1, behind, GrpTag<0>{}, GrpTag<1>{});
         t += G;
         wait_vmcnt<0>();         // the scales
         // held from here on, so that nothing waits for them behind the next tile's copies
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < B; ++i) {
             asm volatile("" : "+v"(sr[i]));
             if constexpr (SCALED) {
 #pragma unroll
@@ -569,18 +577,18 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
             setup(t);
             prologue();
         }
-        // All 32 stores of a wave are issued where the tile is full; a store whose lanes all lie outside may be
+        // All stores of a wave are issued where the tile is full; a store whose lanes all lie outside may be
         // skipped, so a partial tile counts as none.
-        stores = prows == I8_TILE && gc0 - 128 * wc + I8_TILE <= p.N ? 32 : 0;
+        stores = prows == TILE && gc0 - 32 * B * wc + TILE <= p.N ? 2 * B * B : 0;
         mfma_drain();
         int opaque = 0;
         asm volatile("" : "+s"(opaque));
         const int ln = lane + opaque;
         uint16_t* stg = reinterpret_cast<uint16_t*>(s_stg + wave * I8_STG_BYTES) + opaque;
-        // Eight blocks of 32 rows x 64 columns go through the staging area, [32 rows][64 columns] with 16-byte
+        // B * B / 2 blocks of 32 rows x 64 columns go through the staging area, [32 rows][64 columns] with 16-byte
         // chunk c of row r at c ^ (r & 7); the arithmetic of a block covers the LDS round trip of the last.
         auto scaled = [&](auto b_tag, uint2 (&v)[8]) {
-            constexpr int i = decltype(b_tag)::value & 3, jh = decltype(b_tag)::value >> 2;
+            constexpr int i = decltype(b_tag)::value % B, jh = decltype(b_tag)::value / B;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const int j = 2 * jh + (c >> 2), q = c & 3;
@@ -604,16 +612,16 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
         uint2 vals[8];
         scaled(GrpTag<0>{}, vals);
         put(vals);
-        static_for<8>([&](auto b_tag) {
-            constexpr int b = decltype(b_tag)::value, i = b & 3, jh = b >> 2;
-            if constexpr (b < 7) scaled(GrpTag<b + 1>{}, vals);
+        static_for<B * B / 2>([&](auto b_tag) {
+            constexpr int b = decltype(b_tag)::value, i = b % B, jh = b / B;
+            if constexpr (b < B * B / 2 - 1) scaled(GrpTag<b + 1>{}, vals);
             uint4 out[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 out[k] = *reinterpret_cast<const uint4*>(stg + (8 * k + (ln >> 3)) * 64 + (ln & 7) * 8);
-            if constexpr (b < 7) put(vals);
+            if constexpr (b < B * B / 2 - 1) put(vals);
             // lane: row 8 k + (ln >> 3), 16-byte chunk (ln & 7) ^ (ln >> 3)
-            const int gc = gc0 + 64 * jh + 8 * ((ln & 7) ^ (ln >> 3)), gr = 128 * wr + 32 * i + (ln >> 3);
+            const int gc = gc0 + 64 * jh + 8 * ((ln & 7) ^ (ln >> 3)), gr = 32 * B * wr + 32 * i + (ln >> 3);
             uint16_t* to = p.out + static_cast<int64_t>(prow0 + gr) * p.N + gc;
             if (stores) {
 #pragma unroll
@@ -662,20 +670,26 @@ hipError_t launch_int8_pack(const int8_t* q, const float* s, int E, int N, int K
     return hipGetLastError();
 }
 
+template <int B>
+static hipError_t launch_tiles(const Int8Params& p, int num_cu, hipStream_t s) {
+    constexpr int TILE = 64 * B;
+    const int64_t upper = (static_cast<int64_t>(p.M) / TILE + (p.M < p.E ? p.M : p.E)) * ((p.N + TILE - 1) / TILE);
+    const dim3 grid(static_cast<unsigned>(upper < num_cu ? upper : num_cu));
+    if (p.ws) hipLaunchKernelGGL((int8_tile_kernel<B, true>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((int8_tile_kernel<B, false>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
 hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
-    // No expert of a batch of at most 96 rows has a tile.
     Int8Params g = p;
-    g.tiles = p.M > I8_GROUP;
-    const int64_t few = p.M < p.E ? p.M : p.E;
-    if (g.tiles) {
-        const int64_t upper = (static_cast<int64_t>(p.M) / I8_TILE + few) * ((p.N + I8_TILE - 1) / I8_TILE);
-        const dim3 grid(static_cast<unsigned>(upper < num_cu ? upper : num_cu));
-        if (p.ws) hipLaunchKernelGGL((int8_tile_kernel<true>), grid, dim3(256), 0, s, g);
-        else hipLaunchKernelGGL((int8_tile_kernel<false>), grid, dim3(256), 0, s, g);
-        const hipError_t st = hipGetLastError();
+    // No expert of a batch of few rows has a tile.  Small tiles where the rows would make fewer large ones than CUs.
+    const int64_t large = static_cast<int64_t>(p.M) / 256 * ((p.N + 255) / 256);
+    g.tile = p.M <= 64 ? 0 : (large < num_cu ? 128 : 256);
+    if (g.tile) {
+        const hipError_t st = g.tile == 256 ? launch_tiles<4>(g, num_cu, s) : launch_tiles<2>(g, num_cu, s);
         if (st != hipSuccess) return st;
     }
-    const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + few) * ((p.N + 127) / 128);
+    const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E)) * ((p.N + 127) / 128);
     const int64_t most = static_cast<int64_t>(num_cu) * 2;
     hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
     return hipGetLastError();
