@@ -33,21 +33,23 @@ struct QuantParams {
     int M, E, K;             // K: values of a quantized row
     float slope;
     uint16_t* v_out;         // Q_GLU: A [M][K], Q_DGLU: dH1 [M][K]; null: not kept
-    int8_t* q;               // [M][ldq], columns K .. ldq-1 zero
-    int ldq;
+    int8_t* q;               // column c of row r at (c / 64) * q_block + r * q_row + c % 64
+    int64_t q_block, q_row;  // (64, K): rows as they are; (64 M, 64): blocks of 64 columns, for the product
+    int blocked;             // the latter
+    int width;               // columns written: K, or K padded with zeros
     float* s;                // [M]
 };
 
 // out[r][n] = bf16(s[r] * ws_e[n] * sum_k q[r][k] W_e[n][k])
 struct Int8Params {
-    const int8_t* q;         // [M][ldq]
+    const int8_t* q;         // [width / 64][M][64]
     const float* s;          // [M]
     const int64_t* offsets;  // [E+1]
     const int8_t* w;         // packed matrices
     int64_t w_stride;        // bytes of one expert's matrix
     const float* ws;         // [E][ws_ld] output column scales, or null (all one)
     int ws_ld;
-    int ldq;
+    int width;               // summed dimension, padded (a multiple of 128)
     int M, E, N;             // N: output columns, a multiple of 8
     uint16_t* out;           // [M][N]
     int tile;                // rows of a tile, or 0: no tiles (set by the launcher)

@@ -25,28 +25,28 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 // one are scaled by a power of two first, so 1/top neither overflows nor
 // loses bits.
 //
-// One wavefront per row; its values stay in registers between the maximum
-// and the rounding (rows of more than NC * 64 units compute them twice).
+// A wavefront takes a row at a time; its bf16 values stay in registers between
+// the maximum and the rounding (rows of more than NC * 64 units are computed
+// twice).  For large batches of the light modes it takes two neighbouring
+// rows: pairs of lanes then exchange halves, so that a store is 16 bytes a
+// lane and whole 128-byte lines of the two rows in the product's layout (262144 x
+// 4096, 3.2 GB: 560 us, 760 us a row at a time; with a derivative or column
+// scales in front, and in small batches, the second row costs more than it gives: 32768 x
+// 1536 with the derivative 65 us, 105 us in pairs).
 template <int MODE>
 struct QuantUnit {
-    static constexpr int VALS = MODE == Q_DGLU ? 16 : 8;   // values a lane makes at a time
+    static constexpr int HALVES = MODE == Q_DGLU ? 2 : 1;   // groups of 8 values a lane makes at a time
 };
 
+// The bf16 values of unit c of row r (groups of 8: x, A, or dH1's gate and up parts), and their copy to v_out.
 template <int MODE>
-__device__ __forceinline__ void quant_unit(const QuantParams& p, int64_t r, const float* cs, int c, float* v,
-                                           bool store) {
+__device__ __forceinline__ void quant_unit(const QuantParams& p, int64_t r, int c, bool store,
+                                           uint4 (&w)[QuantUnit<MODE>::HALVES]) {
     if constexpr (MODE == Q_PLAIN || MODE == Q_SCALED) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p.x + r * p.K + c * 8);
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = lo_f(xw[i]);
-            v[2 * i + 1] = hi_f(xw[i]);
-        }
+        w[0] = ld16_nt(p.x + r * p.K + c * 8);
     } else if constexpr (MODE == Q_GLU) {
         const uint16_t* row = p.x + r * 2 * p.K + c * 8;
-        const uint4 g4 = *reinterpret_cast<const uint4*>(row);
-        const uint4 u4 = *reinterpret_cast<const uint4*>(row + p.K);
+        const uint4 g4 = ld16_nt(row), u4 = ld16_nt(row + p.K);
         const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
         uint32_t aw[4];
 #pragma unroll
@@ -60,16 +60,13 @@ __device__ __forceinline__ void quant_unit(const QuantParams& p, int64_t r, cons
                 a[y] = sg * u;
             }
             aw[i] = pack2(a[0], a[1]);
-            v[2 * i] = lo_f(aw[i]);
-            v[2 * i + 1] = hi_f(aw[i]);
         }
-        if (store) *reinterpret_cast<uint4*>(p.v_out + r * p.K + c * 8) = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+        w[0] = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+        if (store) *reinterpret_cast<uint4*>(p.v_out + r * p.K + c * 8) = w[0];
     } else {
         const int F = p.K / 2;
         const uint16_t* hrow = p.h1 + r * p.K + c * 8;
-        const uint4 g4 = *reinterpret_cast<const uint4*>(hrow);
-        const uint4 u4 = *reinterpret_cast<const uint4*>(hrow + F);
-        const uint4 d4 = *reinterpret_cast<const uint4*>(p.x + r * F + c * 8);
+        const uint4 g4 = ld16_nt(hrow), u4 = ld16_nt(hrow + F), d4 = ld16_nt(p.x + r * F + c * 8);
         const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
         const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
         uint32_t og[4], ou[4];
@@ -87,28 +84,27 @@ __device__ __forceinline__ void quant_unit(const QuantParams& p, int64_t r, cons
             }
             og[i] = pack2(dg[0], dg[1]);
             ou[i] = pack2(du[0], du[1]);
-            v[2 * i] = lo_f(og[i]);
-            v[2 * i + 1] = hi_f(og[i]);
-            v[8 + 2 * i] = lo_f(ou[i]);
-            v[8 + 2 * i + 1] = hi_f(ou[i]);
         }
+        w[0] = make_uint4(og[0], og[1], og[2], og[3]);
+        w[1] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
         if (store) {
             uint16_t* o = p.v_out + r * p.K + c * 8;
-            *reinterpret_cast<uint4*>(o) = make_uint4(og[0], og[1], og[2], og[3]);
-            *reinterpret_cast<uint4*>(o + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 c0 = *reinterpret_cast<const float4*>(cs + h * F + c * 8);
-            const float4 c1 = *reinterpret_cast<const float4*>(cs + h * F + c * 8 + 4);
-            const float cf[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[8 * h + i] *= cf[i];
+            *reinterpret_cast<uint4*>(o) = w[0];
+            *reinterpret_cast<uint4*>(o + F) = w[1];
         }
     }
-    if constexpr (MODE == Q_SCALED) {
-        const float4 c0 = *reinterpret_cast<const float4*>(cs + c * 8);
-        const float4 c1 = *reinterpret_cast<const float4*>(cs + c * 8 + 4);
+}
+
+// Eight bf16 values as floats, times their column scales (cs null: no scales).
+__device__ __forceinline__ void quant_vals(uint4 w, const float* cs, float (&v)[8]) {
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = lo_f(ww[i]);
+        v[2 * i + 1] = hi_f(ww[i]);
+    }
+    if (cs) {
+        const float4 c0 = *reinterpret_cast<const float4*>(cs), c1 = *reinterpret_cast<const float4*>(cs + 4);
         const float cf[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= cf[i];
@@ -118,22 +114,44 @@ __device__ __forceinline__ void quant_unit(const QuantParams& p, int64_t r, cons
 // Eight values to eight int8: t = v * c127 (127 times the row's power of two),
 // the corrected quotient t / top, then the sum with 1.5 * 2^23, whose rounding
 // is to the nearest even integer and whose low byte is that integer.
-__device__ __forceinline__ uint2 quant8(const float* v, float c127, float top, float inv) {
+struct QuantScale {
+    float c127, top, inv;
+    bool zero;   // a row of zeros, or one that is not finite
+};
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], const QuantScale& s) {
     uint32_t b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = v[i] * c127;
-        const float q0 = t * inv;
-        const float q = __builtin_fmaf(__builtin_fmaf(-q0, top, t), inv, q0);
-        b[i] = __builtin_bit_cast(uint32_t, q + 12582912.0f) & 0xffu;
+        const float t = v[i] * s.c127;
+        const float q0 = t * s.inv;
+        const float q = __builtin_fmaf(__builtin_fmaf(-q0, s.top, t), s.inv, q0);
+        b[i] = __builtin_bit_cast(uint32_t, q + 12582912.0f);
     }
-    return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
+    auto four = [](uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {   // the low bytes
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(x3, x2, 0x0c0c0400u), __builtin_amdgcn_perm(x1, x0, 0x0c0c0400u),
+                                     0x05040100u);
+    };
+    if (s.zero) return make_uint2(0, 0);
+    return make_uint2(four(b[0], b[1], b[2], b[3]), four(b[4], b[5], b[6], b[7]));
 }
 
-template <int MODE, int NC>   // NC = 0: any width, values computed twice
+// top: the largest |v| of the row as bits (a NaN is larger than infinity, which is larger than any number).
+__device__ __forceinline__ QuantScale quant_scale(uint32_t bits) {
+    QuantScale s;
+    const float top = __builtin_bit_cast(float, bits);
+    // a power of two that brings the row near one where it is far from it
+    const float pw = top < 0x1p-90f ? 0x1p64f : (top > 0x1p90f ? 0x1p-64f : 1.0f);
+    s.c127 = 127.0f * pw;
+    s.top = top * pw;
+    s.inv = 1.0f / s.top;
+    s.zero = bits == 0 || bits >= 0x7f800000u;
+    return s;
+}
+
+template <int MODE, int NC, int Y>   // NC = 0: any width, values computed twice; Y: rows a wave takes at a time
 __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
-    constexpr int VALS = QuantUnit<MODE>::VALS;
+    constexpr int HALVES = QuantUnit<MODE>::HALVES;
     constexpr bool SCALES = MODE == Q_SCALED || MODE == Q_DGLU;
     const int lane = threadIdx.x & 63;
     int lo = 0, hi = p.M;
@@ -147,65 +165,115 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
         lo = s_off[0];
         hi = s_off[p.E];
     }
-    const int units = p.K / VALS;
-    for (int64_t r = lo + static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6); r < hi;
-         r += static_cast<int64_t>(gridDim.x) * 4) {
-        const float* cs = nullptr;
-        if constexpr (SCALES)
-            cs = p.cs + static_cast<int64_t>(uni(find_expert(s_off, p.E, static_cast<int>(r)))) * p.cs_ld;
+    const int units = p.K / (8 * HALVES), half = p.K / 2;
+    // an even first row: the two rows of a pair then share their lines
+    for (int64_t r0 = (Y == 2 ? lo & ~1 : lo) + Y * (static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6)); r0 < hi;
+         r0 += static_cast<int64_t>(gridDim.x) * 4 * Y) {
+        int64_t row[Y];
+        row[0] = r0 < lo ? r0 + 1 : r0;
+        if constexpr (Y == 2) row[1] = r0 + 1 < hi ? r0 + 1 : r0;
         const bool keep = p.v_out != nullptr;
-        float v[NC ? NC : 1][VALS];
-        uint32_t m = 0;   // largest |v| as bits: a NaN is larger than infinity, which is larger than any number
+        const float* cs[Y] = {};
+        if constexpr (SCALES) {
+#pragma unroll
+            for (int y = 0; y < Y; ++y)
+                cs[y] = p.cs + static_cast<int64_t>(uni(find_expert_wave(s_off, p.E, static_cast<int>(row[y])))) * p.cs_ld;
+        }
+        uint4 w[Y][NC ? NC : 1][HALVES];
+        uint32_t m[Y] = {};
+        auto top_of = [&](int y, int c, const uint4 (&u)[HALVES]) {
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                float v[8];
+                quant_vals(u[h], SCALES ? cs[y] + h * half + c * 8 : nullptr, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[y] = max(m[y], __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+            }
+        };
         if constexpr (NC > 0) {
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const int c = lane + 64 * j;
-                quant_unit<MODE>(p, r, cs, min(c, units - 1), v[j], keep && c < units);
+            for (int j = 0; j < NC; ++j)
 #pragma unroll
-                for (int i = 0; i < VALS; ++i)   // repeated last units do not change the maximum
-                    m = max(m, __builtin_bit_cast(uint32_t, v[j][i]) & 0x7fffffffu);
+                for (int y = 0; y < Y; ++y) {   // repeated last units do not change the maximum
+                    const int c = lane + 64 * j;
+                    quant_unit<MODE>(p, row[y], min(c, units - 1), keep && c < units, w[y][j]);
+                }
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+#pragma unroll
+                for (int y = 0; y < Y; ++y) top_of(y, min(lane + 64 * j, units - 1), w[y][j]);
             }
         } else {
-            for (int c = lane; c < units; c += 64) {
-                quant_unit<MODE>(p, r, cs, c, v[0], keep);
+            for (int c = lane; c < units; c += 64)
 #pragma unroll
-                for (int i = 0; i < VALS; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[0][i]) & 0x7fffffffu);
-            }
+                for (int y = 0; y < Y; ++y) {
+                    quant_unit<MODE>(p, row[y], c, keep, w[y][0]);
+                    top_of(y, c, w[y][0]);
+                }
         }
+        QuantScale sc[Y];
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 64)));
-        float top = __builtin_bit_cast(float, m);
-        const bool fin = m < 0x7f800000u;
-        if (lane == 0) p.s[r] = fin ? top / 127.0f : __builtin_nanf("");
-        // a power of two that brings the row near one where it is far from it
-        const float pw = top < 0x1p-90f ? 0x1p64f : (top > 0x1p90f ? 0x1p-64f : 1.0f);
-        float c127 = 127.0f * pw;
-        top *= pw;
-        float inv = 1.0f / top;
-        const bool zero = m == 0 || !fin;
-        int8_t* qrow = p.q + r * p.ldq;
-        auto put = [&](int c, const float* u) {
+        for (int y = 0; y < Y; ++y) {
 #pragma unroll
-            for (int h = 0; h < VALS / 8; ++h) {
-                uint2 o = quant8(u + 8 * h, c127, top, inv);
-                if (zero) o = make_uint2(0, 0);
-                *reinterpret_cast<uint2*>(qrow + (MODE == Q_DGLU ? h * (p.K / 2) : 0) + c * 8) = o;
+            for (int d = 32; d >= 1; d >>= 1)
+                m[y] = max(m[y], static_cast<uint32_t>(__shfl_xor(static_cast<int>(m[y]), d, 64)));
+            sc[y] = quant_scale(m[y]);
+            if (lane == 0) p.s[row[y]] = m[y] < 0x7f800000u ? __builtin_bit_cast(float, m[y]) / 127.0f : __builtin_nanf("");
+        }
+        if constexpr (Y == 2 && NC > 0) {
+            // The floats are made again from the kept bf16 values: held over the reductions they would take twice the
+            // registers.
+#pragma unroll
+            for (int y = 0; y < Y; ++y)
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        asm volatile("" : "+v"(w[y][j][h].x), "+v"(w[y][j][h].y), "+v"(w[y][j][h].z), "+v"(w[y][j][h].w));
+        }
+        auto at = [&](int64_t r, int c) { return p.q + r * p.q_row + (c >> 6) * p.q_block + (c & 63); };
+        // unit c of the rows; lanes past the end take part in the exchange of a pair with zeros
+        auto put = [&](int c, int j) {
+            const int cc = min(c, units - 1);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                uint2 q[Y];
+#pragma unroll
+                for (int y = 0; y < Y; ++y) {
+                    float v[8];
+                    quant_vals(w[y][j][h], SCALES ? cs[y] + h * half + cc * 8 : nullptr, v);
+                    q[y] = quant8(v, sc[y]);
+                    if (c >= units) q[y] = make_uint2(0, 0);
+                }
+                const int col = h * half + c * 8;
+                if constexpr (Y == 2) {
+                    // even lanes: 16 bytes of the first row; odd lanes: of the second
+                    const bool odd = lane & 1;
+                    const uint2 send = odd ? q[0] : q[1];
+                    const uint2 got = make_uint2(__builtin_amdgcn_mov_dpp(send.x, 0xb1, 0xf, 0xf, true),     // the other
+                                                 __builtin_amdgcn_mov_dpp(send.y, 0xb1, 0xf, 0xf, true));    // lane of the pair
+                    const uint4 o = odd ? make_uint4(got.x, got.y, q[1].x, q[1].y) : make_uint4(q[0].x, q[0].y, got.x, got.y);
+                    if ((c & ~1) < units) *reinterpret_cast<uint4*>(at(row[odd], col & ~15)) = o;
+                } else if (c < units) {
+                    *reinterpret_cast<uint2*>(at(row[0], col)) = q[0];
+                }
             }
         };
         if constexpr (NC > 0) {
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                const int c = lane + 64 * j;
-                if (c < units) put(c, v[j]);
+                put(lane + 64 * j, j);
             }
         } else {
-            for (int c = lane; c < units; c += 64) {
-                quant_unit<MODE>(p, r, cs, c, v[0], false);
-                put(c, v[0]);
+            for (int c = lane; c - lane < units; c += 64) {
+#pragma unroll
+                for (int y = 0; y < Y; ++y) quant_unit<MODE>(p, row[y], min(c, units - 1), false, w[y][0]);
+                put(c, 0);
             }
         }
-        const int pad = (p.ldq - p.K) / 8;   // below 16
-        if (lane < pad) *reinterpret_cast<uint2*>(qrow + p.K + lane * 8) = make_uint2(0, 0);
+        const int pad = (p.width - p.K) / 8;   // below 16
+        if (lane < Y * pad)
+            *reinterpret_cast<uint2*>(at(row[lane % Y], p.K + lane / Y * 8)) = make_uint2(0, 0);
     }
 }
 
@@ -271,13 +339,14 @@ __device__ __forceinline__ int i8_tile_rows(int m, int tile) {
 template <int TB>
 __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
                                                int nb, int nblocks, int nsteps) {
-    constexpr int G = TB == 1 ? 8 : 4;   // steps loaded at a time
+    constexpr int G = TB == 1 ? 8 : (TB == 2 ? 4 : 2);   // steps loaded at a time
     const int lane = threadIdx.x & 63;
     const int8_t* wp = w + static_cast<int64_t>(min(nb, nblocks - 1)) * nsteps * 1024 + lane * 16;
     const int8_t* tp[TB];
 #pragma unroll
     for (int i = 0; i < TB; ++i)
-        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * p.ldq + 16 * (lane >> 5);
+        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * 64 + 16 * (lane >> 5);
+    const int64_t block = static_cast<int64_t>(p.M) * 64;   // bytes of 64 columns of all rows
     i32x16 acc[TB];
 #pragma unroll
     for (int i = 0; i < TB; ++i)
@@ -290,7 +359,7 @@ __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t
             const int st = min(g + u, nsteps - 1);
             wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024));
 #pragma unroll
-            for (int i = 0; i < TB; ++i) tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + st * 32);
+            for (int i = 0; i < TB; ++i) tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + (st >> 1) * block + (st & 1) * 32);
         }
     };
     auto mma = [&](int buf, int g) {
@@ -336,10 +405,10 @@ __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t
     }
 }
 
-__global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
+__global__ __launch_bounds__(256, 3) void int8_stream_kernel(const Int8Params p) {
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
-    const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32;
+    const int nblocks = (p.N + 31) / 32, nsteps = p.width / 32;
     const int items_n = (nblocks + 3) / 4;
     prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(m - i8_tile_rows(m, p.tile)) * items_n; });
     const int total = uni(s_pre[p.E]);
@@ -396,7 +465,7 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
     __shared__ __attribute__((aligned(16))) int8_t s_stg[4 * I8_STG_BYTES];
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
-    const int nblocks = (p.N + 31) / 32, nsteps = p.ldq / 32, nstages = p.ldq / I8_STAGE;
+    const int nblocks = (p.N + 31) / 32, nsteps = p.width / 32, nstages = p.width / I8_STAGE;
     const int tiles_n = (p.N + TILE - 1) / TILE;
     prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
                    [&](int m) { return (i8_tile_rows(m, TILE) + TILE - 1) / TILE * tiles_n; });
@@ -413,6 +482,7 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
     const int8_t* w_base = nullptr;   // its expert's matrix
     uint32_t t_voff[B];               // this lane's chunks of rows 16 B wave + 16 i ..
     int wb[B / 2];                    // this wave's 32-column blocks
+    const int64_t t_block = static_cast<int64_t>(p.M) * I8_STAGE;   // bytes of 64 columns of all rows
     int e = 0, row0 = 0, rows = 0, col0 = 0;
     auto setup = [&](int t) {
         e = uni(find_expert_wave(s_pre, p.E, t));
@@ -423,13 +493,13 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
         row0 = lo + tm * TILE;
         rows = min(TILE, m - tm * TILE);
         col0 = tn * TILE;
-        t_base = p.q + static_cast<int64_t>(row0) * p.ldq;
+        t_base = p.q + static_cast<int64_t>(row0) * I8_STAGE;
         w_base = p.w + static_cast<int64_t>(e) * p.w_stride;
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int r = 16 * B * wave + 16 * i + (lane >> 2);
             const int c = (lane & 3) ^ ((r >> 2) & 3);
-            t_voff[i] = static_cast<uint32_t>(min(r, rows - 1)) * p.ldq + 16 * c;
+            t_voff[i] = static_cast<uint32_t>(min(r, rows - 1)) * I8_STAGE + 16 * c;
         }
 #pragma unroll
         for (int i = 0; i < B / 2; ++i) wb[i] = min(col0 / 32 + B / 2 * wave + i, nblocks - 1);
@@ -440,7 +510,7 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
         if (st >= nstages) return;
         const uint32_t dst = ring + (st & (SLOTS - 1)) * SLOT_BYTES;
         if constexpr (i < B) {
-            dma16(t_base + st * I8_STAGE, t_voff[i], dst + (16 * B * wave + 16 * i) * I8_STAGE);
+            dma16(t_base + st * t_block, t_voff[i], dst + (16 * B * wave + 16 * i) * I8_STAGE);
         } else {
             constexpr int h = (i - B) >> 1, u = i & 1;
             dma16(w_base + (static_cast<int64_t>(wb[h]) * nsteps + 2 * st + u) * 1024, lane * 16,
@@ -636,26 +706,30 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
 }
 
 // ---------------------------------------------------------------- launchers
-template <int MODE>
+template <int MODE, int Y>
 static hipError_t launch_quant(const QuantParams& p, int num_cu, hipStream_t s) {
-    const int units = p.K / QuantUnit<MODE>::VALS;
-    const int64_t want = (static_cast<int64_t>(p.M) + 3) / 4, most = static_cast<int64_t>(num_cu) * 16;
+    const int units = p.K / (8 * QuantUnit<MODE>::HALVES);
+    // four waves a workgroup; pairs of rows start at an even one
+    const int64_t want = (static_cast<int64_t>(p.M) / Y + 1 + 3) / 4, most = static_cast<int64_t>(num_cu) * 16;
     const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(256);
-    if (units <= 64) hipLaunchKernelGGL((quant_rows_kernel<MODE, 1>), grid, block, 0, s, p);
-    else if (units <= 128) hipLaunchKernelGGL((quant_rows_kernel<MODE, 2>), grid, block, 0, s, p);
-    else if (units <= 256) hipLaunchKernelGGL((quant_rows_kernel<MODE, 4>), grid, block, 0, s, p);
-    else if (units <= 512 && MODE != Q_DGLU) hipLaunchKernelGGL((quant_rows_kernel<MODE, MODE == Q_DGLU ? 4 : 8>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((quant_rows_kernel<MODE, 0>), grid, block, 0, s, p);
+    if (units <= 64) hipLaunchKernelGGL((quant_rows_kernel<MODE, 1, Y>), grid, block, 0, s, p);
+    else if (units <= 128) hipLaunchKernelGGL((quant_rows_kernel<MODE, 2, Y>), grid, block, 0, s, p);
+    else if (units <= 256) hipLaunchKernelGGL((quant_rows_kernel<MODE, 4, Y>), grid, block, 0, s, p);
+    else if (units <= 512 && MODE != Q_DGLU)
+        hipLaunchKernelGGL((quant_rows_kernel<MODE, MODE == Q_DGLU ? 4 : 8, Y>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((quant_rows_kernel<MODE, 0, Y>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
 hipError_t launch_quant_rows(QuantMode mode, const QuantParams& p, int num_cu, hipStream_t s) {
     if (p.M <= 0) return hipSuccess;
+    // pairs where they leave at least eight waves for each CU
+    const bool pairs = p.blocked && p.M >= 16 * num_cu;
     switch (mode) {
-        case Q_PLAIN: return launch_quant<Q_PLAIN>(p, num_cu, s);
-        case Q_GLU: return launch_quant<Q_GLU>(p, num_cu, s);
-        case Q_SCALED: return launch_quant<Q_SCALED>(p, num_cu, s);
-        default: return launch_quant<Q_DGLU>(p, num_cu, s);
+        case Q_PLAIN: return pairs ? launch_quant<Q_PLAIN, 2>(p, num_cu, s) : launch_quant<Q_PLAIN, 1>(p, num_cu, s);
+        case Q_GLU: return pairs ? launch_quant<Q_GLU, 2>(p, num_cu, s) : launch_quant<Q_GLU, 1>(p, num_cu, s);
+        case Q_SCALED: return launch_quant<Q_SCALED, 1>(p, num_cu, s);
+        default: return launch_quant<Q_DGLU, 1>(p, num_cu, s);
     }
 }
 
@@ -690,7 +764,7 @@ hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
         if (st != hipSuccess) return st;
     }
     const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E)) * ((p.N + 127) / 128);
-    const int64_t most = static_cast<int64_t>(num_cu) * 2;
+    const int64_t most = static_cast<int64_t>(num_cu) * 3;
     hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
     return hipGetLastError();
 }

@@ -33,9 +33,12 @@ size_t matrix_bytes(int64_t rows, int64_t cont) { return static_cast<size_t>(i8_
 // Quantize `p` into the workspace, then multiply by the packed matrix [out_cols][p.K].
 int quantize_and_multiply(QuantMode mode, QuantParams p, const void* packed, int64_t out_cols, const float* ws, int ws_ld,
                           void* workspace, void* out, hipStream_t stream, int num_cu) {
-    p.ldq = static_cast<int>(i8_cont_p(p.K));
+    p.width = static_cast<int>(i8_cont_p(p.K));
     p.q = static_cast<int8_t*>(workspace);
-    p.s = reinterpret_cast<float*>(p.q + static_cast<int64_t>(p.M) * p.ldq);
+    p.q_block = static_cast<int64_t>(p.M) * 64;
+    p.q_row = 64;
+    p.blocked = 1;
+    p.s = reinterpret_cast<float*>(p.q + static_cast<int64_t>(p.M) * p.width);
     if (launch_quant_rows(mode, p, num_cu, stream) != hipSuccess) return GG_ERR_HIP;
     Int8Params g{};
     g.q = p.q;
@@ -45,7 +48,7 @@ int quantize_and_multiply(QuantMode mode, QuantParams p, const void* packed, int
     g.w_stride = static_cast<int64_t>(matrix_bytes(out_cols, p.K));
     g.ws = ws;
     g.ws_ld = ws_ld;
-    g.ldq = p.ldq;
+    g.width = p.width;
     g.M = p.M;
     g.E = p.E;
     g.N = static_cast<int>(out_cols);
@@ -69,8 +72,10 @@ int gg_int8_quantize_rows(const void* x, int64_t M, int64_t K, int8_t* q, float*
     QuantParams p{};
     p.x = static_cast<const uint16_t*>(x);
     p.M = static_cast<int>(M);
-    p.K = p.ldq = static_cast<int>(K);
+    p.K = p.width = static_cast<int>(K);
     p.q = q;
+    p.q_block = 64;
+    p.q_row = K;
     p.s = s;
     return launch_quant_rows(Q_PLAIN, p, info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
