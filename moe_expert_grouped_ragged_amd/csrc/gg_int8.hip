@@ -180,14 +180,18 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
                 cs[y] = p.cs + static_cast<int64_t>(uni(find_expert_wave(s_off, p.E, static_cast<int>(row[y])))) * p.cs_ld;
         }
         uint4 w[Y][NC ? NC : 1][HALVES];
+        float f[SCALES ? Y : 1][SCALES && NC ? NC : 1][HALVES][8];   // scaled values, made once
         uint32_t m[Y] = {};
-        auto top_of = [&](int y, int c, const uint4 (&u)[HALVES]) {
+        auto top_of = [&](int y, int j, int c) {
 #pragma unroll
             for (int h = 0; h < HALVES; ++h) {
                 float v[8];
-                quant_vals(u[h], SCALES ? cs[y] + h * half + c * 8 : nullptr, v);
+                quant_vals(w[y][j][h], SCALES ? cs[y] + h * half + c * 8 : nullptr, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m[y] = max(m[y], __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+                for (int i = 0; i < 8; ++i) {
+                    m[y] = max(m[y], __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+                    if constexpr (SCALES) f[y][j][h][i] = v[i];
+                }
             }
         };
         if constexpr (NC > 0) {
@@ -199,16 +203,15 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
                     quant_unit<MODE>(p, row[y], min(c, units - 1), keep && c < units, w[y][j]);
                 }
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
+            for (int j = 0; j < NC; ++j)
 #pragma unroll
-                for (int y = 0; y < Y; ++y) top_of(y, min(lane + 64 * j, units - 1), w[y][j]);
-            }
+                for (int y = 0; y < Y; ++y) top_of(y, j, min(lane + 64 * j, units - 1));
         } else {
             for (int c = lane; c < units; c += 64)
 #pragma unroll
                 for (int y = 0; y < Y; ++y) {
                     quant_unit<MODE>(p, row[y], c, keep, w[y][0]);
-                    top_of(y, c, w[y][0]);
+                    top_of(y, 0, c);
                 }
         }
         QuantScale sc[Y];
@@ -234,15 +237,18 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
         auto at = [&](int64_t r, int c) { return p.q + r * p.q_row + (c >> 6) * p.q_block + (c & 63); };
         // unit c of the rows; lanes past the end take part in the exchange of a pair with zeros
         auto put = [&](int c, int j) {
-            const int cc = min(c, units - 1);
 #pragma unroll
             for (int h = 0; h < HALVES; ++h) {
                 uint2 q[Y];
 #pragma unroll
                 for (int y = 0; y < Y; ++y) {
-                    float v[8];
-                    quant_vals(w[y][j][h], SCALES ? cs[y] + h * half + cc * 8 : nullptr, v);
-                    q[y] = quant8(v, sc[y]);
+                    if constexpr (SCALES) {
+                        q[y] = quant8(f[y][j][h], sc[y]);
+                    } else {
+                        float v[8];
+                        quant_vals(w[y][j][h], nullptr, v);
+                        q[y] = quant8(v, sc[y]);
+                    }
                     if (c >= units) q[y] = make_uint2(0, 0);
                 }
                 const int col = h * half + c * 8;
@@ -267,7 +273,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
         } else {
             for (int c = lane; c - lane < units; c += 64) {
 #pragma unroll
-                for (int y = 0; y < Y; ++y) quant_unit<MODE>(p, row[y], min(c, units - 1), false, w[y][0]);
+                for (int y = 0; y < Y; ++y) {
+                    quant_unit<MODE>(p, row[y], min(c, units - 1), false, w[y][0]);
+                    if constexpr (SCALES) top_of(y, 0, min(c, units - 1));
+                }
                 put(c, 0);
             }
         }
@@ -320,13 +329,12 @@ __global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __re
 // a remainder of few rows (all rows of a small expert) runs as streaming
 // items, which read each weight byte once for all of them.
 //
-// Streaming items: up to 96 rows of one expert x 128 output columns; each of
-// the four waves owns one 32-column block over the whole summed dimension, its
-// weights one coalesced 1 KiB load a step and the token operands loaded
-// straight from the quantized rows.
-constexpr int I8_GROUP = 96;
+// Streaming items: up to 96 rows of one expert x a range of output columns; a
+// wave takes 32 columns at a time over the whole summed dimension, its weights
+// one coalesced 1 KiB load a step.  Bound by the weights' bytes.
+constexpr int I8_GROUP = 96;   // rows of a streaming item, at most
+constexpr int I8_RING = 128 * 1024;   // LDS for operands
 
-__device__ __forceinline__ int i8_groups(int m) { return (m + I8_GROUP - 1) / I8_GROUP; }
 // Rows of an expert that tiles of `tile` rows cover (0: there are no tiles).  256-row tiles leave a remainder
 // of at most 96 rows; 128-row tiles, which run where there is little work, take all of an expert or nothing.
 __device__ __forceinline__ int i8_tile_rows(int m, int tile) {
@@ -336,50 +344,12 @@ __device__ __forceinline__ int i8_tile_rows(int m, int tile) {
     return tail <= I8_GROUP ? m - tail : m;
 }
 
+// Scales and stores a streaming item's sums: lane holds token lane & 31 of each 32-row block and, in register
+// 4q + x, column 32 nb + 8q + 4(lane >> 5) + x.
 template <int TB>
-__device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
-                                               int nb, int nblocks, int nsteps) {
-    constexpr int G = TB == 1 ? 8 : (TB == 2 ? 4 : 2);   // steps loaded at a time
+__device__ __forceinline__ void i8_stream_store(const Int8Params& p, const float* ws, int row0, int rows, int nb,
+                                                const i32x16 (&acc)[TB]) {
     const int lane = threadIdx.x & 63;
-    const int8_t* wp = w + static_cast<int64_t>(min(nb, nblocks - 1)) * nsteps * 1024 + lane * 16;
-    const int8_t* tp[TB];
-#pragma unroll
-    for (int i = 0; i < TB; ++i)
-        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * 64 + 16 * (lane >> 5);
-    const int64_t block = static_cast<int64_t>(p.M) * 64;   // bytes of 64 columns of all rows
-    i32x16 acc[TB];
-#pragma unroll
-    for (int i = 0; i < TB; ++i)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) acc[i][x] = 0;
-    i32x4 wv[2][G], tv[2][G][TB];
-    auto load = [&](int buf, int g) {
-#pragma unroll
-        for (int u = 0; u < G; ++u) {
-            const int st = min(g + u, nsteps - 1);
-            wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024));
-#pragma unroll
-            for (int i = 0; i < TB; ++i) tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + (st >> 1) * block + (st & 1) * 32);
-        }
-    };
-    auto mma = [&](int buf, int g) {
-#pragma unroll
-        for (int u = 0; u < G; ++u)
-            if (g + u < nsteps) {
-#pragma unroll
-                for (int i = 0; i < TB; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[buf][u], tv[buf][u][i], acc[i], 0, 0, 0);
-            }
-    };
-    load(0, 0);
-    for (int g = 0; g < nsteps; g += 2 * G) {
-        load(1, g + G);
-        mma(0, g);
-        load(0, g + 2 * G);
-        mma(1, g + G);
-    }
-    if (nb >= nblocks) return;
-    // lane holds token lane & 31 of each block and, in register 4q + x, column 8q + 4(lane >> 5) + x
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
         const int r = i * 32 + (lane & 31);
@@ -405,27 +375,112 @@ __device__ __forceinline__ void i8_stream_item(const Int8Params& p, const int8_t
     }
 }
 
-__global__ __launch_bounds__(256, 3) void int8_stream_kernel(const Int8Params p) {
+// One wave's 32 output columns (block nb) for up to 32 TB rows over the whole summed dimension, G steps loaded
+// while G are multiplied.  The token operands come from `panel` (LDS, TB operands of 1 KiB a step), or straight
+// from the quantized rows.
+template <int TB, bool PANEL>
+__device__ __forceinline__ void i8_stream_block(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
+                                                int nb, int nsteps, const int8_t* panel) {
+    constexpr int G = PANEL || TB == 1 ? 8 : (TB == 2 ? 4 : 2);
+    const int lane = threadIdx.x & 63;
+    const int8_t* wp = w + static_cast<int64_t>(nb) * nsteps * 1024 + lane * 16;
+    const int8_t* tp[TB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * 64 + 16 * (lane >> 5);
+    const int64_t block = static_cast<int64_t>(p.M) * 64;   // bytes of 64 columns of all rows
+    i32x16 acc[TB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[i][x] = 0;
+    i32x4 wv[2][G], tv[2][PANEL ? 1 : G][TB];
+    auto load = [&](int buf, int g) {
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            const int st = min(g + u, nsteps - 1);
+            wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024));
+            if constexpr (!PANEL) {
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + (st >> 1) * block + (st & 1) * 32);
+            }
+        }
+    };
+    auto mma = [&](int buf, int g) {
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+            if (g + u < nsteps) {
+#pragma unroll
+                for (int i = 0; i < TB; ++i) {
+                    i32x4 t;
+                    if constexpr (PANEL) t = *reinterpret_cast<const i32x4*>(panel + ((g + u) * TB + i) * 1024 + lane * 16);
+                    else t = tv[buf][u][i];
+                    acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[buf][u], t, acc[i], 0, 0, 0);
+                }
+            }
+    };
+    load(0, 0);
+    for (int g = 0; g < nsteps; g += 2 * G) {
+        load(1, g + G);
+        mma(0, g);
+        load(0, g + 2 * G);
+        mma(1, g + G);
+    }
+    i8_stream_store<TB>(p, ws, row0, rows, nb, acc);
+}
+
+// The list of all (row group, 32-column block) pairs, groups of p.group rows.
+//
+// PANEL: each workgroup takes an equal stretch of the list, eight waves a block
+// at a time, and keeps the rows of the group it is in in LDS in operand order (p.group is
+// what 128 KiB hold of the summed width): read by every wave from memory they
+// cost nearly as much of the load path as the weights (128 experts of 22 rows,
+// K 2688, N 3712: 288 us so, 204 us with one row each).
+// Otherwise, for few rows and for what large tiles leave: items of four blocks, a wave each, in turn.
+template <bool PANEL>
+__global__ __launch_bounds__(PANEL ? 512 : 256) void int8_stream_kernel(const Int8Params p) {
+    constexpr int W = PANEL ? 8 : 4;
+    __shared__ __attribute__((aligned(1024))) int8_t s_panel[PANEL ? I8_RING : 16];
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
     const int nblocks = (p.N + 31) / 32, nsteps = p.width / 32;
-    const int items_n = (nblocks + 3) / 4;
-    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return i8_groups(m - i8_tile_rows(m, p.tile)) * items_n; });
-    const int total = uni(s_pre[p.E]);
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
+                   [&](int m) { return (m - i8_tile_rows(m, p.tile) + p.group - 1) / p.group * nblocks; });
+    const int64_t total = uni(s_pre[p.E]);
     const int wave = uni(threadIdx.x >> 6);
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
-        const int e = uni(find_expert_wave(s_pre, p.E, it));
-        const int local = it - uni(s_pre[e]);
-        const int grp = local / items_n, col = local - grp * items_n;
-        const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
-        const int row0 = lo + i8_tile_rows(hi - lo, p.tile) + grp * I8_GROUP;
-        const int rows = min(I8_GROUP, hi - row0);
-        const int8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
-        const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
-        const int nb = col * 4 + wave;
-        if (rows <= 32) i8_stream_item<1>(p, w, ws, row0, rows, nb, nblocks, nsteps);
-        else if (rows <= 64) i8_stream_item<2>(p, w, ws, row0, rows, nb, nblocks, nsteps);
-        else i8_stream_item<3>(p, w, ws, row0, rows, nb, nblocks, nsteps);
+    // items of the list: one stretch a workgroup, or four blocks each
+    const int64_t items = PANEL ? gridDim.x : (total + W - 1) / W;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        int at = static_cast<int>(total * it / items);
+        const int end = static_cast<int>(total * (it + 1) / items);
+        while (at < end) {   // one row group's part of the item
+            const int e = uni(find_expert_wave(s_pre, p.E, at));
+            const int local = at - uni(s_pre[e]), grp = local / nblocks, nb0 = local - grp * nblocks;
+            const int nb1 = min(nblocks, nb0 + end - at);
+            const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
+            const int row0 = lo + i8_tile_rows(hi - lo, p.tile) + grp * p.group;
+            const int rows = min(p.group, hi - row0);
+            const int8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
+            const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
+            const int tb = (rows + 31) / 32;
+            if constexpr (PANEL) {
+                __syncthreads();   // the last group's panel is read
+                for (int i = threadIdx.x; i < nsteps * tb * 64; i += W * 64) {
+                    // operand bytes 16 i: of step st, row block b, row r % 32, columns 16 h onwards
+                    const int st = (i >> 6) / tb, r = ((i >> 6) % tb) * 32 + (i & 31), h = (i >> 5) & 1;
+                    *reinterpret_cast<i32x4*>(s_panel + i * 16) = *reinterpret_cast<const i32x4*>(
+                        p.q + (static_cast<int64_t>(st >> 1) * p.M + row0 + min(r, rows - 1)) * 64 + (st & 1) * 32 + 16 * h);
+                }
+                __syncthreads();
+            }
+            for (int nb = nb0 + wave; nb < nb1; nb += W) {
+                if (tb == 1) i8_stream_block<1, PANEL>(p, w, ws, row0, rows, nb, nsteps, s_panel);
+                else if (tb == 2) i8_stream_block<2, PANEL>(p, w, ws, row0, rows, nb, nsteps, s_panel);
+                else i8_stream_block<3, PANEL>(p, w, ws, row0, rows, nb, nsteps, s_panel);
+            }
+            at += nb1 - nb0;
+        }
     }
 }
 
@@ -447,7 +502,6 @@ __global__ __launch_bounds__(256, 3) void int8_stream_kernel(const Int8Params p)
 // those stages leave the epilogue's stores outstanding: memory operations
 // complete in order, and the stores were issued after the copies.
 constexpr int I8_STAGE = 64;
-constexpr int I8_RING = 128 * 1024;
 constexpr int I8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf16
 
 __device__ __forceinline__ int acc_rd_i(int a) {
@@ -763,9 +817,17 @@ hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
         const hipError_t st = g.tile == 256 ? launch_tiles<4>(g, num_cu, s) : launch_tiles<2>(g, num_cu, s);
         if (st != hipSuccess) return st;
     }
-    const int64_t upper = (static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E)) * ((p.N + 127) / 128);
-    const int64_t most = static_cast<int64_t>(num_cu) * 3;
-    hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
+    const int64_t nblocks = (p.N + 31) / 32;
+    if (g.tile == 128 && p.width * 32 <= I8_RING) {
+        g.group = I8_RING / (p.width * 32) * 32;
+        if (g.group > I8_GROUP) g.group = I8_GROUP;
+        hipLaunchKernelGGL((int8_stream_kernel<true>), dim3(static_cast<unsigned>(num_cu)), dim3(512), 0, s, g);
+    } else {
+        g.group = I8_GROUP;
+        const int64_t groups = static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E);
+        const int64_t upper = (groups * nblocks + 3) / 4, most = static_cast<int64_t>(num_cu) * 3;
+        hipLaunchKernelGGL((int8_stream_kernel<false>), dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
+    }
     return hipGetLastError();
 }
 
