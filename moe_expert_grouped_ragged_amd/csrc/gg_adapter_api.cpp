@@ -26,10 +26,10 @@ int check_adapter_shape(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
 // Rows of one unit of a backward kernel whose workgroups each own one of
 // `chunks` column chunks: about `units` units when the rows are spread evenly,
 // and at least 256 rows, so that the fp32 part a unit leaves behind stays
-// small next to the rows it reads.
+// small next to the rows it reads; at most 2^30, which the kernels count in 32 bits.
 int64_t unit_rows(int64_t M, int64_t chunks, int64_t units) {
     const int64_t rows = (M * chunks / units + AD_BLK - 1) / AD_BLK * AD_BLK;
-    return rows < 256 ? 256 : rows;
+    return rows < 256 ? 256 : (rows < (int64_t(1) << 30) ? rows : int64_t(1) << 30);
 }
 
 // Workspace of the backward pass: byte offsets of its arrays.
