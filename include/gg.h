@@ -302,7 +302,8 @@ size_t gg_int8_workspace_bytes(int64_t M, int64_t width);
 
 /* Forward: x [M][K] with GG_ACT_NONE, or H1 [M][2K] with an activation, in
  * which case a_out (may be NULL) receives A [M][K].  packed: gg_int8_pack(...,
- * transposed = 0).  y [M][N].  Two launches. */
+ * transposed = 0).  y [M][N].  One launch quantizes; the product is one
+ * (M <= 64) or two (tiles, then the rows they leave). */
 int gg_int8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed,
                     int64_t E, int64_t N, int64_t K, int activation, void* a_out,
                     void* workspace, size_t workspace_bytes, void* y, hipStream_t stream);
@@ -310,7 +311,7 @@ int gg_int8_forward(const void* x, const int64_t* offsets, int64_t M, const void
 /* Input gradient: dy [M][N] with GG_ACT_NONE (h1 and dh1_out NULL); with an
  * activation N = 2F (F a multiple of 8), dy is dA [M][F], h1 [M][2F] the saved
  * FC1 output, and dh1_out (may be NULL) receives dH1 [M][2F].  packed:
- * gg_int8_pack(..., transposed = 1).  dx [M][K].  Two launches. */
+ * gg_int8_pack(..., transposed = 1).  dx [M][K].  Launches as the forward's. */
 int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed,
                   int64_t E, int64_t N, int64_t K, int activation, void* dh1_out,
                   void* workspace, size_t workspace_bytes, void* dx, hipStream_t stream);

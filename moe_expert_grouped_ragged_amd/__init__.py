@@ -27,7 +27,20 @@ input rows:
   gg_scale_rows_backward(dxs, x, probs)          -> (dx, dprobs)
         (ScaleRows is the autograd form, to compose with FrozenExpertMLP)
 
-Frozen, bias-free bf16 expert weights only: the Megatron-LM pull request
+Expert products over 8-bit copies of the frozen weights, tokens quantized on
+the way (half the weight bytes, twice the matrix rate), and the trainable
+low-rank adapters next to a frozen product:
+
+  gg_int8_quantize_rows(x)                       -> (q, s), one scale a row
+  gg_int8_pack(wq, ws) / gg_int8_pack_transposed -> laid out for forward / dgrad
+  gg_int8_forward(x, offsets, packed, ...)       -> (y, A or None)
+  gg_int8_dgrad(dy, offsets, packed_t, ...)      -> (dx, dH1 or None)
+  gg_adapter_forward(x, offsets, a, b, scale, base)           -> (y, u)
+  gg_adapter_backward(dy, x, u, offsets, a, b, scale, base)   -> (dx, da, db)
+        (Int8AdapterExpertMLP runs the gated MLP of both, with autograd;
+        int8_experts prepares its weights)
+
+The other calls take frozen, bias-free bf16 expert weights only: the Megatron-LM pull request
 "perf(moe): add frozen grouped GEMM for adapter training" (section "Why
 existing behavior remains safe") accepts only grouped, frozen, bias-free BF16
 expert weights and fails during preparation otherwise; ``gg_pack_weights``
@@ -39,7 +52,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence, Tuple, Union
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -559,6 +572,16 @@ def gg_scale_rows_backward(dxs: torch.Tensor, x: torch.Tensor, probs: torch.Tens
     return dx, dprobs
 
 
+def _used_on(stream: Optional[torch.cuda.Stream], pairs) -> None:
+    """Tells the allocator that the memory it gave out here (pairs of a tensor
+    and the caller's, None where there was none) is used on another stream than
+    the current one, so that it is not given out again before that work is done."""
+    if stream is not None:
+        for new, given in pairs:
+            if new is not None and given is None:
+                new.record_stream(stream)
+
+
 def _typed_cuda(t: torch.Tensor, dtype, name: str, shape, device) -> torch.Tensor:
     """A contiguous device tensor of the given dtype and shape (None: any size there), on the given device."""
     if not isinstance(t, torch.Tensor):
@@ -590,8 +613,10 @@ def gg_int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: 
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
+    given = q, s
     q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else _typed_cuda(q, torch.int8, "q", (M, K), x.device)
     s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else _probs_cuda(s, M, x.device, "s")
+    _used_on(stream, zip((q, s), given))
     _check(lib.gg_int8_quantize_rows(x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(), _stream_ptr(stream, x.device)),
            "gg_int8_quantize_rows")
     return q, s
@@ -604,9 +629,11 @@ def _int8_pack(wq, ws, transposed, packed, stream):
     need = int8_packed_bytes(E, N, K, transposed)
     if need == 0:
         raise ValueError(f"E={E}, N={N}, K={K} is outside the limits of the int8 calls")
+    given = packed
     if packed is None:
         packed = torch.empty(need, dtype=torch.uint8, device=wq.device)
     _workspace(packed, need, wq.device)
+    _used_on(stream, [(packed, given)])
     _check(lib.gg_int8_pack(wq.data_ptr(), ws.data_ptr(), E, N, K, int(transposed), packed.data_ptr(),
                             packed.numel() * packed.element_size(), _stream_ptr(stream, wq.device)), "gg_int8_pack")
     return packed
@@ -655,10 +682,12 @@ def gg_int8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor
         _bf16_cuda(a_out, "a_out", shape=(M, K), device=dev)
     if act == GG_ACT_NONE and (save_a or a_out is not None):
         raise ValueError("A exists with an activation only")
+    given = workspace, a_out, y
     workspace = _workspace(workspace, int8_workspace_bytes(M, K), dev)
     if a_out is None and save_a:
         a_out = _out(None, (M, K), "a_out", dev)
     y = _out(y, (M, N), "y", dev)
+    _used_on(stream, zip((workspace, a_out, y), given))
     _check(lib.gg_int8_forward(x.data_ptr(), off.data_ptr(), M, packed.data_ptr(), E, N, K, act, _ptr(a_out),
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), y.data_ptr(),
                                _stream_ptr(stream, dev)), "gg_int8_forward")
@@ -688,10 +717,12 @@ def gg_int8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
         if h1 is None:
             raise ValueError("dH1 exists with an activation only")
         _bf16_cuda(dh1_out, "dh1_out", shape=(M, N), device=dev)
+    given = workspace, dh1_out, dx
     workspace = _workspace(workspace, int8_workspace_bytes(M, N), dev)
     if dh1_out is None and h1 is not None and save_dh1:
         dh1_out = _out(None, (M, N), "dh1_out", dev)
     dx = _out(dx, (M, K), "dx", dev)
+    _used_on(stream, zip((workspace, dh1_out, dx), given))
     _check(lib.gg_int8_dgrad(dy.data_ptr(), _ptr(h1), off.data_ptr(), M, packed.data_ptr(), E, N, K, act,
                              _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                              dx.data_ptr(), _stream_ptr(stream, dev)), "gg_int8_dgrad")
@@ -734,8 +765,10 @@ def gg_adapter_forward(x: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor, 
         _bf16_cuda(base, "base", shape=(M, N), device=dev)
     if u is not None:
         _bf16_cuda(u, "u", shape=(M, r), device=dev)
+    given = y, u
     y = _out(y, (M, N), "y", dev)
     u = _out(u, (M, r), "u", dev)
+    _used_on(stream, zip((y, u), given))
     _check(lib.gg_adapter_forward(x.data_ptr(), offsets.data_ptr(), M, a.data_ptr(), b.data_ptr(), E, N, K, r, scale,
                                   _ptr(base), u.data_ptr(), y.data_ptr(), _stream_ptr(stream, dev)),
            "gg_adapter_forward")
@@ -766,10 +799,12 @@ def gg_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, offs
         _typed_cuda(db, torch.float32, "db", (E, N, r), dev)
     if dx is not None:
         _bf16_cuda(dx, "dx", shape=(M, K), device=dev)
+    given = workspace, dx, da, db
     workspace = _workspace(workspace, adapter_workspace_bytes(M, E, N, K, r), dev)
     dx = _out(dx, (M, K), "dx", dev)
     da = torch.empty(E, r, K, dtype=torch.float32, device=dev) if da is None else da
     db = torch.empty(E, N, r, dtype=torch.float32, device=dev) if db is None else db
+    _used_on(stream, zip((workspace, dx, da, db), given))
     _check(lib.gg_adapter_backward(dy.data_ptr(), x.data_ptr(), u.data_ptr(), offsets.data_ptr(), M, a.data_ptr(),
                                    b.data_ptr(), E, N, K, r, scale, _ptr(base), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), dx.data_ptr(), da.data_ptr(),
@@ -813,3 +848,69 @@ class FrozenExpertMLP(torch.autograd.Function):
         E, H, F = ctx.shape
         dx = gg_dgrad(dy.contiguous(), h1, offsets, packed, E, H, F)
         return dx, None, None, None, None, None
+
+
+class Int8Experts(NamedTuple):
+    """Frozen gated expert MLPs in 8 bits: W1 [E, 2F, H] and W2 [E, H, F] laid
+    out for the forward (fc1, fc2) and for the input gradient (fc1_t, fc2_t)."""
+    E: int
+    H: int
+    F: int
+    fc1: torch.Tensor
+    fc2: torch.Tensor
+    fc1_t: torch.Tensor
+    fc2_t: torch.Tensor
+
+
+def int8_experts(w1: torch.Tensor, w2: torch.Tensor) -> Int8Experts:
+    """Quantize frozen bf16 weights w1 [E, 2F, H] (gate rows, then up rows) and
+    w2 [E, H, F] for each output channel and lay them out for Int8AdapterExpertMLP."""
+    if w1.requires_grad or w2.requires_grad:
+        raise ValueError("expert base weights must be frozen (requires_grad=False)")
+    if w1.dim() != 3 or w2.dim() != 3 or w1.shape[0] != w2.shape[0] or w1.shape[1] != 2 * w2.shape[2] \
+            or w1.shape[2] != w2.shape[1]:
+        raise ValueError("w1 must be [E, 2F, H] and w2 [E, H, F]")
+    E, H, F = w2.shape
+    packs = []
+    for w in (w1, w2):
+        q, s = gg_int8_quantize_rows(w.reshape(-1, w.shape[2]))
+        q, s = q.view(w.shape), s.view(w.shape[0], w.shape[1])
+        packs.append((gg_int8_pack(q, s), gg_int8_pack_transposed(q, s)))
+    return Int8Experts(E, H, F, packs[0][0], packs[1][0], packs[0][1], packs[1][1])
+
+
+class Int8AdapterExpertMLP(torch.autograd.Function):
+    """The gated expert MLP over frozen 8-bit weights with a low-rank adapter on
+    each of its two products:
+
+      H1 = int8(X) W1^T + scale (X a1^T) b1^T      A = act(gate) * up
+      Y  = int8(A) W2^T + scale (A a2^T) b2^T
+
+    apply(x, offsets, experts, a1, b1, a2, b2, scale, activation) with experts
+    from int8_experts, a1 [E, r1, H], b1 [E, 2F, r1], a2 [E, r2, F],
+    b2 [E, H, r2] (bf16).  The backward gives dX and the adapters' gradients;
+    the base weights have none."""
+
+    @staticmethod
+    def forward(ctx, x, offsets, experts, a1, b1, a2, b2, scale, activation="swiglu"):
+        E, H, F = experts.E, experts.H, experts.F
+        a1, b1, a2, b2 = (t.detach() for t in (a1, b1, a2, b2))
+        h1, _ = gg_int8_forward(x, offsets, experts.fc1, E, 2 * F, H)
+        h1, u1 = gg_adapter_forward(x, offsets, a1, b1, scale, base=h1, y=h1)
+        y, a = gg_int8_forward(h1, offsets, experts.fc2, E, H, F, activation=activation, save_a=True)
+        y, u2 = gg_adapter_forward(a, offsets, a2, b2, scale, base=y, y=y)
+        ctx.save_for_backward(x, offsets, h1, a, u1, u2, a1, b1, a2, b2)
+        ctx.experts, ctx.scale, ctx.activation = experts, scale, activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, offsets, h1, a, u1, u2, a1, b1, a2, b2 = ctx.saved_tensors
+        w, scale = ctx.experts, ctx.scale
+        dy = dy.contiguous()
+        da, _ = gg_int8_dgrad(dy, offsets, w.fc2_t, w.E, w.H, w.F)
+        da, ga2, gb2 = gg_adapter_backward(dy, a, u2, offsets, a2, b2, scale, base=da, dx=da)
+        dx, dh1 = gg_int8_dgrad(da, offsets, w.fc1_t, w.E, 2 * w.F, w.H, h1=h1, activation=ctx.activation)
+        dx, ga1, gb1 = gg_adapter_backward(dh1, x, u1, offsets, a1, b1, scale, base=dx, dx=dx)
+        ga1, gb1, ga2, gb2 = (g.to(torch.bfloat16) for g in (ga1, gb1, ga2, gb2))
+        return dx, None, None, ga1, gb1, ga2, gb2, None, None

@@ -344,12 +344,62 @@ __device__ __forceinline__ int i8_tile_rows(int m, int tile) {
     return tail <= I8_GROUP ? m - tail : m;
 }
 
-// Scales and stores a streaming item's sums: lane holds token lane & 31 of each 32-row block and, in register
-// 4q + x, column 32 nb + 8q + 4(lane >> 5) + x.
+// Four columns' sums of a row, scaled: s ws_e[n] acc, or s acc (SCALED: the output columns have scales).
+template <bool SCALED>
+__device__ __forceinline__ uint2 i8_scale4(int a0, int a1, int a2, int a3, float s, f32x4 c) {
+    float y[4] = {static_cast<float>(a0) * s, static_cast<float>(a1) * s, static_cast<float>(a2) * s,
+                  static_cast<float>(a3) * s};
+    if constexpr (SCALED) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) y[x] *= c[x];
+    }
+    return make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+}
+
+// One wave's 32 output columns (block nb) for up to 32 TB rows over the whole summed dimension, G steps of weights
+// and rows loaded while G are multiplied.
 template <int TB>
-__device__ __forceinline__ void i8_stream_store(const Int8Params& p, const float* ws, int row0, int rows, int nb,
-                                                const i32x16 (&acc)[TB]) {
+__device__ __forceinline__ void i8_stream_block(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
+                                                int nb, int nsteps) {
+    constexpr int G = TB == 1 ? 8 : (TB == 2 ? 4 : 2);
     const int lane = threadIdx.x & 63;
+    const int8_t* wp = w + static_cast<int64_t>(nb) * nsteps * 1024 + lane * 16;
+    const int8_t* tp[TB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * 64 + 16 * (lane >> 5);
+    const int64_t block = static_cast<int64_t>(p.M) * 64;   // bytes of 64 columns of all rows
+    i32x16 acc[TB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i) acc[i] = i32x16{};
+    i32x4 wv[2][G], tv[2][G][TB];
+    auto load = [&](int buf, int g) {
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            const int st = min(g + u, nsteps - 1);
+            wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024));
+#pragma unroll
+            for (int i = 0; i < TB; ++i)
+                tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + (st >> 1) * block + (st & 1) * 32);
+        }
+    };
+    auto mma = [&](int buf, int g) {
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+            if (g + u < nsteps) {
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[buf][u], tv[buf][u][i], acc[i], 0, 0, 0);
+            }
+    };
+    load(0, 0);
+    for (int g = 0; g < nsteps; g += 2 * G) {
+        load(1, g + G);
+        mma(0, g);
+        load(0, g + 2 * G);
+        mma(1, g + G);
+    }
+    // lane holds token lane & 31 of each 32-row block and, in register 4q + x, column 32 nb + 8q + 4(lane >> 5) + x
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
         const int r = i * 32 + (lane & 31);
@@ -360,90 +410,123 @@ __device__ __forceinline__ void i8_stream_store(const Int8Params& p, const float
         for (int q = 0; q < 4; ++q) {
             const int n = nb * 32 + 8 * q + 4 * (lane >> 5);
             if (n >= p.N) continue;
-            float y[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) y[x] = static_cast<float>(acc[i][4 * q + x]) * sr;
-            if (ws) {
-                const float4 c = *reinterpret_cast<const float4*>(ws + n);
-                y[0] *= c.x;
-                y[1] *= c.y;
-                y[2] *= c.z;
-                y[3] *= c.w;
-            }
-            *reinterpret_cast<uint2*>(orow + n) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+            const f32x4 one = {1.0f, 1.0f, 1.0f, 1.0f};
+            const f32x4 c = ws ? *reinterpret_cast<const f32x4*>(ws + n) : one;   // times one is exact
+            *reinterpret_cast<uint2*>(orow + n) =
+                i8_scale4<true>(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3], sr, c);
         }
     }
 }
 
-// One wave's 32 output columns (block nb) for up to 32 TB rows over the whole summed dimension, G steps loaded
-// while G are multiplied.  The token operands come from `panel` (LDS, TB operands of 1 KiB a step), or straight
-// from the quantized rows.
-template <int TB, bool PANEL>
-__device__ __forceinline__ void i8_stream_block(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
-                                                int nb, int nsteps, const int8_t* panel) {
-    constexpr int G = PANEL || TB == 1 ? 8 : (TB == 2 ? 4 : 2);
-    const int lane = threadIdx.x & 63;
-    const int8_t* wp = w + static_cast<int64_t>(nb) * nsteps * 1024 + lane * 16;
-    const int8_t* tp[TB];
+// Column blocks [nb0, nb1) for up to 32 TB rows, dealt to the workgroup's four waves.  The
+// rows' operands lie in `panel` (LDS, TB of 1 KiB a step).  The weights come as one
+// stream over a wave's blocks, in units of four steps (the summed width is padded to
+// that), all but one of R units ahead, the first of them from before the panel is filled: nothing drains at a
+// block's end, where the sums are stored, and loads are repeated only at the stretch's own end.
+template <int TB, bool SCALED>
+__device__ __forceinline__ void i8_stream_blocks(const Int8Params& p, const int8_t* w, const float* ws, int row0, int rows,
+                                                 int nb0, int nb1, int nsteps, int8_t* panel) {
+    constexpr int W = 4, U = 4, R = 8;
+    const int lane = threadIdx.x & 63, nu = nsteps / U;
+    int nb = nb0 + uni(threadIdx.x >> 6);
+    const int total = (nb1 - nb + W - 1) / W * nu;   // none for a wave without a block
+    float sr[TB];
 #pragma unroll
-    for (int i = 0; i < TB; ++i)
-        tp[i] = p.q + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * 64 + 16 * (lane >> 5);
-    const int64_t block = static_cast<int64_t>(p.M) * 64;   // bytes of 64 columns of all rows
+    for (int i = 0; i < TB; ++i) sr[i] = p.s[row0 + min(i * 32 + (lane & 31), rows - 1)];
+    f32x4 cs[4];
+    auto load_scales = [&](int b) {
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                cs[q] = *reinterpret_cast<const f32x4*>(ws + min(b * 32 + 8 * q + 4 * (lane >> 5), p.N - 4));
+        }
+    };
+    load_scales(nb);
+    const int8_t* lp = w + static_cast<int64_t>(min(nb, nb1 - 1)) * nsteps * 1024;
+    int lk = 0, lf = 0;   // the next unit to load: of its block, and of all
+    i32x4 wv[R][U];
+    auto load = [&](i32x4(&v)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(lp + lane * 16 + u * 1024));
+        const bool wrap = ++lk == nu;
+        lk = wrap ? 0 : lk;
+        if (++lf < total) lp += static_cast<int64_t>(U) * 1024 + (wrap ? static_cast<int64_t>(W - 1) * nsteps * 1024 : 0);
+    };
     i32x16 acc[TB];
 #pragma unroll
-    for (int i = 0; i < TB; ++i)
+    for (int i = 0; i < TB; ++i) acc[i] = i32x16{};
+    // in this order: the first unit's wait would otherwise be for all
 #pragma unroll
-        for (int x = 0; x < 16; ++x) acc[i][x] = 0;
-    i32x4 wv[2][G], tv[2][PANEL ? 1 : G][TB];
-    auto load = [&](int buf, int g) {
+    for (int i = 0; i < R - 1; ++i) {
+        load(wv[i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();   // the last panel is read
+    constexpr int F = 8;   // loads of a thread in flight
+    for (int i0 = threadIdx.x; i0 < nsteps * TB * 64; i0 += F * W * 64) {
+        i32x4 v[F];
 #pragma unroll
-        for (int u = 0; u < G; ++u) {
-            const int st = min(g + u, nsteps - 1);
-            wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(st) * 1024));
-            if constexpr (!PANEL) {
+        for (int j = 0; j < F; ++j) {
+            // operand bytes 16 i: of step st, row block b, row r % 32, columns 16 h onwards
+            const int i = min(i0 + j * W * 64, nsteps * TB * 64 - 1);
+            const int st = (i >> 6) / TB, r = ((i >> 6) % TB) * 32 + (i & 31), h = (i >> 5) & 1;
+            v[j] = *reinterpret_cast<const i32x4*>(p.q + (static_cast<int64_t>(st >> 1) * p.M + row0 + min(r, rows - 1)) * 64 +
+                                                   (st & 1) * 32 + 16 * h);
+        }
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int i = i0 + j * W * 64;
+            if (i < nsteps * TB * 64) *reinterpret_cast<i32x4*>(panel + i * 16) = v[j];
+        }
+    }
+    __syncthreads();
+    int k = 0;
+    for (int f = 0; f < total; f += R) {
+        // the last round's units past the end multiply what was loaded last and are not stored
+        static_for<R>([&](auto i_tag) {
+            constexpr int at = decltype(i_tag)::value;
+            load(wv[(at + R - 1) % R]);
+            const int8_t* op = panel + k * (U * TB * 1024) + lane * 16;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < TB; ++i)
-                    tv[buf][u][i] = *reinterpret_cast<const i32x4*>(tp[i] + (st >> 1) * block + (st & 1) * 32);
-            }
-        }
-    };
-    auto mma = [&](int buf, int g) {
-#pragma unroll
-        for (int u = 0; u < G; ++u)
-            if (g + u < nsteps) {
+                    acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                        wv[at][u], *reinterpret_cast<const i32x4*>(op + (u * TB + i) * 1024), acc[i], 0, 0, 0);
+            if (++k == nu) {
+                k = 0;
 #pragma unroll
                 for (int i = 0; i < TB; ++i) {
-                    i32x4 t;
-                    if constexpr (PANEL) t = *reinterpret_cast<const i32x4*>(panel + ((g + u) * TB + i) * 1024 + lane * 16);
-                    else t = tv[buf][u][i];
-                    acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[buf][u], t, acc[i], 0, 0, 0);
+                    const int r = i * 32 + (lane & 31);
+                    uint16_t* orow = p.out + static_cast<int64_t>(row0 + r) * p.N;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = nb * 32 + 8 * q + 4 * (lane >> 5);
+                        const uint2 y = i8_scale4<SCALED>(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2],
+                                                          acc[i][4 * q + 3], sr[i], cs[q]);
+                        if (r < rows && n < p.N && nb < nb1) *reinterpret_cast<uint2*>(orow + n) = y;
+                    }
+                    acc[i] = i32x16{};
                 }
+                nb += W;
+                load_scales(nb);
             }
-    };
-    load(0, 0);
-    for (int g = 0; g < nsteps; g += 2 * G) {
-        load(1, g + G);
-        mma(0, g);
-        load(0, g + 2 * G);
-        mma(1, g + G);
+        });
     }
-    i8_stream_store<TB>(p, ws, row0, rows, nb, acc);
 }
 
-// The list of all (row group, 32-column block) pairs, groups of p.group rows.
+// The list of all (row group, 32-column block) pairs, groups of p.group rows, by
+// workgroups of four waves, a wave a block.  s_off, s_pre: [E + 1].
 //
-// PANEL: each workgroup takes an equal stretch of the list, eight waves a block
-// at a time, and keeps the rows of the group it is in in LDS in operand order (p.group is
+// PANEL: each workgroup takes an equal stretch of the list and keeps the rows
+// of the group it is in in LDS in operand order (p.group is
 // what 128 KiB hold of the summed width): read by every wave from memory they
 // cost nearly as much of the load path as the weights (128 experts of 22 rows,
-// K 2688, N 3712: 288 us so, 204 us with one row each).
+// K 2688, N 3712, quantization included: 300 us from memory, 244 us here, 5.6 TB/s in this kernel).
 // Otherwise, for few rows and for what large tiles leave: items of four blocks, a wave each, in turn.
-template <bool PANEL>
-__global__ __launch_bounds__(PANEL ? 512 : 256) void int8_stream_kernel(const Int8Params p) {
-    constexpr int W = PANEL ? 8 : 4;
-    __shared__ __attribute__((aligned(1024))) int8_t s_panel[PANEL ? I8_RING : 16];
-    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
-    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
+template <bool PANEL, bool SCALED>
+__device__ __forceinline__ void i8_stream_list(const Int8Params& p, int* s_off, int* s_pre, int8_t* s_panel) {
+    constexpr int W = 4;
     const int nblocks = (p.N + 31) / 32, nsteps = p.width / 32;
     prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
                    [&](int m) { return (m - i8_tile_rows(m, p.tile) + p.group - 1) / p.group * nblocks; });
@@ -465,23 +548,25 @@ __global__ __launch_bounds__(PANEL ? 512 : 256) void int8_stream_kernel(const In
             const float* ws = p.ws ? p.ws + static_cast<int64_t>(e) * p.ws_ld : nullptr;
             const int tb = (rows + 31) / 32;
             if constexpr (PANEL) {
-                __syncthreads();   // the last group's panel is read
-                for (int i = threadIdx.x; i < nsteps * tb * 64; i += W * 64) {
-                    // operand bytes 16 i: of step st, row block b, row r % 32, columns 16 h onwards
-                    const int st = (i >> 6) / tb, r = ((i >> 6) % tb) * 32 + (i & 31), h = (i >> 5) & 1;
-                    *reinterpret_cast<i32x4*>(s_panel + i * 16) = *reinterpret_cast<const i32x4*>(
-                        p.q + (static_cast<int64_t>(st >> 1) * p.M + row0 + min(r, rows - 1)) * 64 + (st & 1) * 32 + 16 * h);
+                if (tb == 1) i8_stream_blocks<1, SCALED>(p, w, ws, row0, rows, nb0, nb1, nsteps, s_panel);
+                else if (tb == 2) i8_stream_blocks<2, SCALED>(p, w, ws, row0, rows, nb0, nb1, nsteps, s_panel);
+                else i8_stream_blocks<3, SCALED>(p, w, ws, row0, rows, nb0, nb1, nsteps, s_panel);
+            } else {
+                for (int nb = nb0 + wave; nb < nb1; nb += W) {
+                    if (tb == 1) i8_stream_block<1>(p, w, ws, row0, rows, nb, nsteps);
+                    else if (tb == 2) i8_stream_block<2>(p, w, ws, row0, rows, nb, nsteps);
+                    else i8_stream_block<3>(p, w, ws, row0, rows, nb, nsteps);
                 }
-                __syncthreads();
-            }
-            for (int nb = nb0 + wave; nb < nb1; nb += W) {
-                if (tb == 1) i8_stream_block<1, PANEL>(p, w, ws, row0, rows, nb, nsteps, s_panel);
-                else if (tb == 2) i8_stream_block<2, PANEL>(p, w, ws, row0, rows, nb, nsteps, s_panel);
-                else i8_stream_block<3, PANEL>(p, w, ws, row0, rows, nb, nsteps, s_panel);
             }
             at += nb1 - nb0;
         }
     }
+}
+
+__global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
+    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
+    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
+    i8_stream_list<false, false>(p, s_off, s_pre, nullptr);
 }
 
 // Tiles: 64 B rows x 64 B output columns by four waves, each 32 B x 32 B, as
@@ -757,6 +842,11 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
             }
         });
     }
+    if constexpr (B == 2) {
+        if (p.group == 0) return;   // another launch's
+        __syncthreads();
+        i8_stream_list<true, SCALED>(p, s_off, s_pre, s_ring);
+    }
 }
 
 // ---------------------------------------------------------------- launchers
@@ -802,7 +892,7 @@ template <int B>
 static hipError_t launch_tiles(const Int8Params& p, int num_cu, hipStream_t s) {
     constexpr int TILE = 64 * B;
     const int64_t upper = (static_cast<int64_t>(p.M) / TILE + (p.M < p.E ? p.M : p.E)) * ((p.N + TILE - 1) / TILE);
-    const dim3 grid(static_cast<unsigned>(upper < num_cu ? upper : num_cu));
+    const dim3 grid(static_cast<unsigned>(upper < num_cu && p.group == 0 ? upper : num_cu));
     if (p.ws) hipLaunchKernelGGL((int8_tile_kernel<B, true>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((int8_tile_kernel<B, false>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
@@ -813,21 +903,18 @@ hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
     // No expert of a batch of few rows has a tile.  Small tiles where the rows would make fewer large ones than CUs.
     const int64_t large = static_cast<int64_t>(p.M) / 256 * ((p.N + 255) / 256);
     g.tile = p.M <= 64 ? 0 : (large < num_cu ? 128 : 256);
+    // Small tiles and the experts without any share a launch where LDS holds 32 rows of the summed width.
+    const int panel = I8_RING / (p.width * 32) * 32;
+    g.group = g.tile == 128 ? (panel < I8_GROUP ? panel : I8_GROUP) : 0;
     if (g.tile) {
         const hipError_t st = g.tile == 256 ? launch_tiles<4>(g, num_cu, s) : launch_tiles<2>(g, num_cu, s);
-        if (st != hipSuccess) return st;
+        if (st != hipSuccess || g.group) return st;
     }
+    g.group = I8_GROUP;
     const int64_t nblocks = (p.N + 31) / 32;
-    if (g.tile == 128 && p.width * 32 <= I8_RING) {
-        g.group = I8_RING / (p.width * 32) * 32;
-        if (g.group > I8_GROUP) g.group = I8_GROUP;
-        hipLaunchKernelGGL((int8_stream_kernel<true>), dim3(static_cast<unsigned>(num_cu)), dim3(512), 0, s, g);
-    } else {
-        g.group = I8_GROUP;
-        const int64_t groups = static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E);
-        const int64_t upper = (groups * nblocks + 3) / 4, most = static_cast<int64_t>(num_cu) * 3;
-        hipLaunchKernelGGL((int8_stream_kernel<false>), dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
-    }
+    const int64_t groups = static_cast<int64_t>(p.M) / I8_GROUP + (p.M < p.E ? p.M : p.E);
+    const int64_t upper = (groups * nblocks + 3) / 4, most = static_cast<int64_t>(num_cu) * 3;
+    hipLaunchKernelGGL(int8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, g);
     return hipGetLastError();
 }
 
