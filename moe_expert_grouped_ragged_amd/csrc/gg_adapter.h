@@ -13,9 +13,11 @@ constexpr int AD_WCOLS = 128;    // columns a wavefront of the backward pass own
 // Rank padded to the matrix instruction's tiles: 16, 32 or 64.
 inline int ad_rank_p(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
 // Column groups (AD_WCOLS each) of a workgroup of the output-side backward
-// kernel: at most (its registers hold the columns' part of db), and at least;
-// wavefronts that share a group, 32 ranks each; chunks of N columns.
-constexpr int ad_groups(int rp) { return rp <= 32 ? 8 : 4; }
+// kernel: at most (its registers hold the columns' part of db, LDS their rows), and at least;
+// wavefronts that share a group, 32 ranks each; chunks of N columns.  Up to rank 16 two workgroups of
+// four groups share a CU (32768 rows, N 1536: the backward 157 us with eight groups, 146 us); at rank 32 the
+// chunks' parts of du, twice as many, cost more than that gives (131072 rows, N 2048: 401 us, 385 us with eight).
+constexpr int ad_groups(int rp) { return rp == 32 ? 8 : 4; }
 constexpr int ad_groups_min(int rp) { return ad_groups(rp) * 3 / 4; }
 constexpr int ad_split(int rp) { return rp <= 32 ? 1 : 2; }
 inline int ad_chunks(int n, int rp) { return (n + ad_groups(rp) * AD_WCOLS - 1) / (ad_groups(rp) * AD_WCOLS); }
@@ -35,7 +37,7 @@ struct AdapterParams {
     float* da;                // [E][r][K]
     float* db;                // [E][N][r]
     int accumulate;           // da and db are added to
-    int rows1, rows2;         // rows of a unit of the output-side and of the input-side kernel
+    int rows1, rows2;         // rows of a unit of the output-side and of the input-side kernel, about
     float* du_part;           // [chunks of N][blocks * 32][rp]: partial sums of du over the columns of a chunk
     uint16_t* du;             // [blocks][32][max(rp, 32)] bf16
     uint16_t* du_t;           // [blocks][3][rp][32] bf16: du as the sum of three parts, transposed

@@ -23,8 +23,9 @@ int check_adapter_shape(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     return GG_OK;
 }
 
-// Rows of one unit of a backward kernel whose workgroups each own one of
-// `chunks` column chunks: about `units` units when the rows are spread evenly,
+// Rows of a unit of a backward kernel whose workgroups each own one of
+// `chunks` column chunks (about: an expert's rows are divided evenly): about
+// `units` units when the rows are spread evenly,
 // and at least 256 rows, so that the fp32 part a unit leaves behind stays
 // small next to the rows it reads; at most 2^30, which the kernels count in 32 bits.
 int64_t unit_rows(int64_t M, int64_t chunks, int64_t units) {
@@ -42,7 +43,9 @@ Workspace workspace_of(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     Workspace w{};
     const int64_t rp = ad_rank_p(static_cast<int>(r));
     const int64_t chunks = ad_chunks(static_cast<int>(N), static_cast<int>(rp));
-    w.rows1 = unit_rows(M, chunks, 512);
+    // two workgroups of the smallest rank share a CU, and its parts are small (131072 rows, Zipf, N 2048:
+    // rank 16 338 us, 349 us with half the units; rank 32 402 us and 393 us)
+    w.rows1 = unit_rows(M, chunks, rp == 16 ? 1024 : 512);
     w.rows2 = unit_rows(M, (K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS), 1024);
     w.blocks = M / AD_BLK + (M < E ? M : E);
     size_t at = 0;
@@ -54,7 +57,7 @@ Workspace workspace_of(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     w.du_part = take(chunks * w.blocks * AD_BLK * rp * 4);
     w.du = take(w.blocks * AD_BLK * (rp < 32 ? 32 : rp) * 2);
     w.du_t = take(w.blocks * AD_BLK * rp * 6);
-    // an expert with m > rows has ceil(m / rows) < 2 m / rows parts
+    // an expert of several units has at most m / rows + 1/2 of them, and at least 3/2 rows
     w.db_part = take(M > w.rows1 ? 2 * M / w.rows1 * N * r * 4 : 0);
     w.da_part = take(M > w.rows2 ? 2 * M / w.rows2 * K * r * 4 : 0);
     w.total = at;
