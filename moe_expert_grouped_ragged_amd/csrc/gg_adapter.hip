@@ -45,8 +45,8 @@ __device__ __forceinline__ uint4 gather8(const uint16_t* p, int64_t ld, int n) {
 // columns of four token rows, and base and y move as 256-byte row segments of
 // 16 lanes without passing through LDS.  With few row blocks the columns of y
 // are split over workgroups, which each compute U again.
-// Bound by HBM in large batches (262144 rows, K = N = 4096, rank 32: 1.30 ms, 5.0
-// TB/s of x, base and y), by the chain offsets - x and a - b in small ones (one token's 8
+// Bound by HBM in large batches (262144 rows, K = N = 4096, rank 32: 1.30 ms, 5.6
+// TB/s), by the chain offsets - x and a - b in small ones (one token's 8
 // rows: 10 us; 2880 rows over 128 experts, K 2688, N 3712, rank 12: 31 us, 2.5 TB/s).
 constexpr int af_waves(int rb) { return rb == 2 ? 8 : 4; }
 
@@ -290,9 +290,9 @@ __global__ __launch_bounds__(af_waves(RB) * 64, 2) void adapter_forward_kernel(c
 // loads the same 8 columns of 8 rows (256-byte row segments across 16 lanes)
 // and pairs them up by byte permutes, so its 8 operands are 8 columns with 8
 // rows each.
-// Measured on 262144 rows, K 2048, N 4096, rank 64: 1 takes 0.66 ms (3.3 TB/s; two waves
-// share a tile there, and LDS and the barrier of each block bound it), 2 takes
-// 0.15 ms, 3 0.72 ms (4.5 TB/s of x, base and dx), 4 0.04 ms.
+// Measured on 262144 rows, K 2048, N 4096, rank 64, and the memory traffic with it: 1 takes 0.66 ms
+// (3.2 GB, 4.9 TB/s: dy, and 0.5 GB of du's parts), 2 takes 0.16 ms, 3 0.72 ms (4.0 GB, 5.6 TB/s: x, base, dx,
+// and du once for each 512 columns), 4 0.04 ms.  At rank 16 (32768 rows, K 2048, N 1536) 29, 5, 86 and 9 us.
 __device__ __forceinline__ void transpose8(const uint4 (&in)[8], uint4 (&out)[8]) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
