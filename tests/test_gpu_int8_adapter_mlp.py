@@ -159,3 +159,35 @@ def test_example_learns_and_serves():
     assert all(np.isfinite(losses)) and losses[-1] < losses[0]
     # the same row in another batch: fp32 sums of the adapters may split otherwise, one bf16 step of the largest value
     assert float((token.float() - batch.float()).abs().max()) <= 2.0 ** -7 * float(batch.float().abs().max())
+
+
+def test_no_rows():
+    """A batch without rows: an empty output, an empty input gradient, zero adapter gradients."""
+    gg, c, ad, _ = _setup([3, 0], 64, 32, 4, 64)
+    w = gg.int8_experts(c.w1.to(DEV), c.w2.to(DEV))
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    p = [t.to(DEV).requires_grad_(True) for t in ad]
+    off = torch.zeros(3, dtype=torch.int64, device=DEV)
+    y = gg.Int8AdapterExpertMLP.apply(x, off, w, *p, 0.5)
+    y.backward(torch.empty_like(y))
+    assert y.shape == (0, 64) and x.grad.shape == (0, 64)
+    assert all(torch.count_nonzero(t.grad) == 0 for t in p)
+
+
+def test_refusals():
+    gg, c, ad, off = _setup([3, 5], 64, 32, 4, 65)
+    w1, w2 = c.w1.to(DEV), c.w2.to(DEV)
+    for a, b in ((w1.clone().requires_grad_(True), w2), (w1[:, :-8], w2), (w1[0], w2), (w1, w2[:1])):
+        with pytest.raises(ValueError):
+            gg.int8_experts(a, b)
+    w = gg.int8_experts(w1, w2)
+    x, p = c.x.to(DEV), [t.to(DEV) for t in ad]
+    for i, bad in ((0, p[0].float()), (1, p[1][:, :-8]), (2, p[2][:1]), (3, p[3].cpu())):
+        q = list(p)
+        q[i] = bad
+        with pytest.raises(ValueError):
+            gg.Int8AdapterExpertMLP.apply(x, off, w, *q, 0.5)
+    with pytest.raises(ValueError):
+        gg.Int8AdapterExpertMLP.apply(x[:, :-8], off, w, *p, 0.5)
+    with pytest.raises(ValueError):
+        gg.Int8AdapterExpertMLP.apply(x, off, w, *p, 0.5, "relu")
