@@ -51,6 +51,8 @@ There is no fallback: if libgg.so is missing, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
@@ -572,14 +574,26 @@ def gg_scale_rows_backward(dxs: torch.Tensor, x: torch.Tensor, probs: torch.Tens
     return dx, dprobs
 
 
-def _used_on(stream: Optional[torch.cuda.Stream], pairs) -> None:
-    """Tells the allocator that the memory it gave out here (pairs of a tensor
-    and the caller's, None where there was none) is used on another stream than
-    the current one, so that it is not given out again before that work is done."""
-    if stream is not None:
-        for new, given in pairs:
-            if new is not None and given is None:
-                new.record_stream(stream)
+def _allocates_on_stream(fn):
+    """For a call with a `stream`: what it allocates comes from that stream's
+    memory, so nothing queued elsewhere still uses it when the call's kernels run, and
+    what it returns is not given out again before the current stream's work on it is done."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = kw.get("stream") if len(args) <= at else args[at]
+        if stream is None:
+            return fn(*args, **kw)
+        current = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(current)
+        return out
+
+    return call
 
 
 def _typed_cuda(t: torch.Tensor, dtype, name: str, shape, device) -> torch.Tensor:
@@ -604,6 +618,7 @@ def int8_workspace_bytes(M: int, width: int) -> int:
     return int(lib.gg_int8_workspace_bytes(M, width))
 
 
+@_allocates_on_stream
 def gg_int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
                           stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Rows of x (bf16 [M, K]) to int8 with one scale each: (q int8 [M, K], s
@@ -613,10 +628,8 @@ def gg_int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: 
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    given = q, s
     q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else _typed_cuda(q, torch.int8, "q", (M, K), x.device)
     s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else _probs_cuda(s, M, x.device, "s")
-    _used_on(stream, zip((q, s), given))
     _check(lib.gg_int8_quantize_rows(x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(), _stream_ptr(stream, x.device)),
            "gg_int8_quantize_rows")
     return q, s
@@ -629,16 +642,15 @@ def _int8_pack(wq, ws, transposed, packed, stream):
     need = int8_packed_bytes(E, N, K, transposed)
     if need == 0:
         raise ValueError(f"E={E}, N={N}, K={K} is outside the limits of the int8 calls")
-    given = packed
     if packed is None:
         packed = torch.empty(need, dtype=torch.uint8, device=wq.device)
     _workspace(packed, need, wq.device)
-    _used_on(stream, [(packed, given)])
     _check(lib.gg_int8_pack(wq.data_ptr(), ws.data_ptr(), E, N, K, int(transposed), packed.data_ptr(),
                             packed.numel() * packed.element_size(), _stream_ptr(stream, wq.device)), "gg_int8_pack")
     return packed
 
 
+@_allocates_on_stream
 def gg_int8_pack(wq: torch.Tensor, ws: torch.Tensor, packed: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """8-bit weights wq (int8 [E, N, K]) with channel scales ws (float32
@@ -647,6 +659,7 @@ def gg_int8_pack(wq: torch.Tensor, ws: torch.Tensor, packed: Optional[torch.Tens
     return _int8_pack(wq, ws, False, packed, stream)
 
 
+@_allocates_on_stream
 def gg_int8_pack_transposed(wq: torch.Tensor, ws: torch.Tensor, packed: Optional[torch.Tensor] = None,
                             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The same weights laid out for gg_int8_dgrad (int8_packed_bytes(E, N, K, True) bytes)."""
@@ -664,6 +677,7 @@ def _int8_packed(packed: torch.Tensor, E: int, N: int, K: int, transposed: bool,
     return packed
 
 
+@_allocates_on_stream
 def gg_int8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
                     activation=None, save_a: bool = False, a_out: Optional[torch.Tensor] = None,
                     y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -682,18 +696,17 @@ def gg_int8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor
         _bf16_cuda(a_out, "a_out", shape=(M, K), device=dev)
     if act == GG_ACT_NONE and (save_a or a_out is not None):
         raise ValueError("A exists with an activation only")
-    given = workspace, a_out, y
     workspace = _workspace(workspace, int8_workspace_bytes(M, K), dev)
     if a_out is None and save_a:
         a_out = _out(None, (M, K), "a_out", dev)
     y = _out(y, (M, N), "y", dev)
-    _used_on(stream, zip((workspace, a_out, y), given))
     _check(lib.gg_int8_forward(x.data_ptr(), off.data_ptr(), M, packed.data_ptr(), E, N, K, act, _ptr(a_out),
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), y.data_ptr(),
                                _stream_ptr(stream, dev)), "gg_int8_forward")
     return y, a_out
 
 
+@_allocates_on_stream
 def gg_int8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
                   h1: Optional[torch.Tensor] = None, activation=None, save_dh1: bool = True,
                   dh1_out: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
@@ -717,12 +730,10 @@ def gg_int8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
         if h1 is None:
             raise ValueError("dH1 exists with an activation only")
         _bf16_cuda(dh1_out, "dh1_out", shape=(M, N), device=dev)
-    given = workspace, dh1_out, dx
     workspace = _workspace(workspace, int8_workspace_bytes(M, N), dev)
     if dh1_out is None and h1 is not None and save_dh1:
         dh1_out = _out(None, (M, N), "dh1_out", dev)
     dx = _out(dx, (M, K), "dx", dev)
-    _used_on(stream, zip((workspace, dh1_out, dx), given))
     _check(lib.gg_int8_dgrad(dy.data_ptr(), _ptr(h1), off.data_ptr(), M, packed.data_ptr(), E, N, K, act,
                              _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                              dx.data_ptr(), _stream_ptr(stream, dev)), "gg_int8_dgrad")
@@ -752,6 +763,7 @@ def _adapter(x, offsets, a, b):
     return x.shape[0], E, b.shape[1], K, r
 
 
+@_allocates_on_stream
 def gg_adapter_forward(x: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: float,
                        base: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None,
                        y: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
@@ -765,16 +777,15 @@ def gg_adapter_forward(x: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor, 
         _bf16_cuda(base, "base", shape=(M, N), device=dev)
     if u is not None:
         _bf16_cuda(u, "u", shape=(M, r), device=dev)
-    given = y, u
     y = _out(y, (M, N), "y", dev)
     u = _out(u, (M, r), "u", dev)
-    _used_on(stream, zip((y, u), given))
     _check(lib.gg_adapter_forward(x.data_ptr(), offsets.data_ptr(), M, a.data_ptr(), b.data_ptr(), E, N, K, r, scale,
                                   _ptr(base), u.data_ptr(), y.data_ptr(), _stream_ptr(stream, dev)),
            "gg_adapter_forward")
     return y, u
 
 
+@_allocates_on_stream
 def gg_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor,
                         b: torch.Tensor, scale: float, base: Optional[torch.Tensor] = None,
                         dx: Optional[torch.Tensor] = None, da: Optional[torch.Tensor] = None,
@@ -799,12 +810,10 @@ def gg_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, offs
         _typed_cuda(db, torch.float32, "db", (E, N, r), dev)
     if dx is not None:
         _bf16_cuda(dx, "dx", shape=(M, K), device=dev)
-    given = workspace, dx, da, db
     workspace = _workspace(workspace, adapter_workspace_bytes(M, E, N, K, r), dev)
     dx = _out(dx, (M, K), "dx", dev)
     da = torch.empty(E, r, K, dtype=torch.float32, device=dev) if da is None else da
     db = torch.empty(E, N, r, dtype=torch.float32, device=dev) if db is None else db
-    _used_on(stream, zip((workspace, dx, da, db), given))
     _check(lib.gg_adapter_backward(dy.data_ptr(), x.data_ptr(), u.data_ptr(), offsets.data_ptr(), M, a.data_ptr(),
                                    b.data_ptr(), E, N, K, r, scale, _ptr(base), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), dx.data_ptr(), da.data_ptr(),

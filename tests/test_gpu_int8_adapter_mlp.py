@@ -191,3 +191,23 @@ def test_refusals():
         gg.Int8AdapterExpertMLP.apply(x[:, :-8], off, w, *p, 0.5)
     with pytest.raises(ValueError):
         gg.Int8AdapterExpertMLP.apply(x, off, w, *p, 0.5, "relu")
+
+
+def test_outputs_allocated_for_a_given_stream():
+    """Memory that is free for the current stream, but whose last reader is still queued on it, is not given to a
+    call on another stream: the reader's copy keeps its value."""
+    gg, c, ad, off = _setup([40, 0, 30, 7], 512, 256, 8, 66)
+    x, w = c.x.to(DEV), gg.int8_experts(c.w1.to(DEV), c.w2.to(DEV))
+    st = torch.cuda.Stream()
+    want, _ = gg.gg_int8_forward(x, off, w.fc1, c.E, 512, 512)
+    busy = torch.ones(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        busy = busy @ busy * 2.0 ** -12                       # keeps the current stream busy
+    old = torch.full((c.M, 512), 2.0, dtype=torch.bfloat16, device=DEV)
+    copy = old.clone()                                        # reads `old`, later
+    del old
+    y, _ = gg.gg_int8_forward(x, off, w.fc1, c.E, 512, 512, stream=st)
+    st.synchronize()
+    torch.cuda.synchronize()
+    assert bitwise_equal(y, want) and bool((copy == 2.0).all())
