@@ -303,7 +303,7 @@ size_t gg_int8_workspace_bytes(int64_t M, int64_t width);
 /* Forward: x [M][K] with GG_ACT_NONE, or H1 [M][2K] with an activation, in
  * which case a_out (may be NULL) receives A [M][K].  packed: gg_int8_pack(...,
  * transposed = 0).  y [M][N].  One launch quantizes; the product is one, or two
- * for large batches (tiles, then the rows they leave). */
+ * for wide sums (tiles, then the rows they leave). */
 int gg_int8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed,
                     int64_t E, int64_t N, int64_t K, int activation, void* a_out,
                     void* workspace, size_t workspace_bytes, void* y, hipStream_t stream);

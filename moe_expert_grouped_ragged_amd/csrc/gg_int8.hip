@@ -525,7 +525,7 @@ __device__ __forceinline__ void i8_stream_blocks(const Int8Params& p, const int8
 // what 128 KiB hold of the summed width): read by every wave from memory they
 // cost nearly as much of the load path as the weights (128 experts of 22 rows,
 // K 2688, N 3712, quantization included: 300 us from memory, 244 us here, 5.6 TB/s in this kernel).
-// Otherwise, for few rows and for what large tiles leave: items of four blocks, a wave each, in turn.
+// Otherwise, for few rows in all and for wide ones: items of four blocks, a wave each, in turn.
 template <bool PANEL, bool SCALED>
 __device__ __forceinline__ void i8_stream_list(const Int8Params& p, int* s_off, int* s_pre, int8_t* s_panel) {
     constexpr int W = 4;
@@ -845,11 +845,9 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(const Int8Params p) {
             }
         });
     }
-    if constexpr (B == 2) {
-        if (p.group == 0) return;   // another launch's
-        __syncthreads();
-        i8_stream_list<true, SCALED>(p, s_off, s_pre, s_ring);
-    }
+    if (p.group == 0) return;   // another launch's
+    __syncthreads();
+    i8_stream_list<true, SCALED>(p, s_off, s_pre, s_ring);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -907,9 +905,11 @@ hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
     // CUs (128 experts of 80 rows, K 2048, N 1536: 128 us, 210 us with large ones; of 200 rows 214 us, and 169 us).
     const int64_t large = static_cast<int64_t>(p.M) / 256 * ((p.N + 255) / 256);
     g.tile = p.M <= 64 ? 0 : (large < num_cu ? 128 : 256);
-    // Small tiles and the experts without any share a launch where LDS holds 32 rows of the summed width.
-    const int panel = I8_RING / (p.width * 32) * 32;
-    g.group = g.tile == 128 ? (panel < I8_GROUP ? panel : I8_GROUP) : 0;
+    // Tiles and the rows they leave share a launch where LDS holds 32 rows of the summed width, or, of what large
+    // tiles leave, 64, so that few weights are read twice (128 experts of 300 rows, K 2048, N 1536: 244 us, 269 us in
+    // two launches).
+    const int panel = I8_RING / (p.width * 32) * 32, least = g.tile == 256 ? 64 : 32;
+    g.group = g.tile == 0 || panel < least ? 0 : (panel < I8_GROUP ? panel : I8_GROUP);
     if (g.tile) {
         const hipError_t st = g.tile == 256 ? launch_tiles<4>(g, num_cu, s) : launch_tiles<2>(g, num_cu, s);
         if (st != hipSuccess || g.group) return st;
