@@ -39,3 +39,8 @@ def test_dgrad_sizes(K, N, act):
     # here the output columns are K's and the sum is over N's
     counts, _, _, lead, tail = next(c for c in CASES if c[1:3] == (K, N))
     _dgrad(counts, N, K, lead, tail, act)
+
+
+def test_large_tiles_of_wide_sums():
+    """Large tiles, and what they leave (76 and 4 rows) in a launch of its own: LDS holds too few rows of the sum."""
+    _forward([1100, 1240, 260], 2056, 6416, 0, 0, None)
