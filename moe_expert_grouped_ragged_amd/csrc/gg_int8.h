@@ -53,7 +53,7 @@ struct Int8Params {
     int M, E, N;             // N: output columns, a multiple of 8
     uint16_t* out;           // [M][N]
     int tile;                // rows of a tile, or 0: no tiles (set by the launcher)
-    int group;               // rows of a streaming item, at most (set by the launcher)
+    int group;               // rows of a streaming item, at most; 0: this launch has none (set by the launcher)
 };
 
 hipError_t launch_quant_rows(QuantMode mode, const QuantParams& p, int num_cu, hipStream_t s);

@@ -576,7 +576,7 @@ __global__ __launch_bounds__(256) void int8_stream_kernel(const Int8Params p) {
 // registers; B = 2 (128 x 128) gives four times the tiles where there would
 // be fewer large ones than CUs (777 rows over 5 experts, K 1048, N 2056: 21 us, 30 us with B = 4).
 // With B = 4 a tile costs about 0.83 us a stage and 8.6 us besides: 262144 rows, K = N = 4096, 3.9 ms, 2250
-// TOP/s, what the chip's power leaves for random operands; 131072 rows, K 768, N 2048, 340 us, 1210 TOP/s.
+// TOP/s, what the chip's power leaves for random operands; 131072 rows, K 768, N 2048, 340 us, 1210 TOP/s in the tiles.
 // Rows and weights stream into an LDS ring (128 KiB: four stages, or eight)
 // of 64-byte stages by LDS-DMA, all but one of them ahead: the rows, 16-byte
 // chunk c of row r at c ^ ((r >> 2) & 3), and the weights as they lie in
