@@ -56,6 +56,19 @@ struct Int8Params {
     int group;               // rows of a streaming item, at most; 0: this launch has none (set by the launcher)
 };
 
+// How a wave of the quantization takes Y (1 or 2) rows of [lo, hi) at a time: from i8_first_row, in steps of Y, while
+// below hi.  Pairs start at an even row, so that the two rows share their lines; a pair of which one row lies
+// outside holds its other row twice.  No rows (lo >= hi): no step at all, also where lo is odd.
+template <int Y>
+__host__ __device__ inline int i8_first_row(int lo, int hi) {
+    return Y == 2 && lo < hi ? lo & ~1 : lo;
+}
+template <int Y>
+__host__ __device__ inline void i8_rows_at(int64_t r0, int lo, int hi, int64_t (&row)[Y]) {
+    row[0] = r0 < lo ? r0 + 1 : r0;
+    if (Y == 2) row[Y - 1] = r0 + 1 < hi ? r0 + 1 : r0;
+}
+
 hipError_t launch_quant_rows(QuantMode mode, const QuantParams& p, int num_cu, hipStream_t s);
 hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s);
 // q [E][N][K] and s [E][N] into the packed layout: W = q_e (rows N, summed K), or with

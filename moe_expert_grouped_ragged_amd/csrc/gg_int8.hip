@@ -166,12 +166,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const QuantParams p) {
         hi = s_off[p.E];
     }
     const int units = p.K / (8 * HALVES), half = p.K / 2;
-    // an even first row: the two rows of a pair then share their lines
-    for (int64_t r0 = (Y == 2 ? lo & ~1 : lo) + Y * (static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6)); r0 < hi;
+    for (int64_t r0 = i8_first_row<Y>(lo, hi) + Y * (static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6)); r0 < hi;
          r0 += static_cast<int64_t>(gridDim.x) * 4 * Y) {
         int64_t row[Y];
-        row[0] = r0 < lo ? r0 + 1 : r0;
-        if constexpr (Y == 2) row[1] = r0 + 1 < hi ? r0 + 1 : r0;
+        i8_rows_at<Y>(r0, lo, hi, row);
         const bool keep = p.v_out != nullptr;
         const float* cs[Y] = {};
         if constexpr (SCALES) {
