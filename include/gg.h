@@ -330,6 +330,8 @@ int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_
  * bf16) and kept whole, as three bf16 parts, for da.  Every sum has a fixed order:
  * equal calls give equal bits.  da and db are written for every expert
  * (zeros without rows), or, with accumulate != 0, added to.
+ * An infinity or NaN in dy reaches the gradients as the formulas say; an
+ * infinity in x may reach da as NaN (the parts of du multiply it one by one).
  *
  * x, u, y, dy, dx, a, b: DEVICE bf16; da, db: DEVICE fp32; 16-byte aligned.
  * Limits: 1 <= E <= GG_MAX_EXPERTS; N and K positive multiples of 8 below

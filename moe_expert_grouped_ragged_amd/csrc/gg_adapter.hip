@@ -586,9 +586,11 @@ __global__ __launch_bounds__(256) void adapter_du_kernel(const AdapterParams p) 
             uint32_t hi[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float d = v[x] * p.scale;
+                // ranks that do not exist are zero: the padded operands give them NaN where dy is infinite
+                const float d = c + x < p.r ? v[x] * p.scale : 0.0f;
                 hi[x] = f2bf(d);
-                const float rest = d - bf2f(hi[x]);
+                // an infinity is its first part alone: infinity - infinity is NaN
+                const float rest = __builtin_isinf(bf2f(hi[x])) ? 0.0f : d - bf2f(hi[x]);
                 const uint16_t mid = f2bf(rest);
                 s_t[0][nb * RP + c + x][row] = static_cast<uint16_t>(hi[x]);
                 s_t[1][nb * RP + c + x][row] = mid;
