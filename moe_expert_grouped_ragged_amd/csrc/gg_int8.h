@@ -56,6 +56,39 @@ struct Int8Params {
     int group;               // rows of a streaming item, at most; 0: this launch has none (set by the launcher)
 };
 
+constexpr int I8_GROUP = 96;          // rows of a streaming item, at most
+constexpr int I8_RING = 128 * 1024;   // LDS for operands
+
+// Which tiles a product of M rows over E experts, N columns and a summed width takes (rows of a tile, 0: none), and
+// how many rows a streaming item in the tiles' launch has at most (0: the streaming items have a launch of their own).
+//
+// No expert of a batch of few rows has a tile.  Small tiles where the rows would make fewer large ones than
+// CUs (8 experts of 300 rows, K 1048, N 2056: 28 us, 44 us with large ones), and from 80 to 119 rows an expert on average: such experts fill a small tile, and less than half of a large
+// one, or stream.  Times in us, small and large tiles, 128 experts, uniform:
+//   rows an expert          64         72         80         96        116        132        200
+//   K 4096, N 4096     650  702   516  738   490  821   475  670   506  563   664  557   890  629
+//   K 2688, N 3712     405  406   338  433   318  472   317  444   339  376   427  379   561  429
+//   K 768, N 2048       77   63    82   65    82   83    75   90    84   93   109   88   137   99
+// Below, 36 rows: 413 and 329 (K 2688, N 3712: LDS holds 32 rows, so small tiles' launch reads the weights of 33
+// twice).  Zipf-distributed experts of 72 to 120 rows on average: within 7% of each other either way.
+//
+// Tiles and the rows they leave share a launch where LDS holds 32 rows of the summed width, or, of what large
+// tiles leave, 64, so that few weights are read twice (128 experts of 300 rows, K 2048, N 1536: 244 us, 269 us in
+// two launches).
+struct Int8Plan {
+    int tile, group;
+};
+inline Int8Plan i8_plan(int M, int E, int N, int width, int num_cu) {
+    const int64_t large = static_cast<int64_t>(M) / 256 * ((N + 255) / 256);
+    const int64_t owners = M < E ? M : E;
+    const bool half = M >= 80 * owners && M < 120 * owners;
+    Int8Plan plan;
+    plan.tile = M <= 64 ? 0 : (large < num_cu || half ? 128 : 256);
+    const int panel = I8_RING / (width * 32) * 32, least = plan.tile == 256 ? 64 : 32;
+    plan.group = plan.tile == 0 || panel < least ? 0 : (panel < I8_GROUP ? panel : I8_GROUP);
+    return plan;
+}
+
 // How a wave of the quantization takes Y (1 or 2) rows of [lo, hi) at a time: from i8_first_row, in steps of Y, while
 // below hi.  Pairs start at an even row, so that the two rows share their lines; a pair of which one row lies
 // outside holds its other row twice.  No rows (lo >= hi): no step at all, also where lo is odd.

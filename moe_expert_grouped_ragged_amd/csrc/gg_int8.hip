@@ -330,9 +330,6 @@ __global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __re
 // Streaming items: up to 96 rows of one expert x a range of output columns; a
 // wave takes 32 columns at a time over the whole summed dimension, its weights
 // one coalesced 1 KiB load a step.  Bound by the weights' bytes.
-constexpr int I8_GROUP = 96;   // rows of a streaming item, at most
-constexpr int I8_RING = 128 * 1024;   // LDS for operands
-
 // Rows of an expert that tiles of `tile` rows cover (0: there are no tiles).  256-row tiles leave a remainder
 // of at most 96 rows (32768 rows over 32 experts, K 1536, N 2048: 170 us, 174 us with at most 32); 128-row tiles,
 // which run where there is little work, take all of an expert of more than 64 rows, or nothing (128 experts of
@@ -899,15 +896,9 @@ static hipError_t launch_tiles(const Int8Params& p, int num_cu, hipStream_t s) {
 
 hipError_t launch_int8_gemm(const Int8Params& p, int num_cu, hipStream_t s) {
     Int8Params g = p;
-    // No expert of a batch of few rows has a tile.  Small tiles where the rows would make fewer large ones than
-    // CUs (128 experts of 80 rows, K 2048, N 1536: 128 us, 210 us with large ones; of 200 rows 214 us, and 169 us).
-    const int64_t large = static_cast<int64_t>(p.M) / 256 * ((p.N + 255) / 256);
-    g.tile = p.M <= 64 ? 0 : (large < num_cu ? 128 : 256);
-    // Tiles and the rows they leave share a launch where LDS holds 32 rows of the summed width, or, of what large
-    // tiles leave, 64, so that few weights are read twice (128 experts of 300 rows, K 2048, N 1536: 244 us, 269 us in
-    // two launches).
-    const int panel = I8_RING / (p.width * 32) * 32, least = g.tile == 256 ? 64 : 32;
-    g.group = g.tile == 0 || panel < least ? 0 : (panel < I8_GROUP ? panel : I8_GROUP);
+    const Int8Plan plan = i8_plan(p.M, p.E, p.N, p.width, num_cu);
+    g.tile = plan.tile;
+    g.group = plan.group;
     if (g.tile) {
         const hipError_t st = g.tile == 256 ? launch_tiles<4>(g, num_cu, s) : launch_tiles<2>(g, num_cu, s);
         if (st != hipSuccess || g.group) return st;
