@@ -18,12 +18,14 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 //
 // Per row: top = max|v|, s = top / 127, q = rint(127 v / top) to nearest even;
 // a zero row gives s = 0, q = 0, and a row with a NaN or infinity s = NaN,
-// q = 0, so that its products are NaN and no other row's are.  127 v is exact
-// for bf16 v, and 127 v / top is then either a tie exactly or at least 1/512
-// away from one, so the quotient (a product with 1/top and one residual
-// correction) rounds as the exact quotient does.  Rows whose top is far from
-// one are scaled by a power of two first, so 1/top neither overflows nor
-// loses bits.
+// q = 0, so that its products are NaN and no other row's are.  The quotient (a
+// product with 1/top and one residual correction) rounds as the exact one does:
+// with v = a 2^i and top = b 2^j, 8 bits each, 127 v is exact, and where
+// 127 v / top is not a tie k + 1/2 it differs from one by
+// |254 a - (2k + 1) b 2^d| / (2 b 2^d) >= 1 / (2 b 2^d) (d = j - i), which is the
+// quotient divided by 254 a, above 2^-16 of it; the corrected quotient is within 2^-23.
+// Rows whose top is far from one are scaled by a power of two first, so 1/top
+// neither overflows nor loses bits.
 //
 // A wavefront takes a row at a time; its bf16 values stay in registers between
 // the maximum and the rounding (rows of more than NC * 64 units are computed
@@ -325,11 +327,15 @@ __global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __re
 // The sums are exact in 32-bit integers, so the kernels below give the same
 // bits.  The rows of a large expert run as tiles (the last may be partial);
 // a remainder of few rows (all rows of a small expert) runs as streaming
-// items, which read each weight byte once for all of them.
+// items.
 //
-// Streaming items: up to 96 rows of one expert x a range of output columns; a
-// wave takes 32 columns at a time over the whole summed dimension, its weights
+// Streaming items: a group of rows of one expert x a range of output columns,
+// for which each weight byte is read once.  A group holds up to 96 rows, or in
+// the tiles' launch what LDS holds of the summed width where that is less (64 rows up to
+// 2048 columns, 32 up to 4096): an expert of more rows reads its weights for each group.
+// A wave takes 32 columns at a time over the whole summed dimension, its weights
 // one coalesced 1 KiB load a step.  Bound by the weights' bytes.
+
 // Rows of an expert that tiles of `tile` rows cover (0: there are no tiles).  256-row tiles leave a remainder
 // of at most 96 rows (32768 rows over 32 experts, K 1536, N 2048: 170 us, 174 us with at most 32); 128-row tiles,
 // which run where there is little work, take all of an expert of more than 64 rows, or nothing (128 experts of

@@ -19,7 +19,7 @@ int check_int8_shape(int64_t M, int64_t E, int64_t N, int64_t K) {
     if (E < 1 || E > GG_MAX_EXPERTS) return GG_ERR_INVALID_ARGUMENT;
     if (N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 || N > GG_INT8_MAX_SUM || K > GG_INT8_MAX_SUM)
         return GG_ERR_INVALID_ARGUMENT;
-    // the kernels address one packed matrix with 32-bit byte offsets
+    // the declared limit of one packed matrix; the kernels themselves address it with 64 bits
     if (i8_rows_p(N) * i8_cont_p(K) >= (int64_t(1) << 31) || i8_rows_p(K) * i8_cont_p(N) >= (int64_t(1) << 31))
         return GG_ERR_INVALID_ARGUMENT;
     if (M < 0 || M >= (int64_t(1) << 31)) return GG_ERR_INVALID_ARGUMENT;
