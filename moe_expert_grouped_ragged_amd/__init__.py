@@ -897,8 +897,9 @@ class Int8AdapterExpertMLP(torch.autograd.Function):
 
     apply(x, offsets, experts, a1, b1, a2, b2, scale, activation) with experts
     from int8_experts, a1 [E, r1, H], b1 [E, 2F, r1], a2 [E, r2, F],
-    b2 [E, H, r2] (bf16).  The backward gives dX and the adapters' gradients;
-    the base weights have none."""
+    b2 [E, H, r2] (bf16).  The backward gives dX and the adapters' gradients,
+    those that are needed (FC1's part is left out where neither x, a1 nor b1
+    need one); the base weights have none."""
 
     @staticmethod
     def forward(ctx, x, offsets, experts, a1, b1, a2, b2, scale, activation="swiglu"):
@@ -916,10 +917,14 @@ class Int8AdapterExpertMLP(torch.autograd.Function):
     def backward(ctx, dy):
         x, offsets, h1, a, u1, u2, a1, b1, a2, b2 = ctx.saved_tensors
         w, scale = ctx.experts, ctx.scale
-        dy = dy.contiguous()
-        da, _ = gg_int8_dgrad(dy, offsets, w.fc2_t, w.E, w.H, w.F)
+        need = ctx.needs_input_grad
+        fc1 = need[0] or need[3] or need[4]      # something that lies before A
+        dy, da, dx, ga1, gb1 = dy.contiguous(), None, None, None, None
+        if fc1:
+            da, _ = gg_int8_dgrad(dy, offsets, w.fc2_t, w.E, w.H, w.F)
         da, ga2, gb2 = gg_adapter_backward(dy, a, u2, offsets, a2, b2, scale, base=da, dx=da)
-        dx, dh1 = gg_int8_dgrad(da, offsets, w.fc1_t, w.E, 2 * w.F, w.H, h1=h1, activation=ctx.activation)
-        dx, ga1, gb1 = gg_adapter_backward(dh1, x, u1, offsets, a1, b1, scale, base=dx, dx=dx)
-        ga1, gb1, ga2, gb2 = (g.to(torch.bfloat16) for g in (ga1, gb1, ga2, gb2))
-        return dx, None, None, ga1, gb1, ga2, gb2, None, None
+        if fc1:
+            dx, dh1 = gg_int8_dgrad(da, offsets, w.fc1_t, w.E, 2 * w.F, w.H, h1=h1, activation=ctx.activation)
+            dx, ga1, gb1 = gg_adapter_backward(dh1, x, u1, offsets, a1, b1, scale, base=dx, dx=dx)
+        grads = [g.to(torch.bfloat16) if n else None for g, n in zip((ga1, gb1, ga2, gb2), need[3:7])]
+        return dx if need[0] else None, None, None, *grads, None, None
