@@ -288,7 +288,8 @@ int gg_int8_quantize_rows(const void* x, int64_t M, int64_t K, int8_t* q, float*
  * dimensions zero-padded (output columns to a multiple of 32, the summed
  * dimension to one of 128) in the operand order of the int8 matrix
  * instruction, then the fp32 channel scales.  transposed = 0: for
- * gg_int8_forward; 1: W^T, for gg_int8_dgrad.  0 for sizes outside the limits. */
+ * gg_int8_forward; 1: W^T, for gg_int8_dgrad.  The calls cannot see which one a
+ * buffer holds.  0 for sizes outside the limits. */
 size_t gg_int8_packed_bytes(int64_t E, int64_t N, int64_t K, int transposed);
 
 /* Lay out wq (DEVICE int8 [E][N][K]) and ws (DEVICE fp32 [E][N]) as above into

@@ -647,6 +647,9 @@ def _int8_pack(wq, ws, transposed, packed, stream):
     _workspace(packed, need, wq.device)
     _check(lib.gg_int8_pack(wq.data_ptr(), ws.data_ptr(), E, N, K, int(transposed), packed.data_ptr(),
                             packed.numel() * packed.element_size(), _stream_ptr(stream, wq.device)), "gg_int8_pack")
+    if not packed.is_inference():       # those have no version
+        torch.autograd.graph.increment_version(packed)      # as for any write to it; its views see it too
+        packed._gg_int8_holds = (E, N, K, bool(transposed)), packed._version
     return packed
 
 
@@ -655,7 +658,7 @@ def gg_int8_pack(wq: torch.Tensor, ws: torch.Tensor, packed: Optional[torch.Tens
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """8-bit weights wq (int8 [E, N, K]) with channel scales ws (float32
     [E, N]), laid out once for gg_int8_forward: a byte buffer of
-    int8_packed_bytes(E, N, K)."""
+    int8_packed_bytes(E, N, K).  The tensor returned is refused where another layout is needed."""
     return _int8_pack(wq, ws, False, packed, stream)
 
 
@@ -674,6 +677,11 @@ def _int8_packed(packed: torch.Tensor, E: int, N: int, K: int, transposed: bool,
         raise ValueError(f"packed must be a contiguous tensor on {device}")
     if packed.numel() * packed.element_size() < need:
         raise ValueError(f"packed holds {packed.numel() * packed.element_size()} bytes, {need} needed")
+    # The two layouts of a matrix may be equally large: a tensor that was packed, and not written since, says what it
+    # holds (a copy or a view of one does not).
+    holds = getattr(packed, "_gg_int8_holds", None)
+    if holds is not None and holds[0] != (E, N, K, transposed) and holds[1] == packed._version:
+        raise ValueError(f"packed holds (E, N, K, transposed) = {holds[0]}, not {(E, N, K, transposed)}")
     return packed
 
 
