@@ -317,7 +317,7 @@ int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_
                   int64_t E, int64_t N, int64_t K, int activation, void* dh1_out,
                   void* workspace, size_t workspace_bytes, void* dx, hipStream_t stream);
 
-/* ---- Low-rank adapters of the experts (trainable; next to a frozen product).
+/* ---- Low-rank adapters of the experts (trainable; added to a frozen product).
  *
  * For an expert e with a_e [r][K] and b_e [N][r] (bf16), over its rows:
  *

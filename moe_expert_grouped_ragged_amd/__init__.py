@@ -29,7 +29,9 @@ input rows:
 
 Expert products over 8-bit copies of the frozen weights, tokens quantized on
 the way (half the weight bytes, twice the matrix rate), and the trainable
-low-rank adapters next to a frozen product:
+low-rank adapters added to a product's output (both products of the 8-bit MLP;
+the bf16 calls make H1 and A, and dA and dH1, in one launch each, with no place for
+an adapter between them):
 
   gg_int8_quantize_rows(x)                       -> (q, s), one scale a row
   gg_int8_pack(wq, ws) / gg_int8_pack_transposed -> laid out for forward / dgrad

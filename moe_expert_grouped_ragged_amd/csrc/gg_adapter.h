@@ -15,8 +15,9 @@ inline int ad_rank_p(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
 // Column groups (AD_WCOLS each) of a workgroup of the output-side backward
 // kernel: at most (its registers hold the columns' part of db, LDS their rows), and at least;
 // wavefronts that share a group, 32 ranks each; chunks of N columns.  Up to rank 16 two workgroups of
-// four groups share a CU (32768 rows, N 1536: the backward 157 us with eight groups, 146 us); at rank 32 the
-// chunks' parts of du, twice as many, cost more than that gives (131072 rows, N 2048: 401 us, 385 us with eight).
+// four groups share a CU (131072 rows, Zipf, N 2048: the backward 341 us, 364 us with eight; 32768 rows, N 1536: 134 us and
+// 132 us); at rank 32 the chunks' parts of du, twice as many, cost more than that gives (131072 rows: 402 us, 385 us with
+// eight).
 constexpr int ad_groups(int rp) { return rp == 32 ? 8 : 4; }
 constexpr int ad_groups_min(int rp) { return ad_groups(rp) * 3 / 4; }
 constexpr int ad_split(int rp) { return rp <= 32 ? 1 : 2; }

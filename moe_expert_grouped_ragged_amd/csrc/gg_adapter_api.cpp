@@ -44,7 +44,7 @@ Workspace workspace_of(int64_t M, int64_t E, int64_t N, int64_t K, int64_t r) {
     const int64_t rp = ad_rank_p(static_cast<int>(r));
     const int64_t chunks = ad_chunks(static_cast<int>(N), static_cast<int>(rp));
     // two workgroups of the smallest rank share a CU, and its parts are small (131072 rows, Zipf, N 2048:
-    // rank 16 338 us, 349 us with half the units; rank 32 402 us and 393 us)
+    // rank 16 341 us, 360 us with half the units; rank 32 385 us, 437 us with twice as many)
     w.rows1 = unit_rows(M, chunks, rp == 16 ? 1024 : 512);
     w.rows2 = unit_rows(M, (K + 4 * AD_WCOLS - 1) / (4 * AD_WCOLS), 1024);
     w.blocks = M / AD_BLK + (M < E ? M : E);

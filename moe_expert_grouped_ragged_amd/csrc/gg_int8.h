@@ -73,7 +73,7 @@ constexpr int I8_RING = 128 * 1024;   // LDS for operands
 // twice).  Zipf-distributed experts of 72 to 120 rows on average: within 7% of each other either way.
 //
 // Tiles and the rows they leave share a launch where LDS holds 32 rows of the summed width, or, of what large
-// tiles leave, 64, so that few weights are read twice (128 experts of 300 rows, K 2048, N 1536: 244 us, 269 us in
+// tiles leave, 64, so that few weights are read twice (128 experts of 300 rows, K 2048, N 1536: 245 us, 267 us in
 // two launches).
 struct Int8Plan {
     int tile, group;

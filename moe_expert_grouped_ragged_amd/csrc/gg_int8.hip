@@ -337,9 +337,9 @@ __global__ void int8_pack_kernel(const int8_t* __restrict__ q, const float* __re
 // one coalesced 1 KiB load a step.  Bound by the weights' bytes.
 
 // Rows of an expert that tiles of `tile` rows cover (0: there are no tiles).  256-row tiles leave a remainder
-// of at most 96 rows (32768 rows over 32 experts, K 1536, N 2048: 170 us, 174 us with at most 32); 128-row tiles,
+// of at most 96 rows (32768 rows over 32 experts, K 1536, N 2048: 164 us, 173 us with at most 32); 128-row tiles,
 // which run where there is little work, take all of an expert of more than 64 rows, or nothing (128 experts of
-// 80 rows, K 2048, N 1536: 128 us, 178 us with more than 96; of 24 rows 87 us, 93 us with more than 32).
+// 80 rows, K 2048, N 1536: 124 us, 178 us with more than 96; of 24 rows 87 us, 94 us with more than 32).
 __device__ __forceinline__ int i8_tile_rows(int m, int tile) {
     if (tile == 0) return 0;
     if (tile == 128) return m <= 64 ? 0 : m;
@@ -525,7 +525,7 @@ __device__ __forceinline__ void i8_stream_blocks(const Int8Params& p, const int8
 // of the group it is in in LDS in operand order (p.group is
 // what 128 KiB hold of the summed width): read by every wave from memory they
 // cost nearly as much of the load path as the weights (128 experts of 22 rows,
-// K 2688, N 3712, quantization included: 300 us from memory, 244 us here, 5.6 TB/s in this kernel).
+// K 2688, N 3712, quantization included: 294 us from memory, 245 us here, 5.6 TB/s in this kernel).
 // Otherwise, for few rows in all and for wide ones: items of four blocks, a wave each, in turn.
 template <bool PANEL, bool SCALED>
 __device__ __forceinline__ void i8_stream_list(const Int8Params& p, int* s_off, int* s_pre, int8_t* s_panel) {
