@@ -317,6 +317,97 @@ int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_
                   int64_t E, int64_t N, int64_t K, int activation, void* dh1_out,
                   void* workspace, size_t workspace_bytes, void* dx, hipStream_t stream);
 
+/* ---- Expert products in 8-bit floating point, a scale for each block of 128.
+ *
+ * Values are e4m3 (largest 448); a block's scale is a power of two, stored as
+ * the byte c + 127 for 2^c (the e8m0 format), so that scaling is exact and the
+ * matrix instruction applies it.  Weights have a scale for each 128 x 128
+ * block, rows of the operand one for each 128 values (the last block of a
+ * dimension may be shorter):
+ *
+ *   quant(v)     2^c the least power of two (c >= -126) with max|v| <= 448 * 2^c
+ *                in the block, q = v / 2^c rounded to nearest even; stands for 2^c q
+ *   forward      Y[r] = bf16(quant(v_r) W_e^T),  v = x, or v = A = bf16(act(gate) * up) of x = H1
+ *   input grad.  dX[r] = bf16(quant(v_r) W_e),   v = dY, or v = dH1 (derivative at H1, as above)
+ *
+ * with act and the rounding points of gg_forward_fc1_glu / gg_dgrad_glu.  A
+ * 128 x 128 block is a block of the transposed matrix too, so one quantization
+ * of the weights serves both directions.  `halves` is 2 for a matrix whose N
+ * rows are two halves (W1: gate rows, then up rows): blocks of N then start
+ * anew at the second half, so that none holds values of both (for F a multiple
+ * of 128 the blocks are the same either way).  Sums are fp32, in one order for
+ * all batches, so a row's result does not depend on the rest of the batch.  A
+ * block with a NaN or an infinity becomes NaNs, so such a row of v gives a row of
+ * NaNs, and no other row does.
+ *
+ * Limits: 1 <= E <= GG_MAX_EXPERTS; N and K positive multiples of 8 below
+ * 2^22, N of 16 with halves = 2; one packed expert matrix (both dimensions
+ * padded to whole blocks) below 2 GiB; 0 <= M < 2^31.  Conventions as above. */
+
+/* Bytes of the weights' scales: E * halves * ceil(N / halves / 128) * ceil(K / 128),
+ * ordered [expert][half][row block][column block].  0 for sizes outside the limits. */
+size_t gg_fp8_scale_bytes(int64_t E, int64_t N, int64_t K, int halves);
+
+/* Quantize weights w (DEVICE bf16 [E][N][K], 16-byte aligned) into q (DEVICE
+ * e4m3 [E][N][K], 8-byte aligned) and s (DEVICE, gg_fp8_scale_bytes).  One launch. */
+int gg_fp8_quantize_weights(const void* w, int64_t E, int64_t N, int64_t K, int halves, uint8_t* q, uint8_t* s,
+                            hipStream_t stream);
+
+/* Bytes of a packed matrix of E experts, for either direction. */
+size_t gg_fp8_packed_bytes(int64_t E, int64_t N, int64_t K, int halves);
+
+/* Lay out q and s (as written by gg_fp8_quantize_weights, or any e4m3 values
+ * with such scales) into `packed` (DEVICE, 16-byte aligned): both dimensions
+ * zero-padded to whole blocks, in the operand order of the matrix instruction,
+ * then the scales.  transposed = 0: for gg_fp8_forward; 1: for gg_fp8_dgrad.
+ * The calls cannot see which one a buffer holds.  Once for frozen weights.
+ * One launch. */
+int gg_fp8_pack(const uint8_t* q, const uint8_t* s, int64_t E, int64_t N, int64_t K, int halves, int transposed,
+                void* packed, size_t packed_bytes, hipStream_t stream);
+
+/* Bytes of the workspace of gg_fp8_forward (width = K, halves = 1) or
+ * gg_fp8_dgrad (width = N, halves as given there): the quantized rows. */
+size_t gg_fp8_workspace_bytes(int64_t M, int64_t width, int halves);
+
+/* Forward: x [M][K] with GG_ACT_NONE, or H1 [M][2K] with an activation, in
+ * which case a_out (may be NULL) receives A [M][K].  packed: gg_fp8_pack(...,
+ * halves, transposed = 0).  y [M][N]. */
+int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed, int64_t E, int64_t N,
+                   int64_t K, int halves, int activation, void* a_out, void* workspace, size_t workspace_bytes, void* y,
+                   hipStream_t stream);
+
+/* Input gradient: dy [M][N] with GG_ACT_NONE (h1 and dh1_out NULL); with an
+ * activation halves = 2, N = 2F, dy is dA [M][F], h1 [M][2F] the saved FC1
+ * output, and dh1_out (may be NULL) receives dH1 [M][2F].  packed:
+ * gg_fp8_pack(..., halves, transposed = 1).  dx [M][K]. */
+int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed, int64_t E,
+                 int64_t N, int64_t K, int halves, int activation, void* dh1_out, void* workspace,
+                 size_t workspace_bytes, void* dx, hipStream_t stream);
+
+/* ---- The gated feed-forward block of such products: both projections, the
+ * activation and the down projection, and the block's input gradient.
+ *
+ *   forward      H1 = bf16(quant(x) W1_e^T),  A = bf16(act(gate) * up),  Y = bf16(quant(A) W2_e^T)
+ *   input grad.  dA = bf16(quant(dY) W2_e),   dH1 = bf16 of the derivative at H1 times dA,
+ *                dX = bf16(quant(dH1) W1_e)
+ *
+ * The results are those of the single calls in a row, bit for bit.
+ * fc1: W1 [2F][H], packed with halves = 2; fc2: W2 [H][F], halves = 1; fc1_t,
+ * fc2_t: the same, transposed = 1. */
+
+/* Bytes of the workspace of gg_fp8_glu_forward (dgrad = 0) or gg_fp8_glu_dgrad (1). */
+size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad);
+
+/* x [M][H]; h1_out [M][2F] (saved for the gradient) may be NULL; y [M][H]. */
+int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2, int64_t E,
+                       int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes, void* h1_out,
+                       void* y, hipStream_t stream);
+
+/* dy [M][H], h1 [M][2F] as the forward saved it; dx [M][H]. */
+int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
+                     const void* fc2_t, int64_t E, int64_t H, int64_t F, int activation, void* workspace,
+                     size_t workspace_bytes, void* dx, hipStream_t stream);
+
 /* ---- Low-rank adapters of the experts (trainable; added to a frozen product).
  *
  * For an expert e with a_e [r][K] and b_e [N][r] (bf16), over its rows:

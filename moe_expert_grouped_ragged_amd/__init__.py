@@ -42,6 +42,18 @@ an adapter between them):
         (Int8AdapterExpertMLP runs the gated MLP of both, with autograd;
         int8_experts prepares its weights)
 
+Expert products in 8-bit floating point (e4m3) with a power-of-two scale for
+each block of 128, and the gated feed-forward block made of them:
+
+  gg_fp8_quantize_weights(w, halves)             -> (q, s)
+  gg_fp8_pack(q, s, halves) / gg_fp8_pack_transposed(q, s, halves) -> packed weights
+  gg_fp8_forward(x, offsets, packed, E, N, K, halves, activation)  -> (y, A or None)
+  gg_fp8_dgrad(dy, offsets, packed_t, E, N, K, halves, h1, activation) -> (dx, dH1 or None)
+  gg_fp8_glu_forward(x, offsets, fc1, fc2, E, H, F, activation)    -> (y, H1 or None)
+  gg_fp8_glu_dgrad(dy, h1, offsets, fc1_t, fc2_t, E, H, F, activation) -> dx
+        (Fp8ExpertMLP is the block with autograd, Fp8AdapterExpertMLP the MLP
+        with trainable adapters; fp8_experts prepares their weights)
+
 The other calls take frozen, bias-free bf16 expert weights only: the Megatron-LM pull request
 "perf(moe): add frozen grouped GEMM for adapter training" (section "Why
 existing behavior remains safe") accepts only grouped, frozen, bias-free BF16
@@ -83,7 +95,10 @@ EXPORTED = ("gg_status_string", "gg_packed_bytes", "gg_dgrad_workspace_bytes", "
             "gg_scale_rows", "gg_scale_rows_backward",
             "gg_int8_quantize_rows", "gg_int8_packed_bytes", "gg_int8_pack", "gg_int8_workspace_bytes",
             "gg_int8_forward", "gg_int8_dgrad",
-            "gg_adapter_forward", "gg_adapter_workspace_bytes", "gg_adapter_backward")
+            "gg_adapter_forward", "gg_adapter_workspace_bytes", "gg_adapter_backward",
+            "gg_fp8_scale_bytes", "gg_fp8_quantize_weights", "gg_fp8_packed_bytes", "gg_fp8_pack",
+            "gg_fp8_workspace_bytes", "gg_fp8_forward", "gg_fp8_dgrad",
+            "gg_fp8_glu_workspace_bytes", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad")
 
 
 def _load() -> ctypes.CDLL:
@@ -128,11 +143,26 @@ def _load() -> ctypes.CDLL:
     lib.gg_adapter_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.gg_adapter_workspace_bytes.restype = sz
     lib.gg_adapter_backward.argtypes = [p, p, p, p, i64, p, p, i64, i64, i64, i64, f32, p, p, sz, p, p, p, i32, p]
+    lib.gg_fp8_scale_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gg_fp8_scale_bytes.restype = sz
+    lib.gg_fp8_quantize_weights.argtypes = [p, i64, i64, i64, i32, p, p, p]
+    lib.gg_fp8_packed_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gg_fp8_packed_bytes.restype = sz
+    lib.gg_fp8_pack.argtypes = [p, p, i64, i64, i64, i32, i32, p, sz, p]
+    lib.gg_fp8_workspace_bytes.argtypes = [i64, i64, i32]
+    lib.gg_fp8_workspace_bytes.restype = sz
+    lib.gg_fp8_forward.argtypes = [p, p, i64, p, i64, i64, i64, i32, i32, p, p, sz, p, p]
+    lib.gg_fp8_dgrad.argtypes = [p, p, p, i64, p, i64, i64, i64, i32, i32, p, p, sz, p, p]
+    lib.gg_fp8_glu_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gg_fp8_glu_workspace_bytes.restype = sz
+    lib.gg_fp8_glu_forward.argtypes = [p, p, i64, p, p, i64, i64, i64, i32, p, sz, p, p, p]
+    lib.gg_fp8_glu_dgrad.argtypes = [p, p, p, i64, p, p, i64, i64, i64, i32, p, sz, p, p]
     for name in ("gg_pack_weights", "gg_pack_frag", "gg_forward_fc1_swiglu", "gg_forward_fc2",
                  "gg_forward_fc2_frag", "gg_dgrad", "gg_round_bf16", "gg_forward_fc1_glu", "gg_dgrad_glu",
                  "gg_dgrad_recompute", "gg_dgrad_noalloc", "gg_scale_rows", "gg_scale_rows_backward",
                  "gg_int8_quantize_rows", "gg_int8_pack", "gg_int8_forward", "gg_int8_dgrad",
-                 "gg_adapter_forward", "gg_adapter_backward"):
+                 "gg_adapter_forward", "gg_adapter_backward", "gg_fp8_quantize_weights", "gg_fp8_pack",
+                 "gg_fp8_forward", "gg_fp8_dgrad", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -832,6 +862,230 @@ def gg_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, offs
     return dx, da, db
 
 
+def fp8_scale_shape(E: int, N: int, K: int, halves: int = 1) -> Tuple[int, int, int]:
+    """Shape of the block scales of weights [E, N, K] (rows of blocks of both halves with halves=2)."""
+    return E, halves * -(-N // (128 * halves)), -(-K // 128)
+
+
+def fp8_packed_bytes(E: int, N: int, K: int, halves: int = 1) -> int:
+    return int(lib.gg_fp8_packed_bytes(E, N, K, halves))
+
+
+def fp8_workspace_bytes(M: int, width: int, halves: int = 1) -> int:
+    """Workspace of gg_fp8_forward (width = K, halves 1) or gg_fp8_dgrad (width = N)."""
+    return int(lib.gg_fp8_workspace_bytes(M, width, halves))
+
+
+def fp8_glu_workspace_bytes(M: int, H: int, F: int, dgrad: bool = False) -> int:
+    return int(lib.gg_fp8_glu_workspace_bytes(M, H, F, int(bool(dgrad))))
+
+
+def _fp8_shape(E, N, K, halves) -> int:
+    """Bytes of a packed matrix of these sizes, which are checked."""
+    if halves not in (1, 2):
+        raise ValueError(f"halves must be 1 or 2, got {halves}")
+    need = fp8_packed_bytes(E, N, K, halves)
+    if need == 0:
+        raise ValueError(f"E={E}, N={N}, K={K}, halves={halves} is outside the limits of the fp8 calls")
+    return need
+
+
+@_allocates_on_stream
+def gg_fp8_quantize_weights(w: torch.Tensor, halves: int = 1, q: Optional[torch.Tensor] = None,
+                            s: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Frozen weights w (bf16 [E, N, K]) to e4m3 with a power of two for each
+    128 x 128 block: (q float8_e4m3fn [E, N, K], s float8_e8m0fnu
+    fp8_scale_shape(E, N, K, halves)).  halves=2: the N rows are two halves
+    (gate rows, then up rows), whose blocks are apart."""
+    _bf16_cuda(w, "w")
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, K]")
+    E, N, K = w.shape
+    _fp8_shape(E, N, K, halves)
+    shape = fp8_scale_shape(E, N, K, halves)
+    if q is not None:
+        _typed_cuda(q, torch.float8_e4m3fn, "q", (E, N, K), w.device)
+    if s is not None:
+        _typed_cuda(s, torch.float8_e8m0fnu, "s", shape, w.device)
+    q = torch.empty(E, N, K, dtype=torch.float8_e4m3fn, device=w.device) if q is None else q
+    s = torch.empty(shape, dtype=torch.float8_e8m0fnu, device=w.device) if s is None else s
+    _check(lib.gg_fp8_quantize_weights(w.data_ptr(), E, N, K, halves, q.data_ptr(), s.data_ptr(),
+                                       _stream_ptr(stream, w.device)), "gg_fp8_quantize_weights")
+    return q, s
+
+
+def _fp8_pack(q, s, halves, transposed, packed, stream):
+    _typed_cuda(q, torch.float8_e4m3fn, "q", (None, None, None), None)
+    E, N, K = q.shape
+    need = _fp8_shape(E, N, K, halves)
+    _typed_cuda(s, torch.float8_e8m0fnu, "s", fp8_scale_shape(E, N, K, halves), q.device)
+    if packed is None:
+        packed = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _workspace(packed, need, q.device)
+    _check(lib.gg_fp8_pack(q.data_ptr(), s.data_ptr(), E, N, K, halves, int(transposed), packed.data_ptr(),
+                           packed.numel() * packed.element_size(), _stream_ptr(stream, q.device)), "gg_fp8_pack")
+    if not packed.is_inference():       # those have no version
+        torch.autograd.graph.increment_version(packed)      # as for any write to it; its views see it too
+        packed._gg_fp8_holds = (E, N, K, halves, bool(transposed)), packed._version
+    return packed
+
+
+@_allocates_on_stream
+def gg_fp8_pack(q: torch.Tensor, s: torch.Tensor, halves: int = 1, packed: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """8-bit weights q (float8_e4m3fn [E, N, K]) with block scales s
+    (float8_e8m0fnu fp8_scale_shape(E, N, K, halves)), laid out once for
+    gg_fp8_forward: a byte buffer of fp8_packed_bytes(E, N, K, halves).  The
+    tensor returned is refused where another layout is needed."""
+    return _fp8_pack(q, s, halves, False, packed, stream)
+
+
+@_allocates_on_stream
+def gg_fp8_pack_transposed(q: torch.Tensor, s: torch.Tensor, halves: int = 1, packed: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The same weights and scales laid out for gg_fp8_dgrad."""
+    return _fp8_pack(q, s, halves, True, packed, stream)
+
+
+def _fp8_packed(packed: torch.Tensor, E: int, N: int, K: int, halves: int, transposed: bool, device,
+                name: str = "packed") -> torch.Tensor:
+    need = _fp8_shape(E, N, K, halves)
+    if not isinstance(packed, torch.Tensor) or not packed.is_cuda or not packed.is_contiguous() or packed.device != device:
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if packed.numel() * packed.element_size() < need:
+        raise ValueError(f"{name} holds {packed.numel() * packed.element_size()} bytes, {need} needed")
+    # a tensor that was packed, and not written since, says what it holds (a copy or a view of one does not)
+    holds = getattr(packed, "_gg_fp8_holds", None)
+    want = (E, N, K, halves, transposed)
+    if holds is not None and holds[0] != want and holds[1] == packed._version:
+        raise ValueError(f"{name} holds (E, N, K, halves, transposed) = {holds[0]}, not {want}")
+    return packed
+
+
+@_allocates_on_stream
+def gg_fp8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
+                   halves: int = 1, activation=None, save_a: bool = False, a_out: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(y [M, N], A or None): the rows quantized in blocks of 128, times each
+    expert's 8-bit matrix (gg_fp8_pack with the same halves).  activation None:
+    x is [M, K]; "swiglu" | "qgeglu": x is H1 [M, 2K], the product's operand is
+    A = act(gate) * up [M, K], returned with save_a (or given a_out)."""
+    _bf16_cuda(x, "x")
+    dev, M = x.device, x.shape[0]
+    act = GG_ACT_NONE if activation is None else _activation(activation)
+    _bf16_cuda(x, "x", shape=(M, K if act == GG_ACT_NONE else 2 * K))
+    _fp8_packed(packed, E, N, K, halves, False, dev)
+    off = _offsets(offsets, E, dev)
+    if a_out is not None:
+        _bf16_cuda(a_out, "a_out", shape=(M, K), device=dev)
+    if act == GG_ACT_NONE and (save_a or a_out is not None):
+        raise ValueError("A exists with an activation only")
+    if y is not None:
+        _bf16_cuda(y, "y", shape=(M, N), device=dev)
+    workspace = _workspace(workspace, fp8_workspace_bytes(M, K), dev)
+    if a_out is None and save_a:
+        a_out = _out(None, (M, K), "a_out", dev)
+    y = _out(y, (M, N), "y", dev)
+    _check(lib.gg_fp8_forward(x.data_ptr(), off.data_ptr(), M, packed.data_ptr(), E, N, K, halves, act, _ptr(a_out),
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), y.data_ptr(),
+                              _stream_ptr(stream, dev)), "gg_fp8_forward")
+    return y, a_out
+
+
+@_allocates_on_stream
+def gg_fp8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
+                 halves: int = 1, h1: Optional[torch.Tensor] = None, activation=None, save_dh1: bool = True,
+                 dh1_out: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                 ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(dx [M, K], dH1 or None): input gradient through 8-bit weights
+    (gg_fp8_pack_transposed with the same halves).  activation None: dy is
+    [M, N]; else halves = 2, N = 2F, dy is dA [M, F], h1 the saved [M, 2F], and
+    dH1 [M, 2F] is returned unless save_dh1 is False."""
+    _bf16_cuda(dy, "dy")
+    dev, M = dy.device, dy.shape[0]
+    act = GG_ACT_NONE if activation is None else _activation(activation)
+    if (act == GG_ACT_NONE) != (h1 is None):
+        raise ValueError("h1 and an activation go together")
+    if act != GG_ACT_NONE and halves != 2:
+        raise ValueError("the activation's derivative needs halves=2")
+    _bf16_cuda(dy, "dy", shape=(M, N if act == GG_ACT_NONE else N // 2))
+    if h1 is not None:
+        _bf16_cuda(h1, "h1", shape=(M, N), device=dev)
+    _fp8_packed(packed, E, N, K, halves, True, dev)
+    off = _offsets(offsets, E, dev)
+    if dh1_out is not None:
+        if h1 is None:
+            raise ValueError("dH1 exists with an activation only")
+        _bf16_cuda(dh1_out, "dh1_out", shape=(M, N), device=dev)
+    if dx is not None:
+        _bf16_cuda(dx, "dx", shape=(M, K), device=dev)
+    workspace = _workspace(workspace, fp8_workspace_bytes(M, N, halves), dev)
+    if dh1_out is None and h1 is not None and save_dh1:
+        dh1_out = _out(None, (M, N), "dh1_out", dev)
+    dx = _out(dx, (M, K), "dx", dev)
+    _check(lib.gg_fp8_dgrad(dy.data_ptr(), _ptr(h1), off.data_ptr(), M, packed.data_ptr(), E, N, K, halves, act,
+                            _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            dx.data_ptr(), _stream_ptr(stream, dev)), "gg_fp8_dgrad")
+    return dx, dh1_out
+
+
+@_allocates_on_stream
+def gg_fp8_glu_forward(x: torch.Tensor, offsets: torch.Tensor, fc1: torch.Tensor, fc2: torch.Tensor,
+                       E: int, H: int, F: int, activation="swiglu", save_h1: bool = True,
+                       h1_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                       ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gated block: x [M, H] -> (y [M, H], H1 [M, 2F] or None).  fc1: W1
+    [E, 2F, H] by gg_fp8_pack(..., halves=2); fc2: W2 [E, H, F] by gg_fp8_pack."""
+    _bf16_cuda(x, "x")
+    M, dev = x.shape[0], x.device
+    _bf16_cuda(x, "x", shape=(M, H))
+    _fp8_packed(fc1, E, 2 * F, H, 2, False, dev, "fc1")
+    _fp8_packed(fc2, E, H, F, 1, False, dev, "fc2")
+    off = _offsets(offsets, E, dev)
+    if h1_out is not None:
+        _bf16_cuda(h1_out, "h1_out", shape=(M, 2 * F), device=dev)
+    if y is not None:
+        _bf16_cuda(y, "y", shape=(M, H), device=dev)
+    act = _activation(activation)
+    workspace = _workspace(workspace, fp8_glu_workspace_bytes(M, H, F), dev)
+    if h1_out is None and save_h1:
+        h1_out = _out(None, (M, 2 * F), "h1_out", dev)
+    y = _out(y, (M, H), "y", dev)
+    _check(lib.gg_fp8_glu_forward(x.data_ptr(), off.data_ptr(), M, fc1.data_ptr(), fc2.data_ptr(), E, H, F, act,
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(h1_out),
+                                  y.data_ptr(), _stream_ptr(stream, dev)), "gg_fp8_glu_forward")
+    return y, h1_out
+
+
+@_allocates_on_stream
+def gg_fp8_glu_dgrad(dy: torch.Tensor, h1: torch.Tensor, offsets: torch.Tensor, fc1_t: torch.Tensor,
+                     fc2_t: torch.Tensor, E: int, H: int, F: int, activation="swiglu",
+                     dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gated block's input gradient: dy [M, H] and the saved h1 [M, 2F] ->
+    dx [M, H].  fc1_t, fc2_t: the weights of gg_fp8_glu_forward by gg_fp8_pack_transposed."""
+    _bf16_cuda(dy, "dy")
+    M, dev = dy.shape[0], dy.device
+    _bf16_cuda(dy, "dy", shape=(M, H))
+    _bf16_cuda(h1, "h1", shape=(M, 2 * F), device=dev)
+    _fp8_packed(fc1_t, E, 2 * F, H, 2, True, dev, "fc1_t")
+    _fp8_packed(fc2_t, E, H, F, 1, True, dev, "fc2_t")
+    off = _offsets(offsets, E, dev)
+    if dx is not None:
+        _bf16_cuda(dx, "dx", shape=(M, H), device=dev)
+    act = _activation(activation)
+    workspace = _workspace(workspace, fp8_glu_workspace_bytes(M, H, F, True), dev)
+    dx = _out(dx, (M, H), "dx", dev)
+    _check(lib.gg_fp8_glu_dgrad(dy.data_ptr(), h1.data_ptr(), off.data_ptr(), M, fc1_t.data_ptr(), fc2_t.data_ptr(),
+                                E, H, F, act, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                dx.data_ptr(), _stream_ptr(stream, dev)), "gg_fp8_glu_dgrad")
+    return dx
+
+
 class ScaleRows(torch.autograd.Function):
     """Autograd wrapper of gg_scale_rows: x' = bf16(probs[r] * x[r]); the
     backward gives dx and, when probs requires grad, dprobs."""
@@ -935,6 +1189,86 @@ class Int8AdapterExpertMLP(torch.autograd.Function):
         da, ga2, gb2 = gg_adapter_backward(dy, a, u2, offsets, a2, b2, scale, base=da, dx=da)
         if fc1:
             dx, dh1 = gg_int8_dgrad(da, offsets, w.fc1_t, w.E, 2 * w.F, w.H, h1=h1, activation=ctx.activation)
+            dx, ga1, gb1 = gg_adapter_backward(dh1, x, u1, offsets, a1, b1, scale, base=dx, dx=dx)
+        grads = [g.to(torch.bfloat16) if n else None for g, n in zip((ga1, gb1, ga2, gb2), need[3:7])]
+        return dx if need[0] else None, None, None, *grads, None, None
+
+
+class Fp8Experts(NamedTuple):
+    """Frozen gated expert MLPs in 8-bit floating point: W1 [E, 2F, H] and W2
+    [E, H, F] laid out for the forward (fc1, fc2) and for the input gradient (fc1_t, fc2_t)."""
+    E: int
+    H: int
+    F: int
+    fc1: torch.Tensor
+    fc2: torch.Tensor
+    fc1_t: torch.Tensor
+    fc2_t: torch.Tensor
+
+
+def fp8_experts(w1: torch.Tensor, w2: torch.Tensor) -> Fp8Experts:
+    """Quantize frozen bf16 weights w1 [E, 2F, H] (gate rows, then up rows) and
+    w2 [E, H, F] in blocks of 128 x 128 and lay them out for Fp8ExpertMLP and Fp8AdapterExpertMLP."""
+    if w1.requires_grad or w2.requires_grad:
+        raise ValueError("expert base weights must be frozen (requires_grad=False)")
+    if w1.dim() != 3 or w2.dim() != 3 or w1.shape[0] != w2.shape[0] or w1.shape[1] != 2 * w2.shape[2] \
+            or w1.shape[2] != w2.shape[1]:
+        raise ValueError("w1 must be [E, 2F, H] and w2 [E, H, F]")
+    E, H, F = w2.shape
+    w1q, w2q = gg_fp8_quantize_weights(w1, halves=2), gg_fp8_quantize_weights(w2)
+    return Fp8Experts(E, H, F, gg_fp8_pack(*w1q, halves=2), gg_fp8_pack(*w2q),
+                      gg_fp8_pack_transposed(*w1q, halves=2), gg_fp8_pack_transposed(*w2q))
+
+
+class Fp8ExpertMLP(torch.autograd.Function):
+    """The gated block over frozen 8-bit floating-point weights: apply(x,
+    offsets, experts, activation) with experts from fp8_experts; the backward
+    gives dX (the base weights have no gradient)."""
+
+    @staticmethod
+    def forward(ctx, x, offsets, experts, activation="swiglu"):
+        w = experts
+        y, h1 = gg_fp8_glu_forward(x, offsets, w.fc1, w.fc2, w.E, w.H, w.F, activation, save_h1=ctx.needs_input_grad[0])
+        ctx.save_for_backward(h1, offsets)
+        ctx.experts, ctx.activation = w, activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        h1, offsets = ctx.saved_tensors
+        w = ctx.experts
+        dx = gg_fp8_glu_dgrad(dy.contiguous(), h1, offsets, w.fc1_t, w.fc2_t, w.E, w.H, w.F, ctx.activation)
+        return dx, None, None, None
+
+
+class Fp8AdapterExpertMLP(torch.autograd.Function):
+    """Int8AdapterExpertMLP over weights from fp8_experts, the operands
+    quantized in blocks of 128: the same arguments, formulas and gradients."""
+
+    @staticmethod
+    def forward(ctx, x, offsets, experts, a1, b1, a2, b2, scale, activation="swiglu"):
+        E, H, F = experts.E, experts.H, experts.F
+        a1, b1, a2, b2 = (t.detach() for t in (a1, b1, a2, b2))
+        h1, _ = gg_fp8_forward(x, offsets, experts.fc1, E, 2 * F, H, halves=2)
+        h1, u1 = gg_adapter_forward(x, offsets, a1, b1, scale, base=h1, y=h1)
+        y, a = gg_fp8_forward(h1, offsets, experts.fc2, E, H, F, activation=activation, save_a=True)
+        y, u2 = gg_adapter_forward(a, offsets, a2, b2, scale, base=y, y=y)
+        ctx.save_for_backward(x, offsets, h1, a, u1, u2, a1, b1, a2, b2)
+        ctx.experts, ctx.scale, ctx.activation = experts, scale, activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, offsets, h1, a, u1, u2, a1, b1, a2, b2 = ctx.saved_tensors
+        w, scale = ctx.experts, ctx.scale
+        need = ctx.needs_input_grad
+        fc1 = need[0] or need[3] or need[4]      # something that lies before A
+        dy, da, dx, ga1, gb1 = dy.contiguous(), None, None, None, None
+        if fc1:
+            da, _ = gg_fp8_dgrad(dy, offsets, w.fc2_t, w.E, w.H, w.F)
+        da, ga2, gb2 = gg_adapter_backward(dy, a, u2, offsets, a2, b2, scale, base=da, dx=da)
+        if fc1:
+            dx, dh1 = gg_fp8_dgrad(da, offsets, w.fc1_t, w.E, 2 * w.F, w.H, halves=2, h1=h1, activation=ctx.activation)
             dx, ga1, gb1 = gg_adapter_backward(dh1, x, u1, offsets, a1, b1, scale, base=dx, dx=dx)
         grads = [g.to(torch.bfloat16) if n else None for g, n in zip((ga1, gb1, ga2, gb2), need[3:7])]
         return dx if need[0] else None, None, None, *grads, None, None

@@ -1,0 +1,89 @@
+// Internal interface between the C-ABI entry points of the block-scaled 8-bit
+// floating-point products (gg_fp8_api.cpp) and their kernels (gg_fp8.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gg {
+
+constexpr int F8_BLOCK = 128;   // values that share a scale
+
+// One dimension of a matrix: one part, or two equal halves (gate, up), each
+// padded to whole blocks, so that no block holds values of both.
+struct F8Dim {
+    int part, part_p, parts;   // real and padded values of a part
+    __host__ __device__ int real() const { return part * parts; }
+    __host__ __device__ int padded() const { return part_p * parts; }
+    __host__ __device__ int blocks() const { return padded() / F8_BLOCK; }
+};
+inline F8Dim f8_dim(int64_t n, int parts) {
+    const int64_t part = n / parts;
+    return F8Dim{static_cast<int>(part), static_cast<int>((part + F8_BLOCK - 1) / F8_BLOCK * F8_BLOCK), parts};
+}
+
+// Layouts.  Quantized rows: 64-byte blocks, column c (padded) of row r at
+// (c / 64) * 64 M + 64 r + c % 64; their scales, a byte each (2^(byte - 127)),
+// four blocks of a row in a dword: block k of row r at 4 ((k / 4) M + r) + k % 4.
+// A packed matrix [rows][cont] (rows: output columns of the product, cont: the
+// summed dimension): 32-row blocks, each of cont_p / 64 steps of 2 KiB in the
+// operand order of the 32x32x64 matrix instruction: lane l holds row
+// 32 b + (l & 31), columns 64 s + 32 (l >> 5) onwards, 32 of them, as two
+// 16-byte operands 1 KiB apart.  Its scales: for each 128 rows, a byte for each
+// block of cont, in whole dwords.
+inline int64_t f8_matrix_bytes(const F8Dim& rows, const F8Dim& cont) {
+    return static_cast<int64_t>(rows.padded()) * cont.padded();
+}
+__host__ __device__ inline int f8_scale_ld(const F8Dim& cont) { return (cont.blocks() + 3) / 4 * 4; }
+inline int64_t f8_scale_bytes(const F8Dim& rows, const F8Dim& cont) {
+    return static_cast<int64_t>(rows.blocks()) * f8_scale_ld(cont);
+}
+inline int64_t f8_rows_bytes(int64_t M, const F8Dim& cont) {
+    return M * (cont.padded() + f8_scale_ld(cont));
+}
+
+// What a row's 8-bit values are made from.
+enum F8Mode {
+    F8_PLAIN = 0,   // v = x
+    F8_GLU = 1,     // v = bf16(act(gate) * up) of x = [gate | up]
+    F8_DGLU = 2     // v = bf16(derivative of the activation at h1, times x)
+};
+
+struct F8QuantParams {
+    const uint16_t* x;       // [M][dim] bf16 (F8_GLU: [M][2 dim], F8_DGLU: [M][dim / 2])
+    const uint16_t* h1;      // F8_DGLU: [M][dim]
+    const int64_t* offsets;  // [E+1]
+    int M, E;
+    F8Dim dim;               // a quantized row (F8_DGLU: two parts)
+    float slope;
+    uint16_t* v_out;         // F8_GLU, F8_DGLU: v [M][dim], or null
+    uint8_t* q;
+    uint8_t* s;
+};
+
+// out[r][n] = bf16(sum_k v[r][k] W_e[n][k])
+struct F8Params {
+    const uint8_t* q;        // quantized rows
+    const uint8_t* s;        // and their scales
+    const int64_t* offsets;  // [E+1]
+    const uint8_t* w;        // packed matrices
+    int64_t w_stride;        // bytes of one expert's matrix
+    const uint8_t* ws;       // and their scales
+    int64_t ws_stride;       // bytes of one expert's scales
+    int ws_ld;               // bytes of the scales of 128 rows
+    int M, E;
+    int kblocks;             // blocks of the summed dimension
+    F8Dim n;                 // output columns
+    uint16_t* out;           // [M][n]
+};
+
+hipError_t launch_f8_quant(F8Mode mode, const F8QuantParams& p, int num_cu, hipStream_t s);
+hipError_t launch_f8_gemm(const F8Params& p, int num_cu, hipStream_t s);
+// w [E][n][k] in bf16 to q (e4m3) and s (a byte for each 128 x 128 block, [E][n.blocks()][k.blocks()])
+hipError_t launch_f8_quant_weights(const uint16_t* w, int E, const F8Dim& n, const F8Dim& k, uint8_t* q, uint8_t* s,
+                                   hipStream_t stream);
+// q and s into the packed layout: the matrix is q_e, or with `transposed` q_e^T; the scales follow the matrices
+hipError_t launch_f8_pack(const uint8_t* q, const uint8_t* s, int E, const F8Dim& n, const F8Dim& k, int transposed,
+                          uint8_t* packed, hipStream_t stream);
+
+}  // namespace gg
