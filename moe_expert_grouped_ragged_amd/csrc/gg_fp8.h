@@ -61,7 +61,13 @@ struct F8QuantParams {
     uint8_t* s;
 };
 
-// out[r][n] = bf16(sum_k v[r][k] W_e[n][k])
+// What becomes of a product's sums acc[r][n] = sum_k v[r][k] W_e[n][k].
+enum F8Epilogue {
+    F8_STORE = 0,       // out = bf16(acc)
+    F8_STORE_GLU = 1,   // n: two parts, H1 = bf16(acc) (stored where h1_out is given); A = bf16(act(gate) * up), quantized
+    F8_STORE_DGLU = 2   // dA = bf16(acc), dH1 = bf16(derivative at h1, times dA), quantized
+};
+
 struct F8Params {
     const uint8_t* q;        // quantized rows
     const uint8_t* s;        // and their scales
@@ -73,12 +79,38 @@ struct F8Params {
     int ws_ld;               // bytes of the scales of 128 rows
     int M, E;
     int kblocks;             // blocks of the summed dimension
-    F8Dim n;                 // output columns
-    uint16_t* out;           // [M][n]
+    F8Dim n;                 // columns
+    uint16_t* out;           // F8_STORE: [M][n]; F8_STORE_GLU: H1 [M][n], or null
+    const uint16_t* h1;      // F8_STORE_DGLU: [M][2 n]
+    float slope;
+    uint8_t* q_out;          // A or dH1, quantized
+    uint8_t* s_out;
+    int tile;                // rows of a tile, or 0: no tiles (set by the launcher)
+    int group;               // rows of a streaming item, at most; 0: there are none (set by the launcher)
 };
 
+constexpr int F8_GROUP = 96;                    // rows of a streaming item, at most
+constexpr int F8_PANEL = 128 * 1024;            // LDS for a streaming item's rows
+constexpr int F8_RING = F8_PANEL + 4 * 1024;    // LDS for operands
+
+// Which tiles a product of M rows over E experts takes (rows of a tile, 0: none), and how many rows a streaming item
+// has at most (0: there are none).  columns: of the largest tile, in all.
+struct F8Plan {
+    int tile, group;
+};
+inline F8Plan f8_plan(int M, int E, int tiles_n, int kblocks, int num_cu) {
+    const int64_t large = static_cast<int64_t>(M) / 256 * tiles_n;
+    const int64_t owners = M < E ? M : E;
+    const bool half = M >= 80 * owners && M < 120 * owners;
+    const int panel = F8_PANEL / (kblocks * F8_BLOCK * 32) * 32;
+    F8Plan plan;
+    plan.group = panel < F8_GROUP ? panel : F8_GROUP;
+    plan.tile = M <= 64 && plan.group ? 0 : (large < num_cu || half ? 128 : 256);
+    return plan;
+}
+
 hipError_t launch_f8_quant(F8Mode mode, const F8QuantParams& p, int num_cu, hipStream_t s);
-hipError_t launch_f8_gemm(const F8Params& p, int num_cu, hipStream_t s);
+hipError_t launch_f8_gemm(F8Epilogue epilogue, const F8Params& p, int num_cu, hipStream_t s);
 // w [E][n][k] in bf16 to q (e4m3) and s (a byte for each 128 x 128 block, [E][n.blocks()][k.blocks()])
 hipError_t launch_f8_quant_weights(const uint16_t* w, int E, const F8Dim& n, const F8Dim& k, uint8_t* q, uint8_t* s,
                                    hipStream_t stream);

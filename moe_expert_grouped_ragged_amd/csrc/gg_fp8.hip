@@ -262,97 +262,742 @@ __device__ __forceinline__ i32x8 f8_join(i32x4 a, i32x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// One wave's 32 output columns (padded block nb) for up to 32 TB rows over the whole summed dimension, one block of
-// 128 loaded while another is multiplied.
-template <int TB>
-__device__ __forceinline__ void f8_stream_block(const F8Params& p, const uint8_t* w, const uint8_t* ws, int row0, int rows,
-                                                int nb) {
-    const int lane = threadIdx.x & 63;
-    const uint8_t* wp = w + static_cast<int64_t>(nb) * p.kblocks * 4096 + lane * 16;
-    const uint8_t* sp = ws + static_cast<int64_t>(nb >> 2) * p.ws_ld;
-    const uint8_t *tp[TB], *ts[TB];
+// Rows of an expert that tiles of `tile` rows cover (0: there are no tiles): a remainder of up to `group` rows (of
+// small tiles, an expert of up to that) is left to a streaming item.
+__device__ __forceinline__ int f8_tile_rows(int m, int tile, int group) {
+    if (tile == 0) return 0;
+    if (tile == 128) return m <= min(group, 64) ? 0 : m;
+    const int tail = m % tile;
+    return tail <= group ? m - tail : m;
+}
+
+// One wave-wide copy of 4 bytes a lane to LDS, as dma16.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+                 :: "v"(voff), "s"(uni_ptr(base)), "s"(uni(lds)) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// A dword that no kernel of the launch writes, by the scalar unit.
+__device__ __forceinline__ uint32_t scalar_load(const uint8_t* p) {
+    return *(const __attribute__((address_space(4))) uint32_t*)(reinterpret_cast<uintptr_t>(uni_ptr(p)));
+}
+
+__device__ __forceinline__ uint32_t max_other_half(uint32_t v) {   // of lanes l and l ^ 32
+    return max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32, 64)));
+}
+
+// ---- Streaming items: a group of rows of one expert x a range of 128-column
+// blocks, for which each weight byte is read once; a wave takes 32 columns of a
+// block (of each half with F8_STORE_GLU) at a time over the whole summed
+// dimension.  Bound by the weights' bytes.
+//
+// The rows' operands lie in `panel` (LDS, 4 KiB for 32 rows of a block of the
+// summed dimension), their scales behind them.  The weights come as one stream
+// over a wave's blocks, in units of a block of the summed dimension, all but
+// one of R units ahead, the first of them from before the panel is filled:
+// nothing drains at a block's end, where the sums go to the epilogue, and
+// loads are repeated only at the stretch's own end.
+template <int TB, int EPI>
+__device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_t* w, const uint8_t* ws, int row0, int rows,
+                                                 int nb0, int nb1, uint8_t* panel, uint32_t (*s_top)[4][F8_GROUP]) {
+    constexpr int C = EPI == F8_STORE_GLU ? 2 : 1;   // column blocks of a wave
+    constexpr int R = 8 / C, W = 4;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), nu = p.kblocks;
+    const int total = (nb1 - nb0) * nu;
+    const int64_t wblock = static_cast<int64_t>(nu) * 4096;      // bytes of 32 columns
+    const int64_t up = EPI == F8_STORE_GLU ? static_cast<int64_t>(p.n.part_p / 32) * wblock : 0;
+    const int64_t up_s = EPI == F8_STORE_GLU ? static_cast<int64_t>(p.n.part_p / F8_BLOCK) * p.ws_ld : 0;
+    int zero = 0;
+    asm volatile("" : "+v"(zero));      // keeps the scales' loads off the scalar unit, whose results come out of order
+    const uint8_t* lp = w + (static_cast<int64_t>(nb0) * 4 + wave) * wblock;
+    const uint8_t* sp = ws + static_cast<int64_t>(nb0) * p.ws_ld;
+    int lk = 0, lf = 0;   // the next unit to load: of its block, and of all
+    i32x4 wv[R][C][4];
+    int wsv[R][C];
+    auto load = [&](i32x4(&v)[C][4], int(&sv)[C]) {
 #pragma unroll
-    for (int i = 0; i < TB; ++i) {
-        const int64_t r = row0 + min(i * 32 + (lane & 31), rows - 1);
-        tp[i] = p.q + r * 64 + 32 * (lane >> 5);
-        ts[i] = p.s + r * 4;
-    }
-    const int64_t block = static_cast<int64_t>(p.M) * 64, sgroup = static_cast<int64_t>(p.M) * 4;
-    f32x16 acc[TB];
-#pragma unroll
-    for (int i = 0; i < TB; ++i) acc[i] = f32x16{};
-    i32x4 wv[2][4], tv[2][TB][4];
-    int wsv[2], tsv[2][TB];
-    auto load = [&](auto buf_tag, int k) {
-        constexpr int buf = decltype(buf_tag)::value;
-        k = min(k, p.kblocks - 1);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            wv[buf][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp + static_cast<int64_t>(k) * 4096 + u * 1024));
-        wsv[buf] = sp[k];
-#pragma unroll
-        for (int i = 0; i < TB; ++i) {
+        for (int c = 0; c < C; ++c) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                tv[buf][i][u] = *reinterpret_cast<const i32x4*>(tp[i] + (2 * k + (u >> 1)) * block + 16 * (u & 1));
-            tsv[buf][i] = ts[i][(k >> 2) * sgroup + (k & 3)];
+                v[c][u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(lp + c * up + lane * 16 + u * 1024));
+            sv[c] = (sp + c * up_s + lk)[zero];
+        }
+        const bool wrap = ++lk == nu;
+        if (++lf < total) {
+            lp += 4096 + (wrap ? 3 * wblock : 0);
+            sp += wrap ? p.ws_ld : 0;
+            lk = wrap ? 0 : lk;
+        } else {
+            lk = nu - 1;
         }
     };
-    auto mma = [&](auto buf_tag) {
-        constexpr int buf = decltype(buf_tag)::value;
+    f32x16 acc[C][TB];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int i = 0; i < TB; ++i)
-                acc[i] = f8_mma(f8_join(wv[buf][2 * u], wv[buf][2 * u + 1]), f8_join(tv[buf][i][2 * u], tv[buf][i][2 * u + 1]),
-                                acc[i], wsv[buf], tsv[buf][i]);
-    };
-    load(GrpTag<0>{}, 0);
-    for (int k = 0; k < p.kblocks; k += 2) {
-        load(GrpTag<1>{}, k + 1);
-        mma(GrpTag<0>{});
-        load(GrpTag<0>{}, k + 2);
-        if (k + 1 < p.kblocks) mma(GrpTag<1>{});
+        for (int i = 0; i < TB; ++i) acc[c][i] = f32x16{};
+    // in this order: the first unit's wait would otherwise be for all
+#pragma unroll
+    for (int i = 0; i < R - 1; ++i) {
+        load(wv[i], wsv[i]);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    // lane holds row lane & 31 of each 32-row block and, in register 4q + x, column 32 nb + 8q + 4(lane >> 5) + x
-    const int h = nb * 32 >= p.n.part_p;
+    uint8_t* pscale = panel + F8_PANEL;      // [nu][32 TB]
+    __syncthreads();   // the last panel is read
+    constexpr int F = 8;   // loads of a thread in flight
+    const int chunks = nu * TB * 256;
+    for (int i0 = threadIdx.x; i0 < chunks; i0 += F * W * 64) {
+        i32x4 v[F];
 #pragma unroll
-    for (int i = 0; i < TB; ++i) {
-        const int r = i * 32 + (lane & 31);
-        if (r >= rows) continue;
-        uint16_t* orow = p.out + static_cast<int64_t>(row0 + r) * p.n.real() + h * p.n.part;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int n = nb * 32 - h * p.n.part_p + 8 * q + 4 * (lane >> 5);
-            if (n < p.n.part)
-                *reinterpret_cast<uint2*>(orow + n) = make_uint2(pack2(acc[i][4 * q], acc[i][4 * q + 1]),
-                                                                 pack2(acc[i][4 * q + 2], acc[i][4 * q + 3]));
+        for (int j = 0; j < F; ++j) {
+            // operand bytes 16 i: of step st, row block b, half h of 32 columns, lane l
+            const int i = min(i0 + j * W * 64, chunks - 1);
+            const int l = i & 63, h = (i >> 6) & 1, st = (i >> 7) / TB, b = (i >> 7) % TB;
+            v[j] = *reinterpret_cast<const i32x4*>(
+                p.q + (static_cast<int64_t>(st) * p.M + row0 + min(b * 32 + (l & 31), rows - 1)) * 64 + 32 * (l >> 5) + 16 * h);
         }
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int i = i0 + j * W * 64;
+            if (i < chunks) *reinterpret_cast<i32x4*>(panel + i * 16) = v[j];
+        }
+    }
+    for (int i = threadIdx.x; i < nu * TB * 32; i += W * 64) {
+        const int k = i / (TB * 32), r = i % (TB * 32);
+        pscale[i] = p.s[(static_cast<int64_t>(k >> 2) * p.M + row0 + min(r, rows - 1)) * 4 + (k & 3)];
+    }
+    __syncthreads();
+    // a block's rows of h1, loaded when the block begins
+    uint2 hg[EPI == F8_STORE_DGLU ? TB : 1][4], hu[EPI == F8_STORE_DGLU ? TB : 1][4];
+    int nb = nb0;
+    auto load_h1 = [&](int b) {
+        if constexpr (EPI == F8_STORE_DGLU) {
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                const uint16_t* h = p.h1 + static_cast<int64_t>(row0 + min(i * 32 + (lane & 31), rows - 1)) * 2 * p.n.part;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = b * F8_BLOCK + 32 * wave + 8 * q + 4 * (lane >> 5);
+                    const bool ok = c < p.n.part;
+                    hg[i][q] = ok ? *reinterpret_cast<const uint2*>(h + c) : make_uint2(0, 0);
+                    hu[i][q] = ok ? *reinterpret_cast<const uint2*>(h + p.n.part + c) : make_uint2(0, 0);
+                }
+            }
+        }
+    };
+    load_h1(nb);
+    // lane holds row lane & 31 of each 32-row block and, in register 4q + x, column 8q + 4(lane >> 5) + x of the wave's 32
+    const int64_t qblock = static_cast<int64_t>(p.M) * 64;
+    auto put8 = [&](uint32_t bytes, int r, int c) {     // four 8-bit values from padded column c of row r
+        *reinterpret_cast<uint32_t*>(p.q_out + (c >> 6) * qblock + static_cast<int64_t>(row0 + r) * 64 + (c & 63)) = bytes;
+    };
+    auto put_scale = [&](const F8Scale& s, int r, int kb) {
+        p.s_out[(static_cast<int64_t>(kb >> 2) * p.M + row0 + r) * 4 + (kb & 3)] = static_cast<uint8_t>(s.byte);
+    };
+    // The maxima of a block of 128 columns from those of the waves' 32 each (0 .. PARTS - 1 of them for a row).
+    auto block_tops = [&](uint32_t (&top)[TB], int part) {
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            top[i] = max_other_half(top[i]);
+            if (lane < 32) s_top[part][wave][32 * i + lane] = top[i];
+        }
+    };
+    auto join_tops = [&](uint32_t (&top)[TB], int part) {
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            const int r = 32 * i + (lane & 31);
+            top[i] = max(max(s_top[part][0][r], s_top[part][1][r]), max(s_top[part][2][r], s_top[part][3][r]));
+        }
+    };
+    auto epilogue = [&]() {
+        const int c0 = nb * F8_BLOCK + 32 * wave;     // padded column
+        if constexpr (EPI == F8_STORE) {
+            const int h = c0 >= p.n.part_p, k0 = c0 - h * p.n.part_p;
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                const int r = i * 32 + (lane & 31);
+                uint16_t* o = p.out + static_cast<int64_t>(row0 + r) * p.n.real() + h * p.n.part;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int k = k0 + 8 * q + 4 * (lane >> 5);
+                    if (r < rows && k < p.n.part && nb < nb1)
+                        *reinterpret_cast<uint2*>(o + k) = make_uint2(pack2(acc[0][i][4 * q], acc[0][i][4 * q + 1]),
+                                                                      pack2(acc[0][i][4 * q + 2], acc[0][i][4 * q + 3]));
+                }
+            }
+        } else {
+            constexpr int PARTS = EPI == F8_STORE_DGLU ? 2 : 1;
+            uint32_t v[PARTS][TB][8], top[PARTS][TB];
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                const int r = i * 32 + (lane & 31);
+#pragma unroll
+                for (int h = 0; h < PARTS; ++h) top[h][i] = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = c0 + 8 * q + 4 * (lane >> 5);
+                    uint2 b[C];
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        b[j] = make_uint2(pack2(acc[j][i][4 * q], acc[j][i][4 * q + 1]),
+                                          pack2(acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]));
+                    if constexpr (EPI == F8_STORE_GLU) {
+                        if (p.out && r < rows && c < p.n.part && nb < nb1) {
+                            uint16_t* o = p.out + static_cast<int64_t>(row0 + r) * p.n.real() + c;
+                            *reinterpret_cast<uint2*>(o) = b[0];
+                            *reinterpret_cast<uint2*>(o + p.n.part) = b[C - 1];
+                        }
+                        v[0][i][2 * q] = pack2(f8_act(lo_f(b[0].x), lo_f(b[C - 1].x), p.slope), f8_act(hi_f(b[0].x), hi_f(b[C - 1].x), p.slope));
+                        v[0][i][2 * q + 1] = pack2(f8_act(lo_f(b[0].y), lo_f(b[C - 1].y), p.slope), f8_act(hi_f(b[0].y), hi_f(b[C - 1].y), p.slope));
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t d = y ? b[0].y : b[0].x, g = y ? hg[i][q].y : hg[i][q].x, u = y ? hu[i][q].y : hu[i][q].x;
+                            float g0, u0, g1, u1;
+                            f8_act_grad(lo_f(g), lo_f(u), lo_f(d), p.slope, g0, u0);
+                            f8_act_grad(hi_f(g), hi_f(u), hi_f(d), p.slope, g1, u1);
+                            v[0][i][2 * q + y] = pack2(g0, g1);
+                            v[PARTS - 1][i][2 * q + y] = pack2(u0, u1);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h)
+                        top[h][i] = max(top[h][i], max(f8_top2(v[h][i][2 * q]), f8_top2(v[h][i][2 * q + 1])));
+                }
+            }
+            block_barrier();     // the last block's maxima are read
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) block_tops(top[h], h);
+            block_barrier();
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) {
+                join_tops(top[h], h);
+                const int part_p = p.n.part_p, kb = nb + h * (part_p / F8_BLOCK);
+#pragma unroll
+                for (int i = 0; i < TB; ++i) {
+                    const int r = i * 32 + (lane & 31);
+                    const F8Scale sc = f8_scale(top[h][i]);
+                    if (r >= rows || nb >= nb1) continue;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t a = v[h][i][2 * q], b = v[h][i][2 * q + 1];
+                        put8(f8_four(lo_f(a), hi_f(a), lo_f(b), hi_f(b), sc), r, h * part_p + c0 + 8 * q + 4 * (lane >> 5));
+                    }
+                    if (wave == 0 && lane < 32) put_scale(sc, r, kb);
+                }
+            }
+        }
+    };
+    int k = 0;
+    for (int f = 0; f < total; f += R) {
+        // the last round's units past the end multiply what was loaded last and are not stored
+        static_for<R>([&](auto i_tag) {
+            constexpr int at = decltype(i_tag)::value;
+            load(wv[(at + R - 1) % R], wsv[(at + R - 1) % R]);
+            const uint8_t* op = panel + k * (TB * 4096) + lane * 16;
+            int ts[TB];
+#pragma unroll
+            for (int i = 0; i < TB; ++i) ts[i] = pscale[(k * TB + i) * 32 + (lane & 31)];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < TB; ++i) {
+                    const uint8_t* o = op + (u * TB + i) * 2048;
+                    const i32x8 t = f8_join(*reinterpret_cast<const i32x4*>(o), *reinterpret_cast<const i32x4*>(o + 1024));
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        acc[c][i] = f8_mma(f8_join(wv[at][c][2 * u], wv[at][c][2 * u + 1]), t, acc[c][i], wsv[at][c], ts[i]);
+                }
+            if (++k == nu) {
+                k = 0;
+                epilogue();
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int i = 0; i < TB; ++i) acc[c][i] = f32x16{};
+                ++nb;
+                load_h1(min(nb, nb1 - 1));
+            }
+        });
     }
 }
 
-// The list of all (row group, 128-column block) pairs, groups of up to 96 rows, a workgroup an item and a wave 32
-// of its columns.
-constexpr int F8_GROUP = 96;
-
-__global__ __launch_bounds__(256) void f8_stream_kernel(const F8Params p) {
-    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
-    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
-    const int nblocks = p.n.blocks();
-    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) { return (m + F8_GROUP - 1) / F8_GROUP * nblocks; });
-    const int total = uni(s_pre[p.E]);
-    const int wave = uni(threadIdx.x >> 6);
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
-        const int e = uni(find_expert_wave(s_pre, p.E, it));
-        const int local = it - uni(s_pre[e]), grp = local / nblocks, nb = (local - grp * nblocks) * 4 + wave;
-        const int row0 = uni(s_off[e]) + grp * F8_GROUP, rows = min(F8_GROUP, uni(s_off[e + 1]) - row0);
+// The list of all (row group, 128-column block) pairs, in equal stretches to the workgroups.  s_off, s_pre: [E + 1].
+template <int EPI>
+__device__ __forceinline__ void f8_stream_list(const F8Params& p, int* s_off, int* s_pre, uint8_t* panel,
+                                               uint32_t (*s_top)[4][F8_GROUP]) {
+    const int nblocks = EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : p.n.blocks();
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre, [&](int m) {
+        return (m - f8_tile_rows(m, p.tile, p.group) + p.group - 1) / p.group * nblocks;
+    });
+    const int64_t total = uni(s_pre[p.E]);
+    int at = static_cast<int>(total * blockIdx.x / gridDim.x);
+    const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+    while (at < end) {   // one row group's part of the stretch
+        const int e = uni(find_expert_wave(s_pre, p.E, at));
+        const int local = at - uni(s_pre[e]), grp = local / nblocks, nb0 = local - grp * nblocks;
+        const int nb1 = min(nblocks, nb0 + end - at);
+        const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
+        const int row0 = lo + f8_tile_rows(hi - lo, p.tile, p.group) + grp * p.group;
+        const int rows = min(p.group, hi - row0);
         const uint8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
         const uint8_t* ws = p.ws + static_cast<int64_t>(e) * p.ws_stride;
         const int tb = (rows + 31) / 32;
-        if (tb == 1) f8_stream_block<1>(p, w, ws, row0, rows, nb);
-        else if (tb == 2) f8_stream_block<2>(p, w, ws, row0, rows, nb);
-        else f8_stream_block<3>(p, w, ws, row0, rows, nb);
+        if (tb == 1) f8_stream_blocks<1, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
+        else if (tb == 2) f8_stream_blocks<2, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
+        else f8_stream_blocks<3, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
+        at += nb1 - nb0;
     }
+}
+
+template <int EPI>
+__global__ __launch_bounds__(256, 1) void f8_stream_kernel(const F8Params p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[F8_RING];
+    __shared__ uint32_t s_top[2][4][F8_GROUP];
+    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
+    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
+    f8_stream_list<EPI>(p, s_off, s_pre, s_ring, s_top);
+}
+
+// ---- Tiles: 64 BR rows x 64 BC packed columns by four waves, each 32 BR x
+// 32 BC, as BR x BC accumulators of 32 x 32.  With F8_STORE_GLU a wave's
+// columns are half gate, half the same columns of up, so that A is made where
+// the sums are.
+// Rows, their scales and weights stream into an LDS ring of 64-column stages by
+// LDS-DMA, all but one of them ahead: the rows, 16-byte chunk c of row r at
+// c ^ ((r >> 2) & 3), the weights as they lie in the packed layout (fragment
+// reads of both are free of bank conflicts), and for each row the dword with
+// the scale of the stage's block.  A stage is BR x BC matrix instructions a
+// wave; after the first BC of them the next stage has landed and every wave
+// holds its fragments of this one, whose slot is refilled from there on while
+// the next stage's fragments are read.  The epilogue goes through a small
+// staging area of its own, so the next tile's first stages are already on
+// their way, and the waits of those stages leave the epilogue's stores
+// outstanding: memory operations complete in order.
+constexpr int F8_STAGE = 64;
+constexpr int F8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf16
+
+template <int BR, int BC, int EPI>
+__global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
+    constexpr int TR = 64 * BR, TC = 64 * BC;               // rows and packed columns of a tile
+    constexpr int OC = EPI == F8_STORE_GLU ? TC / 2 : TC;   // columns of what it makes
+    static_assert(EPI == F8_STORE || BC == 4, "a quantized block's columns lie in one tile");
+    constexpr int W_AT = TR * F8_STAGE, S_AT = W_AT + TC * F8_STAGE;
+    constexpr int SLOT_BYTES = S_AT + TR * 4, SLOTS = BR == 4 ? 4 : (BC == 4 ? 4 : 8);
+    static_assert(SLOTS * SLOT_BYTES <= F8_RING, "the ring");
+    constexpr int P = BR + BC + 1;                          // copies a wave issues for a stage
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[F8_RING];
+    __shared__ __attribute__((aligned(16))) uint8_t s_stg[4 * F8_STG_BYTES];
+    __shared__ uint32_t s_row_top[EPI == F8_STORE_GLU ? 4 * 32 * BR : 1];
+    __shared__ int s_off[GG_KMAX_EXPERTS + 1];
+    __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
+    const int nsteps = p.kblocks * 2, nstages = nsteps;
+    const int part_p = p.n.part_p, width = EPI == F8_STORE_GLU ? part_p : p.n.padded();
+    const int tiles_n = (width + OC - 1) / OC;
+    prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
+                   [&](int m) { return (f8_tile_rows(m, TR, p.group) + TR - 1) / TR * tiles_n; });
+    const int n_tiles = uni(s_pre[p.E]);
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int wr = wave >> 1, wc = wave & 1;      // the wave's rows and columns
+    // consecutive tiles to the workgroups of one XCD, which share an L2
+    const int G = gridDim.x, b = blockIdx.x;
+    const int slot = (G % 8 == 0) ? (b & 7) * (G >> 3) + (b >> 3) : b;
+    const uint32_t ring = lds_addr(s_ring);
+
+    // what the copies of one tile read
+    const uint8_t* t_base = nullptr;   // its first row
+    const uint8_t* s_base = nullptr;   // that row's scales
+    const uint8_t* w_base = nullptr;   // its expert's matrix
+    const uint8_t* ws_base[2];         // the scales of this wave's columns (F8_STORE_GLU: of gate and up)
+    uint32_t t_voff[BR], s_voff;       // this lane's chunks of rows 16 BR wave + 16 i .., its scale
+    int wb[BC];                        // the 32-column block of each 1 KiB piece that this wave copies
+    const int64_t t_block = static_cast<int64_t>(p.M) * F8_STAGE;   // bytes of 64 columns of all rows
+    const int64_t s_block = static_cast<int64_t>(p.M) * 4;          // and of four blocks' scales
+    int e = 0, row0 = 0, rows = 0, col0 = 0;
+    auto setup = [&](int t) {
+        e = uni(find_expert_wave(s_pre, p.E, t));
+        const int local = t - uni(s_pre[e]);
+        const int lo = uni(s_off[e]), m = f8_tile_rows(uni(s_off[e + 1]) - lo, TR, p.group);
+        const int tiles_m = (m + TR - 1) / TR;
+        const int tm = local % tiles_m, tn = local / tiles_m;
+        row0 = lo + tm * TR;
+        rows = min(TR, m - tm * TR);
+        col0 = tn * OC;
+        t_base = p.q + static_cast<int64_t>(row0) * F8_STAGE;
+        s_base = p.s + static_cast<int64_t>(row0) * 4;
+        w_base = p.w + static_cast<int64_t>(e) * p.w_stride;
+        const uint8_t* ws = p.ws + static_cast<int64_t>(e) * p.ws_stride;
+        const int rb = col0 / F8_BLOCK + (EPI != F8_STORE_GLU && BC == 4 ? wc : 0);
+        ws_base[0] = ws + static_cast<int64_t>(min(rb, p.n.blocks() - 1)) * p.ws_ld;
+        ws_base[1] = EPI == F8_STORE_GLU ? ws_base[0] + static_cast<int64_t>(part_p / F8_BLOCK) * p.ws_ld : ws_base[0];
+#pragma unroll
+        for (int i = 0; i < BR; ++i) {
+            const int r = 16 * BR * wave + 16 * i + (lane >> 2);
+            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            t_voff[i] = static_cast<uint32_t>(min(r, rows - 1)) * F8_STAGE + 16 * c;
+        }
+        s_voff = static_cast<uint32_t>(min((64 * wave + lane) & (TR - 1), rows - 1)) * 4;
+#pragma unroll
+        for (int i = 0; i < BC; ++i) {
+            const int at = (wave * BC + i) >> 1;          // the block's place in the tile
+            if constexpr (EPI == F8_STORE_GLU)            // each wave column: two gate blocks, then two of up
+                wb[i] = ((at & 3) >> 1) * (part_p / 32) + col0 / 32 + 2 * (at >> 2) + (at & 1);
+            else
+                wb[i] = min(col0 / 32 + at, width / 32 - 1);
+        }
+    };
+    // One of the P copies of a stage that this wave issues (nothing past the last stage).
+    auto piece = [&](int st, auto i_tag) {
+        constexpr int i = decltype(i_tag)::value;
+        if (st >= nstages) return;
+        const uint32_t dst = ring + (st & (SLOTS - 1)) * SLOT_BYTES;
+        if constexpr (i < BR) {
+            dma16(t_base + st * t_block, t_voff[i], dst + (16 * BR * wave + 16 * i) * F8_STAGE);
+        } else if constexpr (i < BR + BC) {
+            constexpr int j = i - BR;
+            const int g = wave * BC + j;
+            dma16(w_base + (static_cast<int64_t>(wb[j]) * nsteps + st) * 2048 + (g & 1) * 1024, lane * 16, dst + W_AT + g * 1024);
+        } else {
+            dma4(s_base + (st >> 3) * s_block, s_voff, dst + S_AT + ((64 * wave) & (TR - 1)) * 4);
+        }
+    };
+
+    f32x16 acc[BR][BC];    // [row block][column block]
+    i32x8 tf[2][BR], wf[2][BC];
+    int ts[BR], ts_next[BR], wsc[2];        // scales of the block that is multiplied, and of the next
+    uint32_t wd[2], wd_next[2];             // the weights' scales, four blocks in a dword
+    auto read_t = [&](int st, auto u_tag) {
+        constexpr int u = decltype(u_tag)::value;
+        const uint8_t* sl = s_ring + (st & (SLOTS - 1)) * SLOT_BYTES;
+        const int c = (2 * (lane >> 5)) ^ ((lane >> 2) & 3);
+#pragma unroll
+        for (int i = 0; i < BR; ++i) {
+            const uint8_t* r = sl + (32 * BR * wr + 32 * i + (lane & 31)) * F8_STAGE;
+            tf[u][i] = f8_join(*reinterpret_cast<const i32x4*>(r + 16 * c), *reinterpret_cast<const i32x4*>(r + 16 * (c ^ 1)));
+        }
+        if constexpr (u == 0) {     // the first of a block's two stages
+#pragma unroll
+            for (int i = 0; i < BR; ++i) ts_next[i] = sl[S_AT + (32 * BR * wr + 32 * i + (lane & 31)) * 4 + ((st >> 1) & 3)];
+        }
+    };
+    auto read_w = [&](int st, auto u_tag) {
+        constexpr int u = decltype(u_tag)::value;
+        const uint8_t* sl = s_ring + (st & (SLOTS - 1)) * SLOT_BYTES + W_AT;
+#pragma unroll
+        for (int j = 0; j < BC; ++j) {
+            const uint8_t* f = sl + (BC * wc + j) * 2048 + lane * 16;
+            wf[u][j] = f8_join(*reinterpret_cast<const i32x4*>(f), *reinterpret_cast<const i32x4*>(f + 1024));
+        }
+    };
+    // the BC matrix instructions of row block i; the tile's first step starts its sums from zero
+    auto mma = [&](auto u_tag, auto i_tag, auto first_tag) {
+        constexpr int u = decltype(u_tag)::value, i = decltype(i_tag)::value;
+#pragma unroll
+        for (int j = 0; j < BC; ++j) {
+            const int s = EPI == F8_STORE_GLU ? wsc[j >= BC / 2] : wsc[0];
+            if constexpr (decltype(first_tag)::value != 0)
+                acc[i][j] = f8_mma(wf[u][j], tf[u][i], f32x16{}, s, ts[i]);
+            else
+                acc[i][j] = f8_mma(wf[u][j], tf[u][i], acc[i][j], s, ts[i]);
+        }
+    };
+    auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
+    // Waits until at most n copies and stores issued after those of the stage that is needed are outstanding.
+    auto wait_after = [&](int n) {
+        if (n >= 60) wait_vmcnt<60>();
+        else if (n >= 52) wait_vmcnt<52>();
+        else if (n >= 44) wait_vmcnt<44>();
+        else if (n >= 36) wait_vmcnt<36>();
+        else if (n >= 27) wait_vmcnt<27>();
+        else if (n >= 21) wait_vmcnt<21>();
+        else if (n >= 18) wait_vmcnt<18>();
+        else if (n >= 14) wait_vmcnt<14>();
+        else if (n >= 9) wait_vmcnt<9>();
+        else if (n >= 7) wait_vmcnt<7>();
+        else if (n >= 5) wait_vmcnt<5>();
+        else wait_vmcnt<0>();
+    };
+    // Stage st, of the parity u.  behind: the stores issued behind the copies of the prologue's stages, at least.
+    auto stage = [&](int st, int behind, auto u_tag, auto first_tag, auto last_tag) {
+        constexpr int u = decltype(u_tag)::value;
+        constexpr bool LAST = decltype(last_tag)::value != 0;
+        if constexpr (u == 0) {
+            const int k = st >> 1;
+#pragma unroll
+            for (int i = 0; i < BR; ++i) ts[i] = ts_next[i];
+            if ((k & 3) == 0) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    wd[c] = wd_next[c];
+                    wd_next[c] = scalar_load(ws_base[c] + min(k + 4, p.ws_ld - 4));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) wsc[c] = static_cast<int>(wd[c] >> (8 * (k & 3)));
+        }
+        mma(u_tag, GrpTag<0>{}, first_tag);
+        fence();
+        if constexpr (!LAST) {
+            // stage st + 1 has landed, and every wave holds its fragments of stage st, whose slot is refilled from here on
+            if (st >= SLOTS - 1 && st + SLOTS <= nstages) wait_vmcnt<P*(SLOTS - 2)>();
+            else wait_after(P * min(nstages - 2 - st, SLOTS - 2) + (st < SLOTS - 1 ? behind : 0));
+            block_barrier();
+        }
+        static_for<BR - 1>([&](auto it) {
+            constexpr int i = decltype(it)::value;
+            if constexpr (!LAST) {
+                if constexpr (i == 0) read_w(st + 1, GrpTag<u ^ 1>{});
+                if constexpr (i == (BR > 2 ? 1 : 0)) read_t(st + 1, GrpTag<u ^ 1>{});
+            }
+            mma(u_tag, GrpTag<i + 1>{}, first_tag);
+            if constexpr (!LAST) {
+                constexpr int a = i * P / (BR - 1), z = (i + 1) * P / (BR - 1);
+                static_for<z - a>([&](auto j) { piece(st + SLOTS, GrpTag<a + decltype(j)::value>{}); });
+            }
+            fence();
+        });
+    };
+    // the copies before a tile's first stage: the whole ring's
+    auto prologue = [&]() {
+        for (int st = 0; st < SLOTS; ++st) static_for<P>([&](auto i) { piece(st, i); });
+    };
+
+    int t = slot, stores = 0;
+    if (t < n_tiles) {
+        setup(t);
+        prologue();
+    }
+    while (t < n_tiles) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) wd_next[c] = scalar_load(ws_base[c]);
+        wait_after(P * min(nstages - 1, SLOTS - 1) + stores);        // stage 0
+        block_barrier();
+        read_w(0, GrpTag<0>{});
+        read_t(0, GrpTag<0>{});
+        // an even number of stages, at least two
+        if (nstages == 2) {
+            stage(0, stores, GrpTag<0>{}, GrpTag<1>{}, GrpTag<0>{});
+        } else {
+            stage(0, stores, GrpTag<0>{}, GrpTag<1>{}, GrpTag<0>{});
+            stage(1, stores, GrpTag<1>{}, GrpTag<0>{}, GrpTag<0>{});
+            for (int st = 2; st < nstages - 2; st += 2) {
+                stage(st, stores, GrpTag<0>{}, GrpTag<0>{}, GrpTag<0>{});
+                stage(st + 1, stores, GrpTag<1>{}, GrpTag<0>{}, GrpTag<0>{});
+            }
+            stage(nstages - 2, stores, GrpTag<0>{}, GrpTag<0>{}, GrpTag<0>{});
+        }
+        stage(nstages - 1, stores, GrpTag<1>{}, GrpTag<0>{}, GrpTag<1>{});
+        const int prow0 = row0, prows = rows, pcol0 = col0;
+        t += G;
+        block_barrier();         // every wave is done with the ring
+        if (t < n_tiles) {
+            setup(t);
+            prologue();
+        }
+        mfma_drain();
+        int opaque = 0;
+        asm volatile("" : "+s"(opaque));
+        const int ln = lane + opaque;
+        uint16_t* stg = reinterpret_cast<uint16_t*>(s_stg + wave * F8_STG_BYTES) + opaque;
+        // Blocks of 32 rows x 64 bf16 columns go through the staging area, [32 rows][64 columns] with 16-byte chunk c
+        // of row r at c ^ (r & 7); lane's part of the sums: row ln & 31, columns 8 c + 4 (ln >> 5) .. + 3.
+        auto put = [&](const uint2 (&v)[8]) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int rr = ln & 31;
+                *reinterpret_cast<uint2*>(stg + rr * 64 + ((c ^ (rr & 7)) << 3) + 4 * (ln >> 5)) = v[c];
+            }
+        };
+        auto take = [&](uint2 (&v)[8]) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int rr = ln & 31;
+                v[c] = *reinterpret_cast<const uint2*>(stg + rr * 64 + ((c ^ (rr & 7)) << 3) + 4 * (ln >> 5));
+            }
+        };
+        // the same block by rows: lane has row 8 k + (ln >> 3), 16-byte chunk (ln & 7) ^ (ln >> 3)
+        auto rows_of = [&](uint4 (&o)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = *reinterpret_cast<const uint4*>(stg + (8 * k + (ln >> 3)) * 64 + (ln & 7) * 8);
+        };
+        const int chunk = 8 * ((ln & 7) ^ (ln >> 3));
+        // the bf16 sums of block (i, column blocks 2 jh and 2 jh + 1)
+        auto sums = [&](auto i_tag, auto jh_tag, uint2 (&v)[8]) {
+            constexpr int i = decltype(i_tag)::value, jh = decltype(jh_tag)::value;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const f32x16& a = acc[i][2 * jh + (c >> 2)];
+                const int q = c & 3;
+                v[c] = make_uint2(pack2(acc_rd(a[4 * q]), acc_rd(a[4 * q + 1])), pack2(acc_rd(a[4 * q + 2]), acc_rd(a[4 * q + 3])));
+            }
+        };
+        // a block's rows to columns col .. of `to` (row stride ld), of which those below `cols` exist
+        auto store = [&](const uint4 (&o)[4], uint16_t* to, int64_t ld, int i, int cols, bool full) {
+            const int gr = 32 * BR * wr + 32 * i + (ln >> 3);
+            uint16_t* at = to + static_cast<int64_t>(prow0 + gr) * ld + chunk;
+            if (full) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) st16_nt(at + static_cast<int64_t>(8 * k) * ld, o[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (gr + 8 * k < prows && chunk < cols) st16_nt(at + static_cast<int64_t>(8 * k) * ld, o[k]);
+            }
+        };
+        // 32 rows x 64 8-bit columns, of which lane has row ln & 31 and the dwords d[c] of columns 8 c + 4 (ln >> 5),
+        // through half of the staging area ([32 rows][64 bytes], chunk c of row r at c ^ ((r >> 2) & 3)) to padded column col
+        const int64_t qblock = static_cast<int64_t>(p.M) * 64;
+        auto store8 = [&](const uint32_t (&d)[8], int half, int i, int col, bool full) {
+            uint8_t* st8 = reinterpret_cast<uint8_t*>(stg) + half * 2048;
+            const int rr = ln & 31;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint32_t*>(st8 + rr * 64 + (((c >> 1) ^ ((rr >> 2) & 3)) << 4) + 8 * (c & 1) + 4 * (ln >> 5)) = d[c];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = 16 * k + (ln >> 2), gr = 32 * BR * wr + 32 * i + r;
+                const uint4 v = *reinterpret_cast<const uint4*>(st8 + r * 64 + (((ln & 3) ^ ((r >> 2) & 3)) << 4));
+                if (full || gr < prows)
+                    *reinterpret_cast<uint4*>(p.q_out + (col >> 6) * qblock + static_cast<int64_t>(prow0 + gr) * 64 + 16 * (ln & 3)) = v;
+            }
+        };
+        auto store_scale = [&](const F8Scale& sc, int i, int kb) {     // lanes below 32
+            const int gr = 32 * BR * wr + 32 * i + ln;
+            if (ln < 32 && gr < prows)
+                p.s_out[(static_cast<int64_t>(kb >> 2) * p.M + prow0 + gr) * 4 + (kb & 3)] = static_cast<uint8_t>(sc.byte);
+        };
+        const bool all_rows = prows == TR;
+        // All stores of a wave are issued where the tile is full; a store whose lanes all lie outside may be
+        // skipped, so a partial tile counts as none.
+        if constexpr (EPI == F8_STORE) {
+            const bool full = all_rows && (p.n.parts == 1 || p.n.part == part_p) && pcol0 + TC <= p.n.real();
+            stores = full ? 2 * BR * BC : 0;
+            const int gc0 = pcol0 + 32 * BC * wc;
+            uint2 vals[8];
+            sums(GrpTag<0>{}, GrpTag<0>{}, vals);
+            put(vals);
+            static_for<BR * BC / 2>([&](auto b_tag) {
+                constexpr int blk = decltype(b_tag)::value, i = blk % BR, jh = blk / BR, nx = blk + 1;
+                if constexpr (nx < BR * BC / 2) sums(GrpTag<nx % BR>{}, GrpTag<nx / BR>{}, vals);
+                uint4 out[4];
+                rows_of(out);
+                if constexpr (nx < BR * BC / 2) put(vals);
+                const int c = gc0 + 64 * jh, h = c >= part_p, k = c - h * part_p;
+                store(out, p.out + h * p.n.part + k, p.n.real(), i, p.n.part - k, full);
+            });
+        } else if constexpr (EPI == F8_STORE_GLU) {
+            const int k0 = pcol0 + 64 * wc;          // the wave's 64 columns of gate, up and A
+            const bool full = all_rows && k0 + 64 <= p.n.part;
+            stores = all_rows ? 2 * BR + (p.out && pcol0 + OC <= p.n.part ? 8 * BR : 0) : 0;
+            uint32_t av[BR][16], top[BR];
+            static_for<BR>([&](auto i_tag) {
+                constexpr int i = decltype(i_tag)::value;
+                uint2 g[8], u[8];
+                sums(i_tag, GrpTag<0>{}, g);
+                sums(i_tag, GrpTag<1>{}, u);
+                top[i] = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), p.slope), f8_act(hi_f(g[c].x), hi_f(u[c].x), p.slope));
+                    av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), p.slope), f8_act(hi_f(g[c].y), hi_f(u[c].y), p.slope));
+                    top[i] = max(top[i], max(f8_top2(av[i][2 * c]), f8_top2(av[i][2 * c + 1])));
+                }
+                top[i] = max_other_half(top[i]);
+                if (ln < 32) s_row_top[wave * 32 * BR + 32 * i + ln] = top[i];
+                if (p.out) {
+                    uint4 o[4];
+                    put(g);
+                    rows_of(o);
+                    put(u);
+                    store(o, p.out + k0, p.n.real(), i, p.n.part - k0, full);
+                    rows_of(o);
+                    store(o, p.out + p.n.part + k0, p.n.real(), i, p.n.part - k0, full);
+                }
+            });
+            block_barrier();
+#pragma unroll
+            for (int i = 0; i < BR; ++i) {
+                const F8Scale sc = f8_scale(max(top[i], s_row_top[(wave ^ 1) * 32 * BR + 32 * i + (ln & 31)]));
+                uint32_t d[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    d[c] = f8_four(lo_f(av[i][2 * c]), hi_f(av[i][2 * c]), lo_f(av[i][2 * c + 1]), hi_f(av[i][2 * c + 1]), sc);
+                store8(d, i & 1, i, k0, all_rows);
+                if (wc == 0) store_scale(sc, i, pcol0 / F8_BLOCK);
+            }
+        } else {
+            const int k0 = pcol0 + F8_BLOCK * wc, kb = k0 / F8_BLOCK;     // the wave's block of dA
+            stores = all_rows && k0 < part_p ? 8 * BR : 0;
+            if (k0 < part_p) {
+                // the rows of h1, gate and up, of block (i, 64 columns jh)
+                uint4 hg[4], hu[4];
+                auto load_h1 = [&](int i, int jh) {
+                    const int c = k0 + 64 * jh + chunk;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int gr = min(32 * BR * wr + 32 * i + 8 * k + (ln >> 3), prows - 1);
+                        const uint16_t* h = p.h1 + static_cast<int64_t>(prow0 + gr) * 2 * p.n.part + c;
+                        const uint4 zero = make_uint4(0, 0, 0, 0);
+                        hg[k] = c < p.n.part ? ld16_nt(h) : zero;
+                        hu[k] = c < p.n.part ? ld16_nt(h + p.n.part) : zero;
+                    }
+                };
+                auto put_rows = [&](const uint4 (&o)[4]) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(stg + (8 * k + (ln >> 3)) * 64 + (ln & 7) * 8) = o[k];
+                };
+                load_h1(0, 0);
+                static_for<BR>([&](auto i_tag) {
+                    constexpr int i = decltype(i_tag)::value;
+                    uint32_t v[2][2][16], top[2] = {0, 0};      // [gate, up][64 columns]
+                    static_for<2>([&](auto jh_tag) {
+                        constexpr int jh = decltype(jh_tag)::value;
+                        uint2 d[8], g[8], u[8];
+                        put_rows(hg);
+                        take(g);
+                        put_rows(hu);
+                        take(u);
+                        if constexpr (2 * i + jh + 1 < 2 * BR) load_h1((2 * i + jh + 1) / 2, (jh + 1) % 2);
+                        sums(i_tag, jh_tag, d);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t dd = y ? d[c].y : d[c].x, gg = y ? g[c].y : g[c].x, uu = y ? u[c].y : u[c].x;
+                                float g0, u0, g1, u1;
+                                f8_act_grad(lo_f(gg), lo_f(uu), lo_f(dd), p.slope, g0, u0);
+                                f8_act_grad(hi_f(gg), hi_f(uu), hi_f(dd), p.slope, g1, u1);
+                                v[0][jh][2 * c + y] = pack2(g0, g1);
+                                v[1][jh][2 * c + y] = pack2(u0, u1);
+                                top[0] = max(top[0], f8_top2(v[0][jh][2 * c + y]));
+                                top[1] = max(top[1], f8_top2(v[1][jh][2 * c + y]));
+                            }
+                    });
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const F8Scale sc = f8_scale(max_other_half(top[h]));
+#pragma unroll
+                        for (int jh = 0; jh < 2; ++jh) {
+                            uint32_t d[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint32_t x = v[h][jh][2 * c], y = v[h][jh][2 * c + 1];
+                                d[c] = f8_four(lo_f(x), hi_f(x), lo_f(y), hi_f(y), sc);
+                            }
+                            store8(d, jh, i, h * part_p + k0 + 64 * jh, all_rows);
+                        }
+                        store_scale(sc, i, kb + h * (part_p / F8_BLOCK));
+                    }
+                });
+            }
+        }
+    }
+    if (p.group == 0) return;
+    __syncthreads();
+    f8_stream_list<EPI>(p, s_off, s_pre, s_ring, reinterpret_cast<uint32_t(*)[4][F8_GROUP]>(s_stg));
 }
 
 // ---------------------------------------------------------------- launchers
@@ -391,11 +1036,37 @@ hipError_t launch_f8_pack(const uint8_t* q, const uint8_t* s, int E, const F8Dim
     return hipGetLastError();
 }
 
-hipError_t launch_f8_gemm(const F8Params& p, int num_cu, hipStream_t s) {
-    const int64_t groups = static_cast<int64_t>(p.M) / F8_GROUP + (p.M < p.E ? p.M : p.E);
-    const int64_t upper = groups * p.n.blocks(), most = static_cast<int64_t>(num_cu) * 3;
-    hipLaunchKernelGGL(f8_stream_kernel, dim3(static_cast<unsigned>(upper < most ? upper : most)), dim3(256), 0, s, p);
+template <int BR, int BC, int EPI>
+static hipError_t launch_tiles(const F8Params& p, int num_cu, hipStream_t s) {
+    constexpr int TR = 64 * BR, OC = EPI == F8_STORE_GLU ? 32 * BC : 64 * BC;
+    const int width = EPI == F8_STORE_GLU ? p.n.part_p : p.n.padded();
+    const int64_t upper = (static_cast<int64_t>(p.M) / TR + (p.M < p.E ? p.M : p.E)) * ((width + OC - 1) / OC);
+    const dim3 grid(static_cast<unsigned>(upper < num_cu && p.group == 0 ? upper : num_cu));
+    hipLaunchKernelGGL((f8_tile_kernel<BR, BC, EPI>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
+}
+
+template <int EPI>
+static hipError_t launch_gemm(const F8Params& p, int num_cu, hipStream_t s) {
+    F8Params g = p;
+    const int tiles_n = EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : (p.n.padded() + 255) / 256;
+    const F8Plan plan = f8_plan(p.M, p.E, tiles_n, p.kblocks, num_cu);
+    g.tile = plan.tile;
+    g.group = plan.group;
+    if (g.tile == 256) return launch_tiles<4, 4, EPI>(g, num_cu, s);
+    if (g.tile) return launch_tiles<2, EPI == F8_STORE ? 2 : 4, EPI>(g, num_cu, s);
+    const int64_t groups = static_cast<int64_t>(p.M) / g.group + (p.M < p.E ? p.M : p.E);
+    const int64_t upper = groups * (EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : p.n.blocks());
+    hipLaunchKernelGGL((f8_stream_kernel<EPI>), dim3(static_cast<unsigned>(upper < num_cu ? upper : num_cu)), dim3(256), 0, s, g);
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_gemm(F8Epilogue epilogue, const F8Params& p, int num_cu, hipStream_t s) {
+    switch (epilogue) {
+        case F8_STORE: return launch_gemm<F8_STORE>(p, num_cu, s);
+        case F8_STORE_GLU: return launch_gemm<F8_STORE_GLU>(p, num_cu, s);
+        default: return launch_gemm<F8_STORE_DGLU>(p, num_cu, s);
+    }
 }
 
 }  // namespace gg

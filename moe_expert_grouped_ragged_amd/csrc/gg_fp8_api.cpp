@@ -69,7 +69,7 @@ F8QuantParams quantization(const void* x, const void* h1, const int64_t* offsets
 
 int quantize_and_multiply(F8Mode mode, const F8QuantParams& p, const F8Params& g, int num_cu, hipStream_t stream) {
     if (launch_f8_quant(mode, p, num_cu, stream) != hipSuccess) return GG_ERR_HIP;
-    return launch_f8_gemm(g, num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+    return launch_f8_gemm(F8_STORE, g, num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 // Quantized rows start on 256 bytes.
@@ -189,8 +189,7 @@ int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t
 
 size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad) {
     if (M == 0 || check_fp8_shape(M, 1, 2 * F, H, 2) != GG_OK) return 0;
-    const size_t rows = glu_rows(M, f8_dim(H, 1)) + glu_rows(M, f8_dim(dgrad ? 2 * F : F, dgrad ? 2 : 1));
-    return rows + static_cast<size_t>(M) * (dgrad ? F : 2 * F) * 2;   // dA, or H1 where it is not saved
+    return glu_rows(M, f8_dim(H, 1)) + glu_rows(M, f8_dim(dgrad ? 2 * F : F, dgrad ? 2 : 1));
 }
 
 int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2, int64_t E,
@@ -216,12 +215,14 @@ int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const v
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     const F8Dim h = f8_dim(H, 1), f2 = f8_dim(2 * F, 2), f = f8_dim(F, 1);
     uint8_t *qx = static_cast<uint8_t*>(workspace), *qa = qx + glu_rows(M, h);
-    void* h1 = h1_out ? h1_out : qa + glu_rows(M, f);
-    st = quantize_and_multiply(F8_PLAIN, quantization(x, nullptr, offsets, M, E, h, 1.0f, nullptr, qx),
-                               product(qx, offsets, M, fc1, E, f2, h, h1), info.num_cu, stream);
-    if (st != GG_OK) return st;
-    return quantize_and_multiply(F8_GLU, quantization(h1, nullptr, offsets, M, E, f, slope, nullptr, qa),
-                                 product(qa, offsets, M, fc2, E, h, f, y), info.num_cu, stream);
+    if (launch_f8_quant(F8_PLAIN, quantization(x, nullptr, offsets, M, E, h, 1.0f, nullptr, qx), info.num_cu, stream) != hipSuccess)
+        return GG_ERR_HIP;
+    F8Params g = product(qx, offsets, M, fc1, E, f2, h, h1_out);
+    g.slope = slope;
+    g.q_out = qa;
+    g.s_out = qa + M * f.padded();
+    if (launch_f8_gemm(F8_STORE_GLU, g, info.num_cu, stream) != hipSuccess) return GG_ERR_HIP;
+    return launch_f8_gemm(F8_STORE, product(qa, offsets, M, fc2, E, h, f, y), info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
@@ -247,12 +248,16 @@ int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int
     if ((st = device_info(stream, &info)) != GG_OK) return st;
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     const F8Dim h = f8_dim(H, 1), f2 = f8_dim(2 * F, 2), f = f8_dim(F, 1);
-    uint8_t *qy = static_cast<uint8_t*>(workspace), *qd = qy + glu_rows(M, h), *da = qd + glu_rows(M, f2);
-    st = quantize_and_multiply(F8_PLAIN, quantization(dy, nullptr, offsets, M, E, h, 1.0f, nullptr, qy),
-                               product(qy, offsets, M, fc2_t, E, f, h, da), info.num_cu, stream);
-    if (st != GG_OK) return st;
-    return quantize_and_multiply(F8_DGLU, quantization(da, h1, offsets, M, E, f2, slope, nullptr, qd),
-                                 product(qd, offsets, M, fc1_t, E, h, f2, dx), info.num_cu, stream);
+    uint8_t *qy = static_cast<uint8_t*>(workspace), *qd = qy + glu_rows(M, h);
+    if (launch_f8_quant(F8_PLAIN, quantization(dy, nullptr, offsets, M, E, h, 1.0f, nullptr, qy), info.num_cu, stream) != hipSuccess)
+        return GG_ERR_HIP;
+    F8Params g = product(qy, offsets, M, fc2_t, E, f, h, nullptr);
+    g.h1 = static_cast<const uint16_t*>(h1);
+    g.slope = slope;
+    g.q_out = qd;
+    g.s_out = qd + M * f2.padded();
+    if (launch_f8_gemm(F8_STORE_DGLU, g, info.num_cu, stream) != hipSuccess) return GG_ERR_HIP;
+    return launch_f8_gemm(F8_STORE, product(qd, offsets, M, fc1_t, E, h, f2, dx), info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 }  // extern "C"
