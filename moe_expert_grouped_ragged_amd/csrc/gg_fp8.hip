@@ -280,6 +280,16 @@ __device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t l
 }
 #pragma clang diagnostic pop
 
+// dma16 with AT bytes added to both addresses by the instruction.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int AT>
+__device__ __forceinline__ void dma16_at(const void* base, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 offset:%3"
+                 :: "v"(voff), "s"(uni_ptr(base)), "s"(uni(lds)), "i"(AT) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // A dword that no kernel of the launch writes, by the scalar unit.
 __device__ __forceinline__ uint32_t scalar_load(const uint8_t* p) {
     return *(const __attribute__((address_space(4))) uint32_t*)(reinterpret_cast<uintptr_t>(uni_ptr(p)));
@@ -577,6 +587,14 @@ __global__ __launch_bounds__(256, 1) void f8_stream_kernel(const F8Params p) {
 // staging area of its own, so the next tile's first stages are already on
 // their way, and the waits of those stages leave the epilogue's stores
 // outstanding: memory operations complete in order.
+// A value kept in an accumulation register, and back.
+__device__ __forceinline__ float acc_wr(uint32_t v) {
+    float a;
+    asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(a) : "v"(v));
+    return a;
+}
+__device__ __forceinline__ uint32_t acc_rd_u(float a) { return __builtin_bit_cast(uint32_t, acc_rd(a)); }
+
 constexpr int F8_STAGE = 64;
 constexpr int F8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf16
 
@@ -589,6 +607,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     constexpr int SLOT_BYTES = S_AT + TR * 4, SLOTS = BR == 4 ? 4 : (BC == 4 ? 4 : 8);
     static_assert(SLOTS * SLOT_BYTES <= F8_RING, "the ring");
     constexpr int P = BR + BC + 1;                          // copies a wave issues for a stage
+    constexpr int WS = EPI == F8_STORE_GLU ? 2 : 1;         // blocks of weights that a wave's columns lie in
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[F8_RING];
     __shared__ __attribute__((aligned(16))) uint8_t s_stg[4 * F8_STG_BYTES];
     __shared__ uint32_t s_row_top[EPI == F8_STORE_GLU ? 4 * 32 * BR : 1];
@@ -607,97 +626,119 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     const int slot = (G % 8 == 0) ? (b & 7) * (G >> 3) + (b >> 3) : b;
     const uint32_t ring = lds_addr(s_ring);
 
-    // what the copies of one tile read
-    const uint8_t* t_base = nullptr;   // its first row
-    const uint8_t* s_base = nullptr;   // that row's scales
-    const uint8_t* w_base = nullptr;   // its expert's matrix
-    const uint8_t* ws_base[2];         // the scales of this wave's columns (F8_STORE_GLU: of gate and up)
+    // A tile: its expert's rows [row0, row0 + rows), its columns from col0 on, and the scales of this wave's columns
+    // (F8_STORE_GLU: of gate and up).
+    struct Tile {
+        int row0, rows, col0;
+        const uint8_t* ws[WS];
+    } next;
+    // The copies' cursor: what a stage's copies of `next` read, moved on a stage at a time.
+    const uint8_t *t_ptr = nullptr, *w_ptr = nullptr, *s_ptr = nullptr;   // first row, its expert's matrix, first row's scales
     uint32_t t_voff[BR], s_voff;       // this lane's chunks of rows 16 BR wave + 16 i .., its scale
-    int wb[BC];                        // the 32-column block of each 1 KiB piece that this wave copies
+    uint32_t w_voff[BC / 2];           // its part of each 32-column block that this wave copies
+    uint32_t wd_first[WS];             // the weights' scales of the first four blocks
+    int c_at = 0;                      // the stage
     const int64_t t_block = static_cast<int64_t>(p.M) * F8_STAGE;   // bytes of 64 columns of all rows
     const int64_t s_block = static_cast<int64_t>(p.M) * 4;          // and of four blocks' scales
-    int e = 0, row0 = 0, rows = 0, col0 = 0;
     auto setup = [&](int t) {
-        e = uni(find_expert_wave(s_pre, p.E, t));
+        const int e = uni(find_expert_wave(s_pre, p.E, t));
         const int local = t - uni(s_pre[e]);
         const int lo = uni(s_off[e]), m = f8_tile_rows(uni(s_off[e + 1]) - lo, TR, p.group);
         const int tiles_m = (m + TR - 1) / TR;
         const int tm = local % tiles_m, tn = local / tiles_m;
-        row0 = lo + tm * TR;
-        rows = min(TR, m - tm * TR);
-        col0 = tn * OC;
-        t_base = p.q + static_cast<int64_t>(row0) * F8_STAGE;
-        s_base = p.s + static_cast<int64_t>(row0) * 4;
-        w_base = p.w + static_cast<int64_t>(e) * p.w_stride;
+        next.row0 = lo + tm * TR;
+        next.rows = min(TR, m - tm * TR);
+        next.col0 = tn * OC;
+        t_ptr = p.q + static_cast<int64_t>(next.row0) * F8_STAGE;
+        s_ptr = p.s + static_cast<int64_t>(next.row0) * 4;
+        w_ptr = p.w + static_cast<int64_t>(e) * p.w_stride;
         const uint8_t* ws = p.ws + static_cast<int64_t>(e) * p.ws_stride;
-        const int rb = col0 / F8_BLOCK + (EPI != F8_STORE_GLU && BC == 4 ? wc : 0);
-        ws_base[0] = ws + static_cast<int64_t>(min(rb, p.n.blocks() - 1)) * p.ws_ld;
-        ws_base[1] = EPI == F8_STORE_GLU ? ws_base[0] + static_cast<int64_t>(part_p / F8_BLOCK) * p.ws_ld : ws_base[0];
+        const int rb = next.col0 / F8_BLOCK + (EPI != F8_STORE_GLU && BC == 4 ? wc : 0);
+        next.ws[0] = ws + static_cast<int64_t>(min(rb, p.n.blocks() - 1)) * p.ws_ld;
+        if constexpr (WS == 2) next.ws[1] = next.ws[0] + static_cast<int64_t>(part_p / F8_BLOCK) * p.ws_ld;
+#pragma unroll
+        for (int c = 0; c < WS; ++c) wd_first[c] = scalar_load(next.ws[c]);
 #pragma unroll
         for (int i = 0; i < BR; ++i) {
             const int r = 16 * BR * wave + 16 * i + (lane >> 2);
             const int c = (lane & 3) ^ ((r >> 2) & 3);
-            t_voff[i] = static_cast<uint32_t>(min(r, rows - 1)) * F8_STAGE + 16 * c;
+            t_voff[i] = static_cast<uint32_t>(min(r, next.rows - 1)) * F8_STAGE + 16 * c;
         }
-        s_voff = static_cast<uint32_t>(min((64 * wave + lane) & (TR - 1), rows - 1)) * 4;
+        s_voff = static_cast<uint32_t>(min((64 * wave + lane) & (TR - 1), next.rows - 1)) * 4;
 #pragma unroll
-        for (int i = 0; i < BC; ++i) {
-            const int at = (wave * BC + i) >> 1;          // the block's place in the tile
+        for (int i = 0; i < BC / 2; ++i) {
+            const int at = wave * (BC / 2) + i;           // the block's place in the tile
+            int wb;
             if constexpr (EPI == F8_STORE_GLU)            // each wave column: two gate blocks, then two of up
-                wb[i] = ((at & 3) >> 1) * (part_p / 32) + col0 / 32 + 2 * (at >> 2) + (at & 1);
+                wb = ((at & 3) >> 1) * (part_p / 32) + next.col0 / 32 + 2 * (at >> 2) + (at & 1);
             else
-                wb[i] = min(col0 / 32 + at, width / 32 - 1);
+                wb = min(next.col0 / 32 + at, width / 32 - 1);
+            w_voff[i] = static_cast<uint32_t>(wb) * static_cast<uint32_t>(nstages * 2048) + lane * 16;    // below 2^31
+        }
+        c_at = 0;
+    };
+    // One of the P copies of the cursor's stage that this wave issues, to the slot at LDS offset `slot_at`.
+    auto piece = [&](uint32_t slot_at, auto i_tag) {
+        constexpr int i = decltype(i_tag)::value;
+        const uint32_t dst = ring + slot_at;
+        if constexpr (i < BR) {
+            dma16(t_ptr, t_voff[i], dst + (16 * BR * wave + 16 * i) * F8_STAGE);
+        } else if constexpr (i < BR + BC) {
+            constexpr int j = (i - BR) / 2, h = (i - BR) % 2;
+            dma16_at<1024 * h>(w_ptr, w_voff[j], dst + W_AT + (wave * (BC / 2) + j) * 2048);
+        } else {
+            dma4(s_ptr, s_voff, dst + S_AT + ((64 * wave) & (TR - 1)) * 4);
         }
     };
-    // One of the P copies of a stage that this wave issues (nothing past the last stage).
-    auto piece = [&](int st, auto i_tag) {
-        constexpr int i = decltype(i_tag)::value;
-        if (st >= nstages) return;
-        const uint32_t dst = ring + (st & (SLOTS - 1)) * SLOT_BYTES;
-        if constexpr (i < BR) {
-            dma16(t_base + st * t_block, t_voff[i], dst + (16 * BR * wave + 16 * i) * F8_STAGE);
-        } else if constexpr (i < BR + BC) {
-            constexpr int j = i - BR;
-            const int g = wave * BC + j;
-            dma16(w_base + (static_cast<int64_t>(wb[j]) * nsteps + st) * 2048 + (g & 1) * 1024, lane * 16, dst + W_AT + g * 1024);
-        } else {
-            dma4(s_base + (st >> 3) * s_block, s_voff, dst + S_AT + ((64 * wave) & (TR - 1)) * 4);
+    // A tile has two stages more than the ring at least (of a shorter sum, the last ones are copied but not multiplied),
+    // so that the cursor, a ring ahead, is never more than a tile ahead.
+    const int nst = max(nstages, SLOTS + 2);
+    int t = slot;
+    // Behind a stage's copies: the cursor moves to the next stage, of the next tile after a tile's last (of the same
+    // one again where there is none: those copies are not used).
+    auto advance = [&]() {
+        ++c_at;
+        if (c_at < nstages) {
+            t_ptr += t_block;
+            w_ptr += 2048;
+            if ((c_at & 7) == 0) s_ptr += s_block;
         }
+        if (c_at == nst) setup(t + G < n_tiles ? t + G : t);
     };
 
     f32x16 acc[BR][BC];    // [row block][column block]
     i32x8 tf[2][BR], wf[2][BC];
-    int ts[BR], ts_next[BR], wsc[2];        // scales of the block that is multiplied, and of the next
-    uint32_t wd[2], wd_next[2];             // the weights' scales, four blocks in a dword
-    auto read_t = [&](int st, auto u_tag) {
+    int ts[BR], ts_next[BR], wsc[WS];       // scales of the block that is multiplied, and of the next
+    uint32_t wd[WS], wd_next[WS];           // the weights' scales, four blocks in a dword
+    // a lane's first 16 bytes of a fragment in a slot; its second are 16 bytes off in the swizzled rows
+    const uint32_t t_at = (32 * BR * wr + (lane & 31)) * F8_STAGE + 16 * ((2 * (lane >> 5)) ^ ((lane >> 2) & 3));
+    const uint32_t w_at = W_AT + BC * wc * 2048 + lane * 16, s_at = S_AT + (32 * BR * wr + (lane & 31)) * 4;
+    // the fragments of the slot at sl, of the parity u; kb: the stage's block of the summed dimension
+    auto read_t = [&](uint32_t sl, int kb, auto u_tag) {
         constexpr int u = decltype(u_tag)::value;
-        const uint8_t* sl = s_ring + (st & (SLOTS - 1)) * SLOT_BYTES;
-        const int c = (2 * (lane >> 5)) ^ ((lane >> 2) & 3);
+        const uint8_t *r0 = s_ring + (sl + t_at), *r1 = s_ring + (sl + (t_at ^ 16));
 #pragma unroll
-        for (int i = 0; i < BR; ++i) {
-            const uint8_t* r = sl + (32 * BR * wr + 32 * i + (lane & 31)) * F8_STAGE;
-            tf[u][i] = f8_join(*reinterpret_cast<const i32x4*>(r + 16 * c), *reinterpret_cast<const i32x4*>(r + 16 * (c ^ 1)));
-        }
+        for (int i = 0; i < BR; ++i)
+            tf[u][i] = f8_join(*reinterpret_cast<const i32x4*>(r0 + i * 32 * F8_STAGE), *reinterpret_cast<const i32x4*>(r1 + i * 32 * F8_STAGE));
         if constexpr (u == 0) {     // the first of a block's two stages
+            const uint8_t* sc = s_ring + (sl + s_at + (kb & 3));
 #pragma unroll
-            for (int i = 0; i < BR; ++i) ts_next[i] = sl[S_AT + (32 * BR * wr + 32 * i + (lane & 31)) * 4 + ((st >> 1) & 3)];
+            for (int i = 0; i < BR; ++i) ts_next[i] = sc[i * 128];
         }
     };
-    auto read_w = [&](int st, auto u_tag) {
+    auto read_w = [&](uint32_t sl, auto u_tag) {
         constexpr int u = decltype(u_tag)::value;
-        const uint8_t* sl = s_ring + (st & (SLOTS - 1)) * SLOT_BYTES + W_AT;
+        const uint8_t* f = s_ring + (sl + w_at);
 #pragma unroll
-        for (int j = 0; j < BC; ++j) {
-            const uint8_t* f = sl + (BC * wc + j) * 2048 + lane * 16;
-            wf[u][j] = f8_join(*reinterpret_cast<const i32x4*>(f), *reinterpret_cast<const i32x4*>(f + 1024));
-        }
+        for (int j = 0; j < BC; ++j)
+            wf[u][j] = f8_join(*reinterpret_cast<const i32x4*>(f + j * 2048), *reinterpret_cast<const i32x4*>(f + j * 2048 + 1024));
     };
     // the BC matrix instructions of row block i; the tile's first step starts its sums from zero
     auto mma = [&](auto u_tag, auto i_tag, auto first_tag) {
         constexpr int u = decltype(u_tag)::value, i = decltype(i_tag)::value;
 #pragma unroll
         for (int j = 0; j < BC; ++j) {
-            const int s = EPI == F8_STORE_GLU ? wsc[j >= BC / 2] : wsc[0];
+            const int s = wsc[WS == 2 && j >= BC / 2];
             if constexpr (decltype(first_tag)::value != 0)
                 acc[i][j] = f8_mma(wf[u][j], tf[u][i], f32x16{}, s, ts[i]);
             else
@@ -705,98 +746,96 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
         }
     };
     auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
-    // Waits until at most n copies and stores issued after those of the stage that is needed are outstanding.
-    auto wait_after = [&](int n) {
-        if (n >= 60) wait_vmcnt<60>();
-        else if (n >= 52) wait_vmcnt<52>();
-        else if (n >= 44) wait_vmcnt<44>();
-        else if (n >= 36) wait_vmcnt<36>();
-        else if (n >= 27) wait_vmcnt<27>();
-        else if (n >= 21) wait_vmcnt<21>();
-        else if (n >= 18) wait_vmcnt<18>();
-        else if (n >= 14) wait_vmcnt<14>();
-        else if (n >= 9) wait_vmcnt<9>();
-        else if (n >= 7) wait_vmcnt<7>();
-        else if (n >= 5) wait_vmcnt<5>();
-        else wait_vmcnt<0>();
+    // Waits until at most the copies of n stages and `behind` stores are outstanding.
+    constexpr int AHEAD = P * (SLOTS - 2);
+    constexpr int S1 = EPI == F8_STORE ? 2 * BR * BC : (EPI == F8_STORE_GLU ? 2 * BR : 8 * BR);   // of a full tile
+    constexpr int S2 = S1 + (EPI == F8_STORE_GLU ? 8 * BR : 0);                                   // with H1
+    constexpr int MOST = 63;
+    auto wait_ahead = [&](int behind) {
+        if (behind == 0) wait_vmcnt<AHEAD>();
+        else if (S2 == S1 || behind == S1) wait_vmcnt<(AHEAD + S1 < MOST ? AHEAD + S1 : MOST)>();
+        else wait_vmcnt<(AHEAD + S2 < MOST ? AHEAD + S2 : MOST)>();
     };
-    // Stage st, of the parity u.  behind: the stores issued behind the copies of the prologue's stages, at least.
-    auto stage = [&](int st, int behind, auto u_tag, auto first_tag, auto last_tag) {
+    // Stage st of the tile, of the parity u, in the slot at cur.  behind: the stores issued behind the copies of the
+    // ring's other stages.  After the tile's last stage the next fragments belong to another tile; they are read again
+    // after the epilogue.
+    uint32_t cur = 0;
+    const uint8_t* cur_ws[WS];
+    auto stage = [&](int st, int behind, auto u_tag, auto first_tag) {
         constexpr int u = decltype(u_tag)::value;
-        constexpr bool LAST = decltype(last_tag)::value != 0;
         if constexpr (u == 0) {
             const int k = st >> 1;
 #pragma unroll
             for (int i = 0; i < BR; ++i) ts[i] = ts_next[i];
             if ((k & 3) == 0) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < WS; ++c) {
                     wd[c] = wd_next[c];
-                    wd_next[c] = scalar_load(ws_base[c] + min(k + 4, p.ws_ld - 4));
+                    wd_next[c] = scalar_load(cur_ws[c] + min(k + 4, p.ws_ld - 4));
                 }
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) wsc[c] = static_cast<int>(wd[c] >> (8 * (k & 3)));
+            for (int c = 0; c < WS; ++c) wsc[c] = static_cast<int>(wd[c] >> (8 * (k & 3)));
         }
         mma(u_tag, GrpTag<0>{}, first_tag);
         fence();
-        if constexpr (!LAST) {
-            // stage st + 1 has landed, and every wave holds its fragments of stage st, whose slot is refilled from here on
-            if (st >= SLOTS - 1 && st + SLOTS <= nstages) wait_vmcnt<P*(SLOTS - 2)>();
-            else wait_after(P * min(nstages - 2 - st, SLOTS - 2) + (st < SLOTS - 1 ? behind : 0));
-            block_barrier();
-        }
+        // stage st + 1 has landed, and every wave holds its fragments of stage st, whose slot is refilled from here on
+        wait_ahead(behind);
+        block_barrier();
+        const uint32_t refill = cur;
+        cur = cur + SLOT_BYTES == SLOTS * SLOT_BYTES ? 0 : cur + SLOT_BYTES;
         static_for<BR - 1>([&](auto it) {
             constexpr int i = decltype(it)::value;
-            if constexpr (!LAST) {
-                if constexpr (i == 0) read_w(st + 1, GrpTag<u ^ 1>{});
-                if constexpr (i == (BR > 2 ? 1 : 0)) read_t(st + 1, GrpTag<u ^ 1>{});
-            }
+            if constexpr (i == 0) read_w(cur, GrpTag<u ^ 1>{});
+            if constexpr (i == (BR > 2 ? 1 : 0)) read_t(cur, (st + 1) >> 1, GrpTag<u ^ 1>{});
             mma(u_tag, GrpTag<i + 1>{}, first_tag);
-            if constexpr (!LAST) {
-                constexpr int a = i * P / (BR - 1), z = (i + 1) * P / (BR - 1);
-                static_for<z - a>([&](auto j) { piece(st + SLOTS, GrpTag<a + decltype(j)::value>{}); });
-            }
+            constexpr int a = i * P / (BR - 1), z = (i + 1) * P / (BR - 1);
+            static_for<z - a>([&](auto j) { piece(refill, GrpTag<a + decltype(j)::value>{}); });
             fence();
         });
-    };
-    // the copies before a tile's first stage: the whole ring's
-    auto prologue = [&]() {
-        for (int st = 0; st < SLOTS; ++st) static_for<P>([&](auto i) { piece(st, i); });
+        advance();
     };
 
-    int t = slot, stores = 0;
+    // a stage without products
+    auto idle = [&](int behind) {
+        wait_ahead(behind);
+        block_barrier();
+        const uint32_t refill = cur;
+        cur = cur + SLOT_BYTES == SLOTS * SLOT_BYTES ? 0 : cur + SLOT_BYTES;
+        static_for<P>([&](auto j) { piece(refill, j); });
+        advance();
+    };
+
+    int stores = 0;
+    Tile tile;
     if (t < n_tiles) {
         setup(t);
-        prologue();
+        tile = next;
+#pragma unroll
+        for (int c = 0; c < WS; ++c) wd_next[c] = wd_first[c];
+#pragma unroll 1
+        for (uint32_t at = 0; at < SLOTS * SLOT_BYTES; at += SLOT_BYTES) {
+            static_for<P>([&](auto j) { piece(at, j); });
+            advance();
+        }
+        wait_vmcnt<P*(SLOTS - 1)>();
+        block_barrier();
     }
     while (t < n_tiles) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) wd_next[c] = scalar_load(ws_base[c]);
-        wait_after(P * min(nstages - 1, SLOTS - 1) + stores);        // stage 0
-        block_barrier();
-        read_w(0, GrpTag<0>{});
-        read_t(0, GrpTag<0>{});
-        // an even number of stages, at least two
-        if (nstages == 2) {
-            stage(0, stores, GrpTag<0>{}, GrpTag<1>{}, GrpTag<0>{});
-        } else {
-            stage(0, stores, GrpTag<0>{}, GrpTag<1>{}, GrpTag<0>{});
-            stage(1, stores, GrpTag<1>{}, GrpTag<0>{}, GrpTag<0>{});
-            for (int st = 2; st < nstages - 2; st += 2) {
-                stage(st, stores, GrpTag<0>{}, GrpTag<0>{}, GrpTag<0>{});
-                stage(st + 1, stores, GrpTag<1>{}, GrpTag<0>{}, GrpTag<0>{});
-            }
-            stage(nstages - 2, stores, GrpTag<0>{}, GrpTag<0>{}, GrpTag<0>{});
+        for (int c = 0; c < WS; ++c) cur_ws[c] = tile.ws[c];
+        read_w(cur, GrpTag<0>{});
+        read_t(cur, 0, GrpTag<0>{});
+        stage(0, stores, GrpTag<0>{}, GrpTag<1>{});     // an even number of stages, at least two
+        stage(1, stores, GrpTag<1>{}, GrpTag<0>{});
+#pragma unroll 1
+        for (int st = 2; st < nstages; st += 2) {
+            stage(st, st < SLOTS - 1 ? stores : 0, GrpTag<0>{}, GrpTag<0>{});
+            stage(st + 1, st + 1 < SLOTS - 1 ? stores : 0, GrpTag<1>{}, GrpTag<0>{});
         }
-        stage(nstages - 1, stores, GrpTag<1>{}, GrpTag<0>{}, GrpTag<1>{});
-        const int prow0 = row0, prows = rows, pcol0 = col0;
-        t += G;
-        block_barrier();         // every wave is done with the ring
-        if (t < n_tiles) {
-            setup(t);
-            prologue();
-        }
+#pragma unroll 1
+        for (int st = nstages; st < nst; ++st) idle(st < SLOTS - 1 ? stores : 0);
+        const int prow0 = tile.row0, prows = tile.rows, pcol0 = tile.col0;
         mfma_drain();
         int opaque = 0;
         asm volatile("" : "+s"(opaque));
@@ -835,10 +874,10 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
             }
         };
         // a block's rows to columns col .. of `to` (row stride ld), of which those below `cols` exist
-        auto store = [&](const uint4 (&o)[4], uint16_t* to, int64_t ld, int i, int cols, bool full) {
+        auto store = [&](const uint4 (&o)[4], uint16_t* to, int64_t ld, int i, int cols, auto full_tag) {
             const int gr = 32 * BR * wr + 32 * i + (ln >> 3);
             uint16_t* at = to + static_cast<int64_t>(prow0 + gr) * ld + chunk;
-            if (full) {
+            if constexpr (decltype(full_tag)::value != 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) st16_nt(at + static_cast<int64_t>(8 * k) * ld, o[k]);
             } else {
@@ -850,7 +889,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
         // 32 rows x 64 8-bit columns, of which lane has row ln & 31 and the dwords d[c] of columns 8 c + 4 (ln >> 5),
         // through half of the staging area ([32 rows][64 bytes], chunk c of row r at c ^ ((r >> 2) & 3)) to padded column col
         const int64_t qblock = static_cast<int64_t>(p.M) * 64;
-        auto store8 = [&](const uint32_t (&d)[8], int half, int i, int col, bool full) {
+        auto store8 = [&](const uint32_t (&d)[8], int half, int i, int col, auto full_tag) {
             uint8_t* st8 = reinterpret_cast<uint8_t*>(stg) + half * 2048;
             const int rr = ln & 31;
 #pragma unroll
@@ -860,142 +899,157 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
             for (int k = 0; k < 2; ++k) {
                 const int r = 16 * k + (ln >> 2), gr = 32 * BR * wr + 32 * i + r;
                 const uint4 v = *reinterpret_cast<const uint4*>(st8 + r * 64 + (((ln & 3) ^ ((r >> 2) & 3)) << 4));
-                if (full || gr < prows)
+                if (decltype(full_tag)::value != 0 || gr < prows)
                     *reinterpret_cast<uint4*>(p.q_out + (col >> 6) * qblock + static_cast<int64_t>(prow0 + gr) * 64 + 16 * (ln & 3)) = v;
             }
         };
-        auto store_scale = [&](const F8Scale& sc, int i, int kb) {     // lanes below 32
+        auto store_scale = [&](const F8Scale& sc, int i, int kb, auto full_tag) {     // lanes below 32
             const int gr = 32 * BR * wr + 32 * i + ln;
-            if (ln < 32 && gr < prows)
+            if (ln < 32 && (decltype(full_tag)::value != 0 || gr < prows))
                 p.s_out[(static_cast<int64_t>(kb >> 2) * p.M + prow0 + gr) * 4 + (kb & 3)] = static_cast<uint8_t>(sc.byte);
         };
         const bool all_rows = prows == TR;
         // All stores of a wave are issued where the tile is full; a store whose lanes all lie outside may be
         // skipped, so a partial tile counts as none.
-        if constexpr (EPI == F8_STORE) {
-            const bool full = all_rows && (p.n.parts == 1 || p.n.part == part_p) && pcol0 + TC <= p.n.real();
-            stores = full ? 2 * BR * BC : 0;
-            const int gc0 = pcol0 + 32 * BC * wc;
-            uint2 vals[8];
-            sums(GrpTag<0>{}, GrpTag<0>{}, vals);
-            put(vals);
-            static_for<BR * BC / 2>([&](auto b_tag) {
-                constexpr int blk = decltype(b_tag)::value, i = blk % BR, jh = blk / BR, nx = blk + 1;
-                if constexpr (nx < BR * BC / 2) sums(GrpTag<nx % BR>{}, GrpTag<nx / BR>{}, vals);
-                uint4 out[4];
-                rows_of(out);
-                if constexpr (nx < BR * BC / 2) put(vals);
-                const int c = gc0 + 64 * jh, h = c >= part_p, k = c - h * part_p;
-                store(out, p.out + h * p.n.part + k, p.n.real(), i, p.n.part - k, full);
-            });
-        } else if constexpr (EPI == F8_STORE_GLU) {
-            const int k0 = pcol0 + 64 * wc;          // the wave's 64 columns of gate, up and A
-            const bool full = all_rows && k0 + 64 <= p.n.part;
-            stores = all_rows ? 2 * BR + (p.out && pcol0 + OC <= p.n.part ? 8 * BR : 0) : 0;
-            uint32_t av[BR][16], top[BR];
-            static_for<BR>([&](auto i_tag) {
-                constexpr int i = decltype(i_tag)::value;
-                uint2 g[8], u[8];
-                sums(i_tag, GrpTag<0>{}, g);
-                sums(i_tag, GrpTag<1>{}, u);
-                top[i] = 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), p.slope), f8_act(hi_f(g[c].x), hi_f(u[c].x), p.slope));
-                    av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), p.slope), f8_act(hi_f(g[c].y), hi_f(u[c].y), p.slope));
-                    top[i] = max(top[i], max(f8_top2(av[i][2 * c]), f8_top2(av[i][2 * c + 1])));
-                }
-                top[i] = max_other_half(top[i]);
-                if (ln < 32) s_row_top[wave * 32 * BR + 32 * i + ln] = top[i];
-                if (p.out) {
-                    uint4 o[4];
-                    put(g);
-                    rows_of(o);
-                    put(u);
-                    store(o, p.out + k0, p.n.real(), i, p.n.part - k0, full);
-                    rows_of(o);
-                    store(o, p.out + p.n.part + k0, p.n.real(), i, p.n.part - k0, full);
-                }
-            });
-            block_barrier();
-#pragma unroll
-            for (int i = 0; i < BR; ++i) {
-                const F8Scale sc = f8_scale(max(top[i], s_row_top[(wave ^ 1) * 32 * BR + 32 * i + (ln & 31)]));
-                uint32_t d[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    d[c] = f8_four(lo_f(av[i][2 * c]), hi_f(av[i][2 * c]), lo_f(av[i][2 * c + 1]), hi_f(av[i][2 * c + 1]), sc);
-                store8(d, i & 1, i, k0, all_rows);
-                if (wc == 0) store_scale(sc, i, pcol0 / F8_BLOCK);
-            }
-        } else {
-            const int k0 = pcol0 + F8_BLOCK * wc, kb = k0 / F8_BLOCK;     // the wave's block of dA
-            stores = all_rows && k0 < part_p ? 8 * BR : 0;
-            if (k0 < part_p) {
-                // the rows of h1, gate and up, of block (i, 64 columns jh)
-                uint4 hg[4], hu[4];
-                auto load_h1 = [&](int i, int jh) {
-                    const int c = k0 + 64 * jh + chunk;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int gr = min(32 * BR * wr + 32 * i + 8 * k + (ln >> 3), prows - 1);
-                        const uint16_t* h = p.h1 + static_cast<int64_t>(prow0 + gr) * 2 * p.n.part + c;
-                        const uint4 zero = make_uint4(0, 0, 0, 0);
-                        hg[k] = c < p.n.part ? ld16_nt(h) : zero;
-                        hu[k] = c < p.n.part ? ld16_nt(h + p.n.part) : zero;
-                    }
-                };
-                auto put_rows = [&](const uint4 (&o)[4]) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(stg + (8 * k + (ln >> 3)) * 64 + (ln & 7) * 8) = o[k];
-                };
-                load_h1(0, 0);
+        bool full = all_rows;
+        if constexpr (EPI == F8_STORE) full &= (p.n.parts == 1 || p.n.part == part_p) && pcol0 + TC <= p.n.real();
+        if constexpr (EPI == F8_STORE_GLU) full &= pcol0 + OC <= p.n.part;
+        if constexpr (EPI == F8_STORE_DGLU) full &= pcol0 + OC <= part_p;
+        stores = full ? (EPI == F8_STORE_GLU && p.out ? S2 : S1) : 0;
+        auto epilogue = [&](auto full_tag) {
+            if constexpr (EPI == F8_STORE) {
+                const int gc0 = pcol0 + 32 * BC * wc;
+                uint2 vals[8];
+                sums(GrpTag<0>{}, GrpTag<0>{}, vals);
+                put(vals);
+                static_for<BR * BC / 2>([&](auto b_tag) {
+                    constexpr int blk = decltype(b_tag)::value, i = blk % BR, jh = blk / BR, nx = blk + 1;
+                    if constexpr (nx < BR * BC / 2) sums(GrpTag<nx % BR>{}, GrpTag<nx / BR>{}, vals);
+                    uint4 out[4];
+                    rows_of(out);
+                    if constexpr (nx < BR * BC / 2) put(vals);
+                    const int c = gc0 + 64 * jh, h = p.n.parts == 2 && c >= part_p, k = c - h * part_p;
+                    store(out, p.out + h * p.n.part + k, p.n.real(), i, p.n.part - k, full_tag);
+                });
+            } else if constexpr (EPI == F8_STORE_GLU) {
+                const int k0 = pcol0 + 64 * wc;          // the wave's 64 columns of gate, up and A
+                uint32_t av[BR][16], top[BR];
                 static_for<BR>([&](auto i_tag) {
                     constexpr int i = decltype(i_tag)::value;
-                    uint32_t v[2][2][16], top[2] = {0, 0};      // [gate, up][64 columns]
-                    static_for<2>([&](auto jh_tag) {
-                        constexpr int jh = decltype(jh_tag)::value;
-                        uint2 d[8], g[8], u[8];
-                        put_rows(hg);
-                        take(g);
-                        put_rows(hu);
-                        take(u);
-                        if constexpr (2 * i + jh + 1 < 2 * BR) load_h1((2 * i + jh + 1) / 2, (jh + 1) % 2);
-                        sums(i_tag, jh_tag, d);
+                    uint2 g[8], u[8];
+                    sums(i_tag, GrpTag<0>{}, g);
+                    sums(i_tag, GrpTag<1>{}, u);
+                    top[i] = 0;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t dd = y ? d[c].y : d[c].x, gg = y ? g[c].y : g[c].x, uu = y ? u[c].y : u[c].x;
-                                float g0, u0, g1, u1;
-                                f8_act_grad(lo_f(gg), lo_f(uu), lo_f(dd), p.slope, g0, u0);
-                                f8_act_grad(hi_f(gg), hi_f(uu), hi_f(dd), p.slope, g1, u1);
-                                v[0][jh][2 * c + y] = pack2(g0, g1);
-                                v[1][jh][2 * c + y] = pack2(u0, u1);
-                                top[0] = max(top[0], f8_top2(v[0][jh][2 * c + y]));
-                                top[1] = max(top[1], f8_top2(v[1][jh][2 * c + y]));
-                            }
-                    });
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const F8Scale sc = f8_scale(max_other_half(top[h]));
-#pragma unroll
-                        for (int jh = 0; jh < 2; ++jh) {
-                            uint32_t d[8];
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const uint32_t x = v[h][jh][2 * c], y = v[h][jh][2 * c + 1];
-                                d[c] = f8_four(lo_f(x), hi_f(x), lo_f(y), hi_f(y), sc);
-                            }
-                            store8(d, jh, i, h * part_p + k0 + 64 * jh, all_rows);
-                        }
-                        store_scale(sc, i, kb + h * (part_p / F8_BLOCK));
+                    for (int c = 0; c < 8; ++c) {
+                        av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), p.slope), f8_act(hi_f(g[c].x), hi_f(u[c].x), p.slope));
+                        av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), p.slope), f8_act(hi_f(g[c].y), hi_f(u[c].y), p.slope));
+                        top[i] = max(top[i], max(f8_top2(av[i][2 * c]), f8_top2(av[i][2 * c + 1])));
+                    }
+                    top[i] = max_other_half(top[i]);
+                    if (ln < 32) s_row_top[wave * 32 * BR + 32 * i + ln] = top[i];
+                    if (p.out) {
+                        uint4 o[4];
+                        put(g);
+                        rows_of(o);
+                        put(u);
+                        store(o, p.out + k0, p.n.real(), i, p.n.part - k0, full_tag);
+                        rows_of(o);
+                        store(o, p.out + p.n.part + k0, p.n.real(), i, p.n.part - k0, full_tag);
                     }
                 });
+                block_barrier();
+#pragma unroll
+                for (int i = 0; i < BR; ++i) {
+                    const F8Scale sc = f8_scale(max(top[i], s_row_top[(wave ^ 1) * 32 * BR + 32 * i + (ln & 31)]));
+                    uint32_t d[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        d[c] = f8_four(lo_f(av[i][2 * c]), hi_f(av[i][2 * c]), lo_f(av[i][2 * c + 1]), hi_f(av[i][2 * c + 1]), sc);
+                    store8(d, i & 1, i, k0, full_tag);
+                    if (wc == 0) store_scale(sc, i, pcol0 / F8_BLOCK, full_tag);
+                }
+            } else {
+                const int k0 = pcol0 + F8_BLOCK * wc, kb = k0 / F8_BLOCK;     // the wave's block of dA
+                if (k0 < part_p) {
+                    // the rows of h1, gate and up, of block (i, 64 columns jh)
+                    uint4 hg[4], hu[4];
+                    auto load_h1 = [&](int i, int jh) {
+                        // rows that exist, from a uniform one on (32-bit offsets: 32 rows of 4 part bytes)
+                        const int r0 = min(32 * BR * wr + 32 * i, prows - 1), last = prows - 1 - r0;
+                        const int c = min(k0 + 64 * jh + chunk, p.n.part - 8);     // past the end: values that meet dA = 0
+                        const uint16_t* gate = uni_ptr(p.h1 + static_cast<int64_t>(prow0 + r0) * 2 * p.n.part);
+                        const uint16_t* up = uni_ptr(gate + p.n.part);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t at = static_cast<uint32_t>(min(8 * k + (ln >> 3), last)) * (2 * p.n.part) + c;
+                            hg[k] = ld16_nt(gate + at);
+                            hu[k] = ld16_nt(up + at);
+                        }
+                    };
+                    auto put_rows = [&](const uint4 (&o)[4]) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(stg + (8 * k + (ln >> 3)) * 64 + (ln & 7) * 8) = o[k];
+                    };
+                    load_h1(0, 0);
+                    static_for<BR>([&](auto i_tag) {
+                        constexpr int i = decltype(i_tag)::value;
+                        float v[2][2][16];      // [gate, up][64 columns]: pairs, kept where the block's sums were
+                        uint32_t top[2] = {0, 0};
+                        static_for<2>([&](auto jh_tag) {
+                            constexpr int jh = decltype(jh_tag)::value;
+                            uint2 d[8], g[8], u[8];
+                            put_rows(hg);
+                            take(g);
+                            put_rows(hu);
+                            take(u);
+                            if constexpr (2 * i + jh + 1 < 2 * BR) load_h1((2 * i + jh + 1) / 2, (jh + 1) % 2);
+                            sums(i_tag, jh_tag, d);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const uint32_t dd = y ? d[c].y : d[c].x, gg = y ? g[c].y : g[c].x, uu = y ? u[c].y : u[c].x;
+                                    float g0, u0, g1, u1;
+                                    f8_act_grad(lo_f(gg), lo_f(uu), lo_f(dd), p.slope, g0, u0);
+                                    f8_act_grad(hi_f(gg), hi_f(uu), hi_f(dd), p.slope, g1, u1);
+                                    const uint32_t pg = pack2(g0, g1), pu = pack2(u0, u1);
+                                    top[0] = max(top[0], f8_top2(pg));
+                                    top[1] = max(top[1], f8_top2(pu));
+                                    v[0][jh][2 * c + y] = acc_wr(pg);
+                                    v[1][jh][2 * c + y] = acc_wr(pu);
+                                }
+                            fence();
+                        });
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const F8Scale sc = f8_scale(max_other_half(top[h]));
+#pragma unroll
+                            for (int jh = 0; jh < 2; ++jh) {
+                                uint32_t d[8];
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint32_t x = acc_rd_u(v[h][jh][2 * c]), y = acc_rd_u(v[h][jh][2 * c + 1]);
+                                    d[c] = f8_four(lo_f(x), hi_f(x), lo_f(y), hi_f(y), sc);
+                                }
+                                store8(d, jh, i, h * part_p + k0 + 64 * jh, full_tag);
+                            }
+                            store_scale(sc, i, kb + h * (part_p / F8_BLOCK), full_tag);
+                            fence();
+                        }
+                    });
+                }
             }
-        }
+        };
+        if (full) epilogue(GrpTag<1>{});
+        else epilogue(GrpTag<0>{});
+        t += G;
+        tile = next;
+#pragma unroll
+        for (int c = 0; c < WS; ++c) wd_next[c] = wd_first[c];
     }
     if (p.group == 0) return;
+    wait_vmcnt<0>();     // the last copies
     __syncthreads();
     f8_stream_list<EPI>(p, s_off, s_pre, s_ring, reinterpret_cast<uint32_t(*)[4][F8_GROUP]>(s_stg));
 }
