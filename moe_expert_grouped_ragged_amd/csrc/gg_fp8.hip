@@ -607,6 +607,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     constexpr int SLOT_BYTES = S_AT + TR * 4, SLOTS = BR == 4 ? 4 : (BC == 4 ? 4 : 8);
     static_assert(SLOTS * SLOT_BYTES <= F8_RING, "the ring");
     constexpr int P = BR + BC + 1;                          // copies a wave issues for a stage
+    constexpr int READS_A_STEP = BR == 4 ? 1 : 2;           // fragments read behind a matrix instruction
     constexpr int WS = EPI == F8_STORE_GLU ? 2 : 1;         // blocks of weights that a wave's columns lie in
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[F8_RING];
     __shared__ __attribute__((aligned(16))) uint8_t s_stg[4 * F8_STG_BYTES];
@@ -713,37 +714,39 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     // a lane's first 16 bytes of a fragment in a slot; its second are 16 bytes off in the swizzled rows
     const uint32_t t_at = (32 * BR * wr + (lane & 31)) * F8_STAGE + 16 * ((2 * (lane >> 5)) ^ ((lane >> 2) & 3));
     const uint32_t w_at = W_AT + BC * wc * 2048 + lane * 16, s_at = S_AT + (32 * BR * wr + (lane & 31)) * 4;
-    // the fragments of the slot at sl, of the parity u; kb: the stage's block of the summed dimension
-    auto read_t = [&](uint32_t sl, int kb, auto u_tag) {
-        constexpr int u = decltype(u_tag)::value;
-        const uint8_t *r0 = s_ring + (sl + t_at), *r1 = s_ring + (sl + (t_at ^ 16));
-#pragma unroll
-        for (int i = 0; i < BR; ++i)
-            tf[u][i] = f8_join(*reinterpret_cast<const i32x4*>(r0 + i * 32 * F8_STAGE), *reinterpret_cast<const i32x4*>(r1 + i * 32 * F8_STAGE));
-        if constexpr (u == 0) {     // the first of a block's two stages
-            const uint8_t* sc = s_ring + (sl + s_at + (kb & 3));
-#pragma unroll
-            for (int i = 0; i < BR; ++i) ts_next[i] = sc[i * 128];
-        }
-    };
-    auto read_w = [&](uint32_t sl, auto u_tag) {
-        constexpr int u = decltype(u_tag)::value;
-        const uint8_t* f = s_ring + (sl + w_at);
-#pragma unroll
-        for (int j = 0; j < BC; ++j)
-            wf[u][j] = f8_join(*reinterpret_cast<const i32x4*>(f + j * 2048), *reinterpret_cast<const i32x4*>(f + j * 2048 + 1024));
-    };
-    // the BC matrix instructions of row block i; the tile's first step starts its sums from zero
-    auto mma = [&](auto u_tag, auto i_tag, auto first_tag) {
+    // fragment i of the slot at sl, of the parity u
+    auto read_t = [&](uint32_t sl, auto i_tag, auto u_tag) {
         constexpr int u = decltype(u_tag)::value, i = decltype(i_tag)::value;
+        tf[u][i] = f8_join(*reinterpret_cast<const i32x4*>(s_ring + (sl + t_at) + i * 32 * F8_STAGE),
+                           *reinterpret_cast<const i32x4*>(s_ring + (sl + (t_at ^ 16)) + i * 32 * F8_STAGE));
+    };
+    auto read_w = [&](uint32_t sl, auto j_tag, auto u_tag) {
+        constexpr int u = decltype(u_tag)::value, j = decltype(j_tag)::value;
+        const uint8_t* f = s_ring + (sl + w_at) + j * 2048;
+        wf[u][j] = f8_join(*reinterpret_cast<const i32x4*>(f), *reinterpret_cast<const i32x4*>(f + 1024));
+    };
+    // the rows' scales of the stage's block kb, with the first of a block's two stages
+    auto read_s = [&](uint32_t sl, int kb) {
+        const uint8_t* sc = s_ring + (sl + s_at + (kb & 3));
 #pragma unroll
-        for (int j = 0; j < BC; ++j) {
-            const int s = wsc[WS == 2 && j >= BC / 2];
-            if constexpr (decltype(first_tag)::value != 0)
-                acc[i][j] = f8_mma(wf[u][j], tf[u][i], f32x16{}, s, ts[i]);
-            else
-                acc[i][j] = f8_mma(wf[u][j], tf[u][i], acc[i][j], s, ts[i]);
-        }
+        for (int i = 0; i < BR; ++i) ts_next[i] = sc[i * 128];
+    };
+    // Read f of a stage's BR + BC, in the order in which the next stage needs them.
+    auto read = [&](uint32_t sl, auto f_tag, auto u_tag) {
+        constexpr int f = decltype(f_tag)::value;
+        if constexpr (f == 0) read_t(sl, GrpTag<0>{}, u_tag);
+        else if constexpr (f <= BC) read_w(sl, GrpTag<f - 1>{}, u_tag);
+        else read_t(sl, GrpTag<f - BC>{}, u_tag);
+    };
+    // matrix instruction m of a stage, rows first; the tile's first stage starts its sums from zero
+    auto mma = [&](auto u_tag, auto m_tag, auto first_tag) {
+        constexpr int u = decltype(u_tag)::value, i = decltype(m_tag)::value / BC, j = decltype(m_tag)::value % BC;
+        const int s = wsc[WS == 2 && j >= BC / 2];
+        if constexpr (decltype(first_tag)::value != 0)
+            acc[i][j] = f8_mma(wf[u][j], tf[u][i], f32x16{}, s, ts[i]);
+        else
+            acc[i][j] = f8_mma(wf[u][j], tf[u][i], acc[i][j], s, ts[i]);
+        asm volatile("" : "+a"(acc[i][j]));     // in its place: the compiler sinks matrix instructions past branches
     };
     auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
     // Waits until at most the copies of n stages and `behind` stores are outstanding.
@@ -777,19 +780,22 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
 #pragma unroll
             for (int c = 0; c < WS; ++c) wsc[c] = static_cast<int>(wd[c] >> (8 * (k & 3)));
         }
-        mma(u_tag, GrpTag<0>{}, first_tag);
+        static_for<BC>([&](auto m) { mma(u_tag, m, first_tag); });
         fence();
         // stage st + 1 has landed, and every wave holds its fragments of stage st, whose slot is refilled from here on
         wait_ahead(behind);
         block_barrier();
         const uint32_t refill = cur;
         cur = cur + SLOT_BYTES == SLOTS * SLOT_BYTES ? 0 : cur + SLOT_BYTES;
-        static_for<BR - 1>([&](auto it) {
-            constexpr int i = decltype(it)::value;
-            if constexpr (i == 0) read_w(cur, GrpTag<u ^ 1>{});
-            if constexpr (i == (BR > 2 ? 1 : 0)) read_t(cur, (st + 1) >> 1, GrpTag<u ^ 1>{});
-            mma(u_tag, GrpTag<i + 1>{}, first_tag);
-            constexpr int a = i * P / (BR - 1), z = (i + 1) * P / (BR - 1);
+        // behind each of the other matrix instructions a fragment's reads and a copy, so that neither holds them up
+        constexpr int REST = BR * BC - BC, FR = BR + BC;
+        static_for<REST>([&](auto m_tag) {
+            constexpr int m = decltype(m_tag)::value;
+            mma(u_tag, GrpTag<m + BC>{}, first_tag);
+            if constexpr (u == 1 && m == 0) read_s(cur, (st + 1) >> 1);
+            constexpr int f0 = m * READS_A_STEP, f1 = (m + 1) * READS_A_STEP;
+            static_for<(f1 < FR ? f1 : FR) - (f0 < FR ? f0 : FR)>([&](auto f) { read(cur, GrpTag<f0 + decltype(f)::value>{}, GrpTag<u ^ 1>{}); });
+            constexpr int a = m * P / REST, z = (m + 1) * P / REST;
             static_for<z - a>([&](auto j) { piece(refill, GrpTag<a + decltype(j)::value>{}); });
             fence();
         });
@@ -824,8 +830,8 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     while (t < n_tiles) {
 #pragma unroll
         for (int c = 0; c < WS; ++c) cur_ws[c] = tile.ws[c];
-        read_w(cur, GrpTag<0>{});
-        read_t(cur, 0, GrpTag<0>{});
+        read_s(cur, 0);
+        static_for<BR + BC>([&](auto f) { read(cur, f, GrpTag<0>{}); });
         stage(0, stores, GrpTag<0>{}, GrpTag<1>{});     // an even number of stages, at least two
         stage(1, stores, GrpTag<1>{}, GrpTag<0>{});
 #pragma unroll 1
