@@ -59,109 +59,109 @@ __device__ __forceinline__ void f8_act_grad(float g, float u, float da, float sl
     du = da * g * sg;
 }
 
-// Half a wave takes 512 columns of a row, 16 a lane, so eight lanes are a block
-// and its maximum stays in registers; the two halves take neighbouring rows
-// from an even one on, so that a store covers whole 128-byte lines of the two
-// rows in the product's layout.  U such groups of columns are in flight at a
-// time.  Bound by the bytes.
+// A wave takes 512 columns of two neighbouring rows, from an even one on: 8 columns of each a lane, so 16 lanes are a
+// block and its maximum stays in registers.  Pairs of lanes then exchange halves, so that a store is 16 bytes a lane and
+// whole 128-byte lines of the two rows in the product's layout.  U such groups of columns are in flight at a time.
+// Bound by the bytes.
 template <int MODE, int U>
 __global__ __launch_bounds__(256) void f8_quant_kernel(const F8QuantParams p) {
     constexpr int PARTS = MODE == F8_DGLU ? 2 : 1;    // blocks that a lane makes at a time
     constexpr int IN = MODE == F8_PLAIN ? 1 : (MODE == F8_GLU ? 2 : 3);
-    const int lane = threadIdx.x & 63, sub = lane & 31;
+    const int lane = threadIdx.x & 63;
     const auto clamp = [&](int64_t o) { return static_cast<int>(o < 0 ? 0 : (o > p.M ? p.M : o)); };
     const int lo = clamp(p.offsets[0]), hi = clamp(p.offsets[p.E]);
     const int part = p.dim.part, part_p = p.dim.part_p;
     const int width = MODE == F8_DGLU ? part_p : p.dim.padded();
     const int64_t qblock = static_cast<int64_t>(p.M) * 64;
+    const int c0 = static_cast<int>(blockIdx.y) * U * 512 + 8 * lane;
     for (int64_t r0 = (lo & ~1) + 2 * (static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6)); r0 < hi;
          r0 += static_cast<int64_t>(gridDim.x) * 8) {
-        const int64_t r = r0 + (lane >> 5);
-        const bool live = r >= lo && r < hi;
-        const int64_t rr = live ? r : (r < lo ? r + 1 : r - 1);    // a row that exists, where this half has none
-        uint4 in[U][IN][2];
-        const int c0 = (static_cast<int>(blockIdx.y) * U) * 512 + sub * 16;
-        // the real column of a padded one's 16, and whether its two eights exist
-        auto at = [&](int u, bool (&ok)[2]) {
-            const int c = c0 + u * 512;
-            const int h = MODE != F8_DGLU && c >= part_p, k = c - h * part_p;
-            ok[0] = c < width && k < part;
-            ok[1] = c < width && k + 8 < part;
-            return h * part + k;
-        };
+        // rows that exist, where the pair has only one
+        const int64_t row[2] = {r0 < lo ? r0 + 1 : r0, r0 + 1 < hi ? r0 + 1 : r0};
+        uint4 in[U][2][IN];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            bool ok[2];
-            const int col = at(u, ok);
+            const int c = c0 + u * 512, h = MODE != F8_DGLU && c >= part_p, k = c - h * part_p;
+            const bool ok = c < width && k < part;
+            const int col = ok ? h * part + k : 0;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int y = 0; y < 2; ++y) {
                 const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < IN; ++i) in[u][i][e] = zero;
-                if (!ok[e]) continue;
                 if constexpr (MODE == F8_PLAIN) {
-                    in[u][0][e] = ld16_nt(p.x + rr * p.dim.real() + col + 8 * e);
+                    in[u][y][0] = ok ? ld16_nt(p.x + row[y] * p.dim.real() + col) : zero;
                 } else {
-                    const uint16_t* h = (MODE == F8_GLU ? p.x : p.h1) + rr * 2 * part + col + 8 * e;
-                    in[u][0][e] = ld16_nt(h);
-                    in[u][1][e] = ld16_nt(h + part);
-                    if constexpr (MODE == F8_DGLU) in[u][IN - 1][e] = ld16_nt(p.x + rr * part + col + 8 * e);
+                    const uint16_t* g = (MODE == F8_GLU ? p.x : p.h1) + row[y] * 2 * part + col;
+                    in[u][y][0] = ok ? ld16_nt(g) : zero;
+                    in[u][y][1] = ok ? ld16_nt(g + part) : zero;
+                    if constexpr (MODE == F8_DGLU) in[u][y][IN - 1] = ok ? ld16_nt(p.x + row[y] * part + col) : zero;
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            bool ok[2];
-            const int col = at(u, ok);
             const int c = c0 + u * 512;
             if (c >= width) continue;     // whole blocks of lanes
-            uint32_t v[PARTS][8];         // 16 bf16 values
+            const int h = MODE != F8_DGLU && c >= part_p, k = c - h * part_p;
+            uint2 q[PARTS][2];
+            uint32_t byte[PARTS][2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint4(&x)[IN][2] = in[u];
-                const uint32_t a[4] = {x[0][e].x, x[0][e].y, x[0][e].z, x[0][e].w};
-                const uint32_t b[4] = {x[IN > 1][e].x, x[IN > 1][e].y, x[IN > 1][e].z, x[IN > 1][e].w};
-                const uint32_t d[4] = {x[IN - 1][e].x, x[IN - 1][e].y, x[IN - 1][e].z, x[IN - 1][e].w};
+            for (int y = 0; y < 2; ++y) {
+                uint32_t v[PARTS][4];         // 8 bf16 values
+                const uint4(&x)[IN] = in[u][y];
+                const uint32_t a[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+                const uint32_t b[4] = {x[IN > 1].x, x[IN > 1].y, x[IN > 1].z, x[IN > 1].w};
+                const uint32_t d[4] = {x[IN - 1].x, x[IN - 1].y, x[IN - 1].z, x[IN - 1].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if constexpr (MODE == F8_PLAIN) {
-                        v[0][4 * e + i] = a[i];
+                        v[0][i] = a[i];
                     } else if constexpr (MODE == F8_GLU) {
-                        v[0][4 * e + i] = pack2(f8_act(lo_f(a[i]), lo_f(b[i]), p.slope), f8_act(hi_f(a[i]), hi_f(b[i]), p.slope));
+                        v[0][i] = pack2(f8_act(lo_f(a[i]), lo_f(b[i]), p.slope), f8_act(hi_f(a[i]), hi_f(b[i]), p.slope));
                     } else {
                         float g0, u0, g1, u1;
                         f8_act_grad(lo_f(a[i]), lo_f(b[i]), lo_f(d[i]), p.slope, g0, u0);
                         f8_act_grad(hi_f(a[i]), hi_f(b[i]), hi_f(d[i]), p.slope, g1, u1);
-                        v[0][4 * e + i] = pack2(g0, g1);
-                        v[PARTS - 1][4 * e + i] = pack2(u0, u1);
+                        v[0][i] = pack2(g0, g1);
+                        v[PARTS - 1][i] = pack2(u0, u1);
                     }
                 }
                 if constexpr (MODE != F8_PLAIN) {
-                    if (p.v_out && live && ok[e]) {
-                        uint16_t* o = p.v_out + r * p.dim.real() + col + 8 * e;
+                    if (p.v_out && k < part) {      // twice the same where the pair has one row
+                        uint16_t* o = p.v_out + row[y] * p.dim.real() + k;
 #pragma unroll
-                        for (int h = 0; h < PARTS; ++h)
-                            st16_nt(o + h * part, make_uint4(v[h][4 * e], v[h][4 * e + 1], v[h][4 * e + 2], v[h][4 * e + 3]));
+                        for (int z = 0; z < PARTS; ++z) st16_nt(o + z * part, make_uint4(v[z][0], v[z][1], v[z][2], v[z][3]));
                     }
                 }
+#pragma unroll
+                for (int z = 0; z < PARTS; ++z) {
+                    uint32_t m = max(max(f8_top2(v[z][0]), f8_top2(v[z][1])), max(f8_top2(v[z][2]), f8_top2(v[z][3])));
+                    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xb1, 0xf, 0xf, true)));    // lane ^ 1
+                    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4e, 0xf, 0xf, true)));    // lane ^ 2
+                    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x141, 0xf, 0xf, true)));   // the other four
+                    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x140, 0xf, 0xf, true)));   // the other eight
+                    const F8Scale s = f8_scale(m);
+                    q[z][y] = make_uint2(f8_four(lo_f(v[z][0]), hi_f(v[z][0]), lo_f(v[z][1]), hi_f(v[z][1]), s),
+                                         f8_four(lo_f(v[z][2]), hi_f(v[z][2]), lo_f(v[z][3]), hi_f(v[z][3]), s));
+                    byte[z][y] = s.byte;
+                }
             }
+            // even lanes: 16 columns of the first row; odd lanes: of the second
+            const bool odd = lane & 1;
+            const int64_t r = r0 + odd;
+            const bool live = r >= lo && r < hi;
 #pragma unroll
-            for (int h = 0; h < PARTS; ++h) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, f8_top2(v[h][i]));
-                m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xb1, 0xf, 0xf, true)));    // lane ^ 1
-                m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4e, 0xf, 0xf, true)));    // lane ^ 2
-                m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x141, 0xf, 0xf, true)));   // the other four
-                const F8Scale s = f8_scale(m);
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = f8_four(lo_f(v[h][2 * i]), hi_f(v[h][2 * i]), lo_f(v[h][2 * i + 1]), hi_f(v[h][2 * i + 1]), s);
+            for (int z = 0; z < PARTS; ++z) {
+                const uint2 send = odd ? q[z][0] : q[z][1], keep = odd ? q[z][1] : q[z][0];
+                const uint2 got = make_uint2(__builtin_amdgcn_mov_dpp(send.x, 0xb1, 0xf, 0xf, true),
+                                             __builtin_amdgcn_mov_dpp(send.y, 0xb1, 0xf, 0xf, true));
+                // by bits: an index would put the two into memory
+                const uint32_t mine = byte[z][0] ^ ((byte[z][0] ^ byte[z][1]) & (0u - static_cast<uint32_t>(odd)));
                 if (!live) continue;
-                const int cp = c + h * part_p, kb = cp / F8_BLOCK;
-                *reinterpret_cast<uint4*>(p.q + (cp >> 6) * qblock + r * 64 + (cp & 63)) = make_uint4(o[0], o[1], o[2], o[3]);
-                if ((lane & 7) == 0) p.s[4 * (static_cast<int64_t>(kb >> 2) * p.M + r) + (kb & 3)] = static_cast<uint8_t>(s.byte);
+                const int cp = (c & ~15) + z * part_p, kb = cp / F8_BLOCK;
+                *reinterpret_cast<uint4*>(p.q + (cp >> 6) * qblock + r * 64 + (cp & 63)) =
+                    odd ? make_uint4(got.x, got.y, keep.x, keep.y) : make_uint4(keep.x, keep.y, got.x, got.y);
+                if ((lane & 14) == 0)
+                    p.s[4 * (static_cast<int64_t>(kb >> 2) * p.M + r) + (kb & 3)] = static_cast<uint8_t>(mine);
             }
         }
     }
@@ -1072,9 +1072,11 @@ static hipError_t launch_quant(const F8QuantParams& p, int num_cu, hipStream_t s
 }
 
 hipError_t launch_f8_quant(F8Mode mode, const F8QuantParams& p, int num_cu, hipStream_t s) {
+    // few rows: a group of columns a wave, for more waves
+    const bool few = static_cast<int64_t>(p.M) < 16 * num_cu;
     switch (mode) {
-        case F8_PLAIN: return launch_quant<F8_PLAIN, 2>(p, num_cu, s);
-        case F8_GLU: return launch_quant<F8_GLU, 1>(p, num_cu, s);
+        case F8_PLAIN: return few ? launch_quant<F8_PLAIN, 1>(p, num_cu, s) : launch_quant<F8_PLAIN, 4>(p, num_cu, s);
+        case F8_GLU: return few ? launch_quant<F8_GLU, 1>(p, num_cu, s) : launch_quant<F8_GLU, 2>(p, num_cu, s);
         default: return launch_quant<F8_DGLU, 1>(p, num_cu, s);
     }
 }
