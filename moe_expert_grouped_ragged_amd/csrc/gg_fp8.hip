@@ -43,20 +43,25 @@ __device__ __forceinline__ uint32_t f8_four(float a, float b, float c, float d, 
     r = __builtin_amdgcn_cvt_pk_fp8_f32(c * s.inv, d * s.inv, r, true);
     return s.nan ? 0x7f7f7f7fu : static_cast<uint32_t>(r);
 }
-// The largest |v| of a packed pair of bf16 values, as fp32 bits.
-__device__ __forceinline__ uint32_t f8_top2(uint32_t pair) {
-    return max((pair & 0x7fffu) << 16, pair & 0x7fff0000u);
+// Running |v| maxima of packed pairs of bf16 values, half by half, and the larger half as fp32 bits.
+__device__ __forceinline__ uint32_t f8_max2(uint32_t top, uint32_t pair) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, top),
+                                                                  __builtin_bit_cast(u16x2, pair & 0x7fff7fffu)));
 }
+__device__ __forceinline__ uint32_t f8_top(uint32_t top) { return max(top << 16, top & 0xffff0000u); }
 
-// The activation and its derivative on bf16 values, with the arithmetic of the
-// bf16 path's epilogues: A = bf16(act(gate) * up), dH1 = bf16 of dg and du.
-__device__ __forceinline__ float f8_act(float g, float u, float slope) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-(slope * g))) * u;
+// The activation and its derivative on bf16 values: A = bf16(act(gate) * up), dH1 = bf16 of dg and du.  e: -slope
+// log2 e, so that the sigmoid is one product, 2^x, a sum and a reciprocal.
+__device__ __forceinline__ float f8_log2e(float slope) { return -1.44269504088896340736f * slope; }
+__device__ __forceinline__ float f8_sigmoid(float g, float e) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(e * g));
 }
-__device__ __forceinline__ void f8_act_grad(float g, float u, float da, float slope, float& dg, float& du) {
-    const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-(slope * g)));
-    dg = da * u * sg * (1.0f + slope * g * (1.0f - sg));
-    du = da * g * sg;
+__device__ __forceinline__ float f8_act(float g, float u, float e) { return g * f8_sigmoid(g, e) * u; }
+__device__ __forceinline__ void f8_act_grad(float g, float u, float da, float slope, float e, float& dg, float& du) {
+    const float sg = f8_sigmoid(g, e), t = da * sg;
+    dg = t * u * (1.0f + slope * g * (1.0f - sg));
+    du = t * g;
 }
 
 // A wave takes 512 columns of two neighbouring rows, from an even one on: 8 columns of each a lane, so 16 lanes are a
@@ -73,6 +78,7 @@ __global__ __launch_bounds__(256) void f8_quant_kernel(const F8QuantParams p) {
     const int part = p.dim.part, part_p = p.dim.part_p;
     const int width = MODE == F8_DGLU ? part_p : p.dim.padded();
     const int64_t qblock = static_cast<int64_t>(p.M) * 64;
+    const float e2 = f8_log2e(p.slope);
     const int c0 = static_cast<int>(blockIdx.y) * U * 512 + 8 * lane;
     for (int64_t r0 = (lo & ~1) + 2 * (static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6)); r0 < hi;
          r0 += static_cast<int64_t>(gridDim.x) * 8) {
@@ -116,11 +122,11 @@ __global__ __launch_bounds__(256) void f8_quant_kernel(const F8QuantParams p) {
                     if constexpr (MODE == F8_PLAIN) {
                         v[0][i] = a[i];
                     } else if constexpr (MODE == F8_GLU) {
-                        v[0][i] = pack2(f8_act(lo_f(a[i]), lo_f(b[i]), p.slope), f8_act(hi_f(a[i]), hi_f(b[i]), p.slope));
+                        v[0][i] = pack2(f8_act(lo_f(a[i]), lo_f(b[i]), e2), f8_act(hi_f(a[i]), hi_f(b[i]), e2));
                     } else {
                         float g0, u0, g1, u1;
-                        f8_act_grad(lo_f(a[i]), lo_f(b[i]), lo_f(d[i]), p.slope, g0, u0);
-                        f8_act_grad(hi_f(a[i]), hi_f(b[i]), hi_f(d[i]), p.slope, g1, u1);
+                        f8_act_grad(lo_f(a[i]), lo_f(b[i]), lo_f(d[i]), p.slope, e2, g0, u0);
+                        f8_act_grad(hi_f(a[i]), hi_f(b[i]), hi_f(d[i]), p.slope, e2, g1, u1);
                         v[0][i] = pack2(g0, g1);
                         v[PARTS - 1][i] = pack2(u0, u1);
                     }
@@ -134,7 +140,7 @@ __global__ __launch_bounds__(256) void f8_quant_kernel(const F8QuantParams p) {
                 }
 #pragma unroll
                 for (int z = 0; z < PARTS; ++z) {
-                    uint32_t m = max(max(f8_top2(v[z][0]), f8_top2(v[z][1])), max(f8_top2(v[z][2]), f8_top2(v[z][3])));
+                    uint32_t m = f8_top(f8_max2(f8_max2(f8_max2(f8_max2(0, v[z][0]), v[z][1]), v[z][2]), v[z][3]));
                     m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xb1, 0xf, 0xf, true)));    // lane ^ 1
                     m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4e, 0xf, 0xf, true)));    // lane ^ 2
                     m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x141, 0xf, 0xf, true)));   // the other four
@@ -184,8 +190,9 @@ __global__ __launch_bounds__(256) void f8_quant_weights_kernel(const uint16_t* _
     for (int i = 0; i < 8; ++i) {
         v[i] = make_uint4(0, 0, 0, 0);
         if (16 * i + t < rows && col < k.part) v[i] = *reinterpret_cast<const uint4*>(w + (row0 + 16 * i + t) * k.part + col);
-        m = max(max(max(m, f8_top2(v[i].x)), max(f8_top2(v[i].y), f8_top2(v[i].z))), f8_top2(v[i].w));
+        m = f8_max2(f8_max2(f8_max2(f8_max2(m, v[i].x), v[i].y), v[i].z), v[i].w);
     }
+    m = f8_top(m);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 64)));
     if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = m;
@@ -383,6 +390,7 @@ __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_
     // a block's rows of h1, loaded when the block begins
     uint2 hg[EPI == F8_STORE_DGLU ? TB : 1][4], hu[EPI == F8_STORE_DGLU ? TB : 1][4];
     int nb = nb0;
+    const float e2 = f8_log2e(p.slope);
     auto load_h1 = [&](int b) {
         if constexpr (EPI == F8_STORE_DGLU) {
 #pragma unroll
@@ -411,7 +419,7 @@ __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_
     auto block_tops = [&](uint32_t (&top)[TB], int part) {
 #pragma unroll
         for (int i = 0; i < TB; ++i) {
-            top[i] = max_other_half(top[i]);
+            top[i] = max_other_half(f8_top(top[i]));
             if (lane < 32) s_top[part][wave][32 * i + lane] = top[i];
         }
     };
@@ -460,22 +468,22 @@ __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_
                             *reinterpret_cast<uint2*>(o) = b[0];
                             *reinterpret_cast<uint2*>(o + p.n.part) = b[C - 1];
                         }
-                        v[0][i][2 * q] = pack2(f8_act(lo_f(b[0].x), lo_f(b[C - 1].x), p.slope), f8_act(hi_f(b[0].x), hi_f(b[C - 1].x), p.slope));
-                        v[0][i][2 * q + 1] = pack2(f8_act(lo_f(b[0].y), lo_f(b[C - 1].y), p.slope), f8_act(hi_f(b[0].y), hi_f(b[C - 1].y), p.slope));
+                        v[0][i][2 * q] = pack2(f8_act(lo_f(b[0].x), lo_f(b[C - 1].x), e2), f8_act(hi_f(b[0].x), hi_f(b[C - 1].x), e2));
+                        v[0][i][2 * q + 1] = pack2(f8_act(lo_f(b[0].y), lo_f(b[C - 1].y), e2), f8_act(hi_f(b[0].y), hi_f(b[C - 1].y), e2));
                     } else {
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             const uint32_t d = y ? b[0].y : b[0].x, g = y ? hg[i][q].y : hg[i][q].x, u = y ? hu[i][q].y : hu[i][q].x;
                             float g0, u0, g1, u1;
-                            f8_act_grad(lo_f(g), lo_f(u), lo_f(d), p.slope, g0, u0);
-                            f8_act_grad(hi_f(g), hi_f(u), hi_f(d), p.slope, g1, u1);
+                            f8_act_grad(lo_f(g), lo_f(u), lo_f(d), p.slope, e2, g0, u0);
+                            f8_act_grad(hi_f(g), hi_f(u), hi_f(d), p.slope, e2, g1, u1);
                             v[0][i][2 * q + y] = pack2(g0, g1);
                             v[PARTS - 1][i][2 * q + y] = pack2(u0, u1);
                         }
                     }
 #pragma unroll
                     for (int h = 0; h < PARTS; ++h)
-                        top[h][i] = max(top[h][i], max(f8_top2(v[h][i][2 * q]), f8_top2(v[h][i][2 * q + 1])));
+                        top[h][i] = f8_max2(f8_max2(top[h][i], v[h][i][2 * q]), v[h][i][2 * q + 1]);
                 }
             }
             block_barrier();     // the last block's maxima are read
@@ -617,6 +625,8 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     const int nsteps = p.kblocks * 2, nstages = nsteps;
     const int part_p = p.n.part_p, width = EPI == F8_STORE_GLU ? part_p : p.n.padded();
     const int tiles_n = (width + OC - 1) / OC;
+    // The 32 tiles that an XCD works on at a time are about as many row as column tiles, whose operands its L2 holds.
+    const int band = max(4, 32 / tiles_n);
     prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
                    [&](int m) { return (f8_tile_rows(m, TR, p.group) + TR - 1) / TR * tiles_n; });
     const int n_tiles = uni(s_pre[p.E]);
@@ -646,7 +656,9 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
         const int local = t - uni(s_pre[e]);
         const int lo = uni(s_off[e]), m = f8_tile_rows(uni(s_off[e + 1]) - lo, TR, p.group);
         const int tiles_m = (m + TR - 1) / TR;
-        const int tm = local % tiles_m, tn = local / tiles_m;
+        // groups of `band` row tiles, columns by columns
+        const int g = local / (band * tiles_n), r = local - g * band * tiles_n, high = min(band, tiles_m - g * band);
+        const int tm = g * band + r % high, tn = r / high;
         next.row0 = lo + tm * TR;
         next.rows = min(TR, m - tm * TR);
         next.col0 = tn * OC;
@@ -915,6 +927,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
                 p.s_out[(static_cast<int64_t>(kb >> 2) * p.M + prow0 + gr) * 4 + (kb & 3)] = static_cast<uint8_t>(sc.byte);
         };
         const bool all_rows = prows == TR;
+        const float e2 = f8_log2e(p.slope);
         // All stores of a wave are issued where the tile is full; a store whose lanes all lie outside may be
         // skipped, so a partial tile counts as none.
         bool full = all_rows;
@@ -948,11 +961,11 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
                     top[i] = 0;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), p.slope), f8_act(hi_f(g[c].x), hi_f(u[c].x), p.slope));
-                        av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), p.slope), f8_act(hi_f(g[c].y), hi_f(u[c].y), p.slope));
-                        top[i] = max(top[i], max(f8_top2(av[i][2 * c]), f8_top2(av[i][2 * c + 1])));
+                        av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), e2), f8_act(hi_f(g[c].x), hi_f(u[c].x), e2));
+                        av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), e2), f8_act(hi_f(g[c].y), hi_f(u[c].y), e2));
+                        top[i] = f8_max2(f8_max2(top[i], av[i][2 * c]), av[i][2 * c + 1]);
                     }
-                    top[i] = max_other_half(top[i]);
+                    top[i] = max_other_half(f8_top(top[i]));
                     if (ln < 32) s_row_top[wave * 32 * BR + 32 * i + ln] = top[i];
                     if (p.out) {
                         uint4 o[4];
@@ -1017,11 +1030,11 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
                                 for (int y = 0; y < 2; ++y) {
                                     const uint32_t dd = y ? d[c].y : d[c].x, gg = y ? g[c].y : g[c].x, uu = y ? u[c].y : u[c].x;
                                     float g0, u0, g1, u1;
-                                    f8_act_grad(lo_f(gg), lo_f(uu), lo_f(dd), p.slope, g0, u0);
-                                    f8_act_grad(hi_f(gg), hi_f(uu), hi_f(dd), p.slope, g1, u1);
+                                    f8_act_grad(lo_f(gg), lo_f(uu), lo_f(dd), p.slope, e2, g0, u0);
+                                    f8_act_grad(hi_f(gg), hi_f(uu), hi_f(dd), p.slope, e2, g1, u1);
                                     const uint32_t pg = pack2(g0, g1), pu = pack2(u0, u1);
-                                    top[0] = max(top[0], f8_top2(pg));
-                                    top[1] = max(top[1], f8_top2(pu));
+                                    top[0] = f8_max2(top[0], pg);
+                                    top[1] = f8_max2(top[1], pu);
                                     v[0][jh][2 * c + y] = acc_wr(pg);
                                     v[1][jh][2 * c + y] = acc_wr(pu);
                                 }
@@ -1029,7 +1042,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
                         });
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const F8Scale sc = f8_scale(max_other_half(top[h]));
+                            const F8Scale sc = f8_scale(max_other_half(f8_top(top[h])));
 #pragma unroll
                             for (int jh = 0; jh < 2; ++jh) {
                                 uint32_t d[8];
@@ -1054,8 +1067,8 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
 #pragma unroll
         for (int c = 0; c < WS; ++c) wd_next[c] = wd_first[c];
     }
+    wait_vmcnt<0>();     // the last copies: none is under way to LDS that is another workgroup's
     if (p.group == 0) return;
-    wait_vmcnt<0>();     // the last copies
     __syncthreads();
     f8_stream_list<EPI>(p, s_off, s_pre, s_ring, reinterpret_cast<uint32_t(*)[4][F8_GROUP]>(s_stg));
 }
