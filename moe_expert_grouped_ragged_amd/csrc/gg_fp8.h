@@ -80,6 +80,8 @@ struct F8Params {
     int M, E;
     int kblocks;             // blocks of the summed dimension
     F8Dim n;                 // columns
+    const uint16_t* x;       // rows [M][k] to be quantized by the product itself (f8_quantizes), or null
+    F8Dim k;                 // with x: the summed dimension
     uint16_t* out;           // F8_STORE: [M][n]; F8_STORE_GLU: H1 [M][n], or null
     const uint16_t* h1;      // F8_STORE_DGLU: [M][2 n]
     float slope;
@@ -107,6 +109,13 @@ inline F8Plan f8_plan(int M, int E, int tiles_n, int kblocks, int num_cu) {
     plan.group = panel < F8_GROUP ? panel : F8_GROUP;
     plan.tile = M <= 64 && plan.group ? 0 : (large < num_cu || half ? 128 : 256);
     return plan;
+}
+
+// Whether a product quantizes its rows itself (all of them run as streaming items, and few enough that every workgroup
+// makes its own panel of them sooner than a launch of its own would: one row each for 8 of 128 experts, K = N = 4096:
+// TOKENS).
+inline bool f8_quantizes(int64_t M, const F8Dim& k) {
+    return M <= 64 && static_cast<int64_t>(k.padded()) * 32 <= F8_PANEL;
 }
 
 hipError_t launch_f8_quant(F8Mode mode, const F8QuantParams& p, int num_cu, hipStream_t s);

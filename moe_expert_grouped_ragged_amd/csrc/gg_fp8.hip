@@ -317,11 +317,73 @@ __device__ __forceinline__ uint32_t max_other_half(uint32_t v) {   // of lanes l
 // one of R units ahead, the first of them from before the panel is filled:
 // nothing drains at a block's end, where the sums go to the epilogue, and
 // loads are repeated only at the stretch's own end.
+// The panel of quantized rows, F 16-byte operands of a thread in flight.
+template <int TB>
+__device__ __forceinline__ void f8_copy_panel(const F8Params& p, int row0, int rows, uint8_t* panel, uint8_t* pscale) {
+    constexpr int F = 8, T = 256;
+    const int nu = p.kblocks, chunks = nu * TB * 256;
+    for (int i0 = threadIdx.x; i0 < chunks; i0 += F * T) {
+        i32x4 v[F];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            // operand bytes 16 i: of step st, row block b, half h of 32 columns, lane l
+            const int i = min(i0 + j * T, chunks - 1);
+            const int l = i & 63, h = (i >> 6) & 1, st = (i >> 7) / TB, b = (i >> 7) % TB, r = b * 32 + (l & 31);
+            if (r < rows)
+                v[j] = *reinterpret_cast<const i32x4*>(p.q + (static_cast<int64_t>(st) * p.M + row0 + r) * 64 + 32 * (l >> 5) + 16 * h);
+        }
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int i = i0 + j * T, r = (i >> 7) % TB * 32 + (i & 31);
+            if (i < chunks && r < rows) *reinterpret_cast<i32x4*>(panel + i * 16) = v[j];
+        }
+    }
+    for (int i = threadIdx.x; i < nu * TB * 32; i += T) {
+        const int k = i / (TB * 32), r = i % (TB * 32);
+        if (r < rows) pscale[i] = p.s[(static_cast<int64_t>(k >> 2) * p.M + row0 + r) * 4 + (k & 3)];
+    }
+}
+
+// The panel made from the rows themselves: 16 lanes a block of a row, F of them in flight.
+template <int TB>
+__device__ __forceinline__ void f8_quant_panel(const F8Params& p, int row0, int rows, uint8_t* panel, uint8_t* pscale) {
+    constexpr int F = 4, G = 16;      // G: groups of 16 lanes
+    const int nu = p.kblocks, items = rows * nu, s = threadIdx.x & 15;
+    const int part = p.k.part, part_p = p.k.part_p;
+    for (int i0 = threadIdx.x >> 4; i0 < items; i0 += F * G) {
+        uint4 v[F];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int i = min(i0 + j * G, items - 1), r = i / nu, c = (i - r * nu) * F8_BLOCK + 8 * s;
+            const int h = c >= part_p, k = c - h * part_p;      // padded columns of both parts lie below 2 part_p
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (k < part) v[j] = *reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row0 + r) * p.k.real() + h * part + k);
+        }
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int i = i0 + j * G, r = i / nu, kb = i - r * nu;
+            uint32_t m = f8_top(f8_max2(f8_max2(f8_max2(f8_max2(0, v[j].x), v[j].y), v[j].z), v[j].w));
+            m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xb1, 0xf, 0xf, true)));
+            m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4e, 0xf, 0xf, true)));
+            m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x141, 0xf, 0xf, true)));
+            m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x140, 0xf, 0xf, true)));
+            const F8Scale sc = f8_scale(m);
+            if (i >= items) continue;
+            // columns 8 s .. of the block: step s / 8, lanes' half s / 4 % 2, operand half s / 2 % 2
+            *reinterpret_cast<uint2*>(panel + ((kb * 2 + (s >> 3)) * TB + (r >> 5)) * 2048 + ((s >> 1) & 1) * 1024 +
+                                      ((s >> 2) & 1) * 512 + (r & 31) * 16 + (s & 1) * 8) =
+                make_uint2(f8_four(lo_f(v[j].x), hi_f(v[j].x), lo_f(v[j].y), hi_f(v[j].y), sc),
+                           f8_four(lo_f(v[j].z), hi_f(v[j].z), lo_f(v[j].w), hi_f(v[j].w), sc));
+            if (s == 0) pscale[(kb * TB + (r >> 5)) * 32 + (r & 31)] = static_cast<uint8_t>(sc.byte);
+        }
+    }
+}
+
 template <int TB, int EPI>
 __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_t* w, const uint8_t* ws, int row0, int rows,
                                                  int nb0, int nb1, uint8_t* panel, uint32_t (*s_top)[4][F8_GROUP]) {
     constexpr int C = EPI == F8_STORE_GLU ? 2 : 1;   // column blocks of a wave
-    constexpr int R = 8 / C, W = 4;
+    constexpr int R = 8 / C;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), nu = p.kblocks;
     const int total = (nb1 - nb0) * nu;
     const int64_t wblock = static_cast<int64_t>(nu) * 4096;      // bytes of 32 columns
@@ -364,28 +426,9 @@ __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_
     }
     uint8_t* pscale = panel + F8_PANEL;      // [nu][32 TB]
     __syncthreads();   // the last panel is read
-    constexpr int F = 8;   // loads of a thread in flight
-    const int chunks = nu * TB * 256;
-    for (int i0 = threadIdx.x; i0 < chunks; i0 += F * W * 64) {
-        i32x4 v[F];
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
-            // operand bytes 16 i: of step st, row block b, half h of 32 columns, lane l
-            const int i = min(i0 + j * W * 64, chunks - 1);
-            const int l = i & 63, h = (i >> 6) & 1, st = (i >> 7) / TB, b = (i >> 7) % TB;
-            v[j] = *reinterpret_cast<const i32x4*>(
-                p.q + (static_cast<int64_t>(st) * p.M + row0 + min(b * 32 + (l & 31), rows - 1)) * 64 + 32 * (l >> 5) + 16 * h);
-        }
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int i = i0 + j * W * 64;
-            if (i < chunks) *reinterpret_cast<i32x4*>(panel + i * 16) = v[j];
-        }
-    }
-    for (int i = threadIdx.x; i < nu * TB * 32; i += W * 64) {
-        const int k = i / (TB * 32), r = i % (TB * 32);
-        pscale[i] = p.s[(static_cast<int64_t>(k >> 2) * p.M + row0 + min(r, rows - 1)) * 4 + (k & 3)];
-    }
+    // What belongs to rows that do not exist stays as it is: a row's products meet no other row's.
+    if (p.x) f8_quant_panel<TB>(p, row0, rows, panel, pscale);
+    else f8_copy_panel<TB>(p, row0, rows, panel, pscale);
     __syncthreads();
     // a block's rows of h1, loaded when the block begins
     uint2 hg[EPI == F8_STORE_DGLU ? TB : 1][4], hu[EPI == F8_STORE_DGLU ? TB : 1][4];

@@ -67,9 +67,15 @@ F8QuantParams quantization(const void* x, const void* h1, const int64_t* offsets
     return p;
 }
 
-int quantize_and_multiply(F8Mode mode, const F8QuantParams& p, const F8Params& g, int num_cu, hipStream_t stream) {
-    if (launch_f8_quant(mode, p, num_cu, stream) != hipSuccess) return GG_ERR_HIP;
-    return launch_f8_gemm(F8_STORE, g, num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+int quantize_and_multiply(F8Mode mode, F8Epilogue epilogue, const F8QuantParams& p, F8Params g, int num_cu,
+                          hipStream_t stream) {
+    if (mode == F8_PLAIN && f8_quantizes(p.M, p.dim)) {
+        g.x = p.x;
+        g.k = p.dim;
+    } else if (launch_f8_quant(mode, p, num_cu, stream) != hipSuccess) {
+        return GG_ERR_HIP;
+    }
+    return launch_f8_gemm(epilogue, g, num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 // Quantized rows start on 256 bytes.
@@ -154,7 +160,7 @@ int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void*
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     uint8_t* q = static_cast<uint8_t*>(workspace);
     const F8Dim n = f8_dim(N, halves), k = f8_dim(K, 1);
-    return quantize_and_multiply(glu ? F8_GLU : F8_PLAIN, quantization(x, nullptr, offsets, M, E, k, slope, a_out, q),
+    return quantize_and_multiply(glu ? F8_GLU : F8_PLAIN, F8_STORE, quantization(x, nullptr, offsets, M, E, k, slope, a_out, q),
                                  product(q, offsets, M, packed, E, n, k, y), info.num_cu, stream);
 }
 
@@ -183,7 +189,7 @@ int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     uint8_t* q = static_cast<uint8_t*>(workspace);
     const F8Dim n = f8_dim(N, halves), k = f8_dim(K, 1);
-    return quantize_and_multiply(glu ? F8_DGLU : F8_PLAIN, quantization(dy, h1, offsets, M, E, n, slope, dh1_out, q),
+    return quantize_and_multiply(glu ? F8_DGLU : F8_PLAIN, F8_STORE, quantization(dy, h1, offsets, M, E, n, slope, dh1_out, q),
                                  product(q, offsets, M, packed, E, k, n, dx), info.num_cu, stream);
 }
 
@@ -215,13 +221,13 @@ int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const v
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     const F8Dim h = f8_dim(H, 1), f2 = f8_dim(2 * F, 2), f = f8_dim(F, 1);
     uint8_t *qx = static_cast<uint8_t*>(workspace), *qa = qx + glu_rows(M, h);
-    if (launch_f8_quant(F8_PLAIN, quantization(x, nullptr, offsets, M, E, h, 1.0f, nullptr, qx), info.num_cu, stream) != hipSuccess)
-        return GG_ERR_HIP;
     F8Params g = product(qx, offsets, M, fc1, E, f2, h, h1_out);
     g.slope = slope;
     g.q_out = qa;
     g.s_out = qa + M * f.padded();
-    if (launch_f8_gemm(F8_STORE_GLU, g, info.num_cu, stream) != hipSuccess) return GG_ERR_HIP;
+    st = quantize_and_multiply(F8_PLAIN, F8_STORE_GLU, quantization(x, nullptr, offsets, M, E, h, 1.0f, nullptr, qx), g, info.num_cu,
+                               stream);
+    if (st != GG_OK) return st;
     return launch_f8_gemm(F8_STORE, product(qa, offsets, M, fc2, E, h, f, y), info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
@@ -249,14 +255,14 @@ int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     const F8Dim h = f8_dim(H, 1), f2 = f8_dim(2 * F, 2), f = f8_dim(F, 1);
     uint8_t *qy = static_cast<uint8_t*>(workspace), *qd = qy + glu_rows(M, h);
-    if (launch_f8_quant(F8_PLAIN, quantization(dy, nullptr, offsets, M, E, h, 1.0f, nullptr, qy), info.num_cu, stream) != hipSuccess)
-        return GG_ERR_HIP;
     F8Params g = product(qy, offsets, M, fc2_t, E, f, h, nullptr);
     g.h1 = static_cast<const uint16_t*>(h1);
     g.slope = slope;
     g.q_out = qd;
     g.s_out = qd + M * f2.padded();
-    if (launch_f8_gemm(F8_STORE_DGLU, g, info.num_cu, stream) != hipSuccess) return GG_ERR_HIP;
+    st = quantize_and_multiply(F8_PLAIN, F8_STORE_DGLU, quantization(dy, nullptr, offsets, M, E, h, 1.0f, nullptr, qy), g, info.num_cu,
+                               stream);
+    if (st != GG_OK) return st;
     return launch_f8_gemm(F8_STORE, product(qd, offsets, M, fc1_t, E, h, f2, dx), info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
