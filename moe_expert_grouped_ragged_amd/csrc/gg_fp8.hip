@@ -348,33 +348,48 @@ __device__ __forceinline__ void f8_copy_panel(const F8Params& p, int row0, int r
 template <int TB>
 __device__ __forceinline__ void f8_quant_panel(const F8Params& p, int row0, int rows, uint8_t* panel, uint8_t* pscale) {
     constexpr int F = 4, G = 16;      // G: groups of 16 lanes
-    const int nu = p.kblocks, items = rows * nu, s = threadIdx.x & 15;
+    const int nu = p.kblocks, s = threadIdx.x & 15;
     const int part = p.k.part, part_p = p.k.part_p;
-    for (int i0 = threadIdx.x >> 4; i0 < items; i0 += F * G) {
+    // the group's items (row, block), G blocks apart
+    int r = 0, kb = threadIdx.x >> 4;
+    auto wrap = [&]() {
+        while (kb >= nu) {
+            kb -= nu;
+            ++r;
+        }
+    };
+    wrap();
+    while (r < rows) {
         uint4 v[F];
+        int at[F];       // where the item's values go; -1: no item
+        int scale[F];
 #pragma unroll
         for (int j = 0; j < F; ++j) {
-            const int i = min(i0 + j * G, items - 1), r = i / nu, c = (i - r * nu) * F8_BLOCK + 8 * s;
-            const int h = c >= part_p, k = c - h * part_p;      // padded columns of both parts lie below 2 part_p
+            const int c = kb * F8_BLOCK + 8 * s, h = c >= part_p, k = c - h * part_p;
             v[j] = make_uint4(0, 0, 0, 0);
-            if (k < part) v[j] = *reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row0 + r) * p.k.real() + h * part + k);
+            if (r < rows && k < part)
+                v[j] = *reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row0 + r) * p.k.real() + h * part + k);
+            // columns 8 s .. of the block: step s / 8, lanes' half s / 4 % 2, operand half s / 2 % 2
+            at[j] = r < rows ? ((kb * 2 + (s >> 3)) * TB + (r >> 5)) * 2048 + ((s >> 1) & 1) * 1024 + ((s >> 2) & 1) * 512 +
+                                   (r & 31) * 16 + (s & 1) * 8
+                             : -1;
+            scale[j] = (kb * TB + (r >> 5)) * 32 + (r & 31);
+            kb += G;
+            wrap();
         }
 #pragma unroll
         for (int j = 0; j < F; ++j) {
-            const int i = i0 + j * G, r = i / nu, kb = i - r * nu;
             uint32_t m = f8_top(f8_max2(f8_max2(f8_max2(f8_max2(0, v[j].x), v[j].y), v[j].z), v[j].w));
             m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xb1, 0xf, 0xf, true)));
             m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4e, 0xf, 0xf, true)));
             m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x141, 0xf, 0xf, true)));
             m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x140, 0xf, 0xf, true)));
             const F8Scale sc = f8_scale(m);
-            if (i >= items) continue;
-            // columns 8 s .. of the block: step s / 8, lanes' half s / 4 % 2, operand half s / 2 % 2
-            *reinterpret_cast<uint2*>(panel + ((kb * 2 + (s >> 3)) * TB + (r >> 5)) * 2048 + ((s >> 1) & 1) * 1024 +
-                                      ((s >> 2) & 1) * 512 + (r & 31) * 16 + (s & 1) * 8) =
+            if (at[j] < 0) continue;
+            *reinterpret_cast<uint2*>(panel + at[j]) =
                 make_uint2(f8_four(lo_f(v[j].x), hi_f(v[j].x), lo_f(v[j].y), hi_f(v[j].y), sc),
                            f8_four(lo_f(v[j].z), hi_f(v[j].z), lo_f(v[j].w), hi_f(v[j].w), sc));
-            if (s == 0) pscale[(kb * TB + (r >> 5)) * 32 + (r & 31)] = static_cast<uint8_t>(sc.byte);
+            if (s == 0) pscale[scale[j]] = static_cast<uint8_t>(sc.byte);
         }
     }
 }
@@ -1002,23 +1017,34 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
                     sums(i_tag, GrpTag<0>{}, g);
                     sums(i_tag, GrpTag<1>{}, u);
                     top[i] = 0;
+                    auto act = [&](int c0) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), e2), f8_act(hi_f(g[c].x), hi_f(u[c].x), e2));
-                        av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), e2), f8_act(hi_f(g[c].y), hi_f(u[c].y), e2));
-                        top[i] = f8_max2(f8_max2(top[i], av[i][2 * c]), av[i][2 * c + 1]);
-                    }
-                    top[i] = max_other_half(f8_top(top[i]));
-                    if (ln < 32) s_row_top[wave * 32 * BR + 32 * i + ln] = top[i];
+                        for (int c = c0; c < c0 + 4; ++c) {
+                            av[i][2 * c] = pack2(f8_act(lo_f(g[c].x), lo_f(u[c].x), e2), f8_act(hi_f(g[c].x), hi_f(u[c].x), e2));
+                            av[i][2 * c + 1] = pack2(f8_act(lo_f(g[c].y), lo_f(u[c].y), e2), f8_act(hi_f(g[c].y), hi_f(u[c].y), e2));
+                            top[i] = f8_max2(f8_max2(top[i], av[i][2 * c]), av[i][2 * c + 1]);
+                        }
+                    };
+                    // the arithmetic covers the staging area's round trips
+                    uint4 o[4];
                     if (p.out) {
-                        uint4 o[4];
                         put(g);
                         rows_of(o);
                         put(u);
+                    }
+                    fence();
+                    act(0);
+                    fence();
+                    if (p.out) {
                         store(o, p.out + k0, p.n.real(), i, p.n.part - k0, full_tag);
                         rows_of(o);
-                        store(o, p.out + p.n.part + k0, p.n.real(), i, p.n.part - k0, full_tag);
                     }
+                    fence();
+                    act(4);
+                    top[i] = max_other_half(f8_top(top[i]));
+                    if (ln < 32) s_row_top[wave * 32 * BR + 32 * i + ln] = top[i];
+                    fence();
+                    if (p.out) store(o, p.out + p.n.part + k0, p.n.real(), i, p.n.part - k0, full_tag);
                 });
                 block_barrier();
 #pragma unroll

@@ -69,7 +69,7 @@ F8QuantParams quantization(const void* x, const void* h1, const int64_t* offsets
 
 int quantize_and_multiply(F8Mode mode, F8Epilogue epilogue, const F8QuantParams& p, F8Params g, int num_cu,
                           hipStream_t stream) {
-    if (mode == F8_PLAIN && f8_quantizes(p.M, p.dim)) {
+    if (mode == F8_PLAIN && f8_quantizes(p.M, p.E, p.dim)) {
         g.x = p.x;
         g.k = p.dim;
     } else if (launch_f8_quant(mode, p, num_cu, stream) != hipSuccess) {
