@@ -867,6 +867,7 @@ def fp8_scale_shape(E: int, N: int, K: int, halves: int = 1) -> Tuple[int, int, 
     return E, halves * -(-N // (128 * halves)), -(-K // 128)
 
 
+@functools.lru_cache(maxsize=None)      # sizes, asked for at every call
 def fp8_packed_bytes(E: int, N: int, K: int, halves: int = 1) -> int:
     return int(lib.gg_fp8_packed_bytes(E, N, K, halves))
 

@@ -80,6 +80,7 @@ __global__ __launch_bounds__(256) void f8_quant_kernel(const F8QuantParams p) {
     const int64_t qblock = static_cast<int64_t>(p.M) * 64;
     const float e2 = f8_log2e(p.slope);
     const int c0 = static_cast<int>(blockIdx.y) * U * 512 + 8 * lane;
+    if (lo >= hi) return;      // also where lo is odd
     for (int64_t r0 = (lo & ~1) + 2 * (static_cast<int64_t>(blockIdx.x) * 4 + uni(threadIdx.x >> 6)); r0 < hi;
          r0 += static_cast<int64_t>(gridDim.x) * 8) {
         // rows that exist, where the pair has only one

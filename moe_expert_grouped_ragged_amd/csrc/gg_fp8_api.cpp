@@ -27,6 +27,12 @@ int check_fp8_shape(int64_t M, int64_t E, int64_t N, int64_t K, int halves) {
     return GG_OK;
 }
 
+// The gated block's sizes: W1 [2F][H], W2 [H][F].
+int check_glu_shape(int64_t M, int64_t E, int64_t H, int64_t F) {
+    if (F <= 0 || F >= (int64_t(1) << 22)) return GG_ERR_INVALID_ARGUMENT;     // 2F does not overflow
+    return check_fp8_shape(M, E, 2 * F, H, 2);
+}
+
 size_t packed_bytes_of(int64_t E, const F8Dim& rows, const F8Dim& cont) {
     return static_cast<size_t>(E) * (f8_matrix_bytes(rows, cont) + f8_scale_bytes(rows, cont));
 }
@@ -194,14 +200,14 @@ int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t
 }
 
 size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad) {
-    if (M == 0 || check_fp8_shape(M, 1, 2 * F, H, 2) != GG_OK) return 0;
+    if (M == 0 || check_glu_shape(M, 1, H, F) != GG_OK) return 0;
     return glu_rows(M, f8_dim(H, 1)) + glu_rows(M, f8_dim(dgrad ? 2 * F : F, dgrad ? 2 : 1));
 }
 
 int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2, int64_t E,
                        int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes, void* h1_out,
                        void* y, hipStream_t stream) {
-    int st = check_fp8_shape(M, E, 2 * F, H, 2);
+    int st = check_glu_shape(M, E, H, F);
     if (st != GG_OK) return st;
     const float slope = act_slope(activation);
     if (slope == 0.0f) return GG_ERR_INVALID_ARGUMENT;
@@ -234,7 +240,7 @@ int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const v
 int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
                      const void* fc2_t, int64_t E, int64_t H, int64_t F, int activation, void* workspace,
                      size_t workspace_bytes, void* dx, hipStream_t stream) {
-    int st = check_fp8_shape(M, E, 2 * F, H, 2);
+    int st = check_glu_shape(M, E, H, F);
     if (st != GG_OK) return st;
     const float slope = act_slope(activation);
     if (slope == 0.0f) return GG_ERR_INVALID_ARGUMENT;
