@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 namespace gg {
 
 constexpr int F8_BLOCK = 128;   // values that share a scale
@@ -87,27 +89,53 @@ struct F8Params {
     float slope;
     uint8_t* q_out;          // A or dH1, quantized
     uint8_t* s_out;
-    int tile;                // rows of a tile, or 0: no tiles (set by the launcher)
+    int tile;                // whether there are tiles (set by the launcher)
     int group;               // rows of a streaming item, at most; 0: there are none (set by the launcher)
 };
 
-constexpr int F8_GROUP = 96;                    // rows of a streaming item, at most
+constexpr int F8_GROUP = 64;                    // rows of a streaming item, at most
 constexpr int F8_PANEL = 128 * 1024;            // LDS for a streaming item's rows
 constexpr int F8_RING = F8_PANEL + 4 * 1024;    // LDS for operands
 
-// Which tiles a product of M rows over E experts takes (rows of a tile, 0: none), and how many rows a streaming item
-// has at most (0: there are none).  columns: of the largest tile, in all.
+// Which tiles a product of M rows over E experts takes (0 rows: none), and how many rows a streaming item has at most
+// (0: there are none; what 128 KiB hold of the summed width).  wide, narrow: tiles of 256 and of 128 packed columns
+// side by side (narrow 0: there is no such kernel).
+//
+// Up to 64 rows in all are streamed.  Otherwise the tiles whose rounds over the CUs cost least, for experts of equal
+// size (and their spread about it): a 256 x 256 tile counts 1, one of 128 x 256 0.6, one of 128 x 128 0.37.  Times in us
+// of the three (128 experts, whole calls; the last two lines 8 experts):
+//   rows an expert        72              96             132             200             320
+//   K 4096, N 4096  486 425 425     494 431 450     504 596 650     543 709 822     911 878 1075
+//   K 768, N 2048    76  70  71      90  62  65      76  83  95      87  95 113     129 125 159
+//   rows an expert       100             300             700
+//   K 4096, N 4096   57  48  34      78  73  73     123 115 140
+//   K 1048, N 2056   42  22  19      45  25  27      41  40  43
 struct F8Plan {
-    int tile, group;
+    int rows, columns, group;
 };
-inline F8Plan f8_plan(int M, int E, int tiles_n, int kblocks, int num_cu) {
-    const int64_t large = static_cast<int64_t>(M) / 256 * tiles_n;
-    const int64_t owners = M < E ? M : E;
-    const bool half = M >= 80 * owners && M < 120 * owners;
+inline F8Plan f8_plan(int M, int E, int wide, int narrow, int kblocks, int num_cu) {
     const int panel = F8_PANEL / (kblocks * F8_BLOCK * 32) * 32;
     F8Plan plan;
     plan.group = panel < F8_GROUP ? panel : F8_GROUP;
-    plan.tile = M <= 64 && plan.group ? 0 : (large < num_cu || half ? 128 : 256);
+    plan.rows = plan.columns = 0;
+    if (M <= 64 && plan.group) return plan;
+    const int64_t owners = M < E ? M : E;
+    const double mean = static_cast<double>(M) / owners, most = mean + std::sqrt(mean);
+    const auto cost = [&](int rows, int columns, double tile) {
+        const double tiles = owners * std::ceil(most / rows) * columns;
+        return std::ceil(tiles / num_cu) * tile;
+    };
+    plan.rows = 256;
+    plan.columns = 256;
+    double best = cost(256, wide, 1.0);
+    if (const double c = cost(128, wide, 0.6); c < best) {
+        best = c;
+        plan.rows = 128;
+    }
+    if (narrow && cost(128, narrow, 0.37) < best) {
+        plan.rows = 128;
+        plan.columns = 128;
+    }
     return plan;
 }
 

@@ -270,14 +270,10 @@ __device__ __forceinline__ i32x8 f8_join(i32x4 a, i32x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Rows of an expert that tiles of `tile` rows cover (0: there are no tiles): a remainder of up to `group` rows (of
-// small tiles, an expert of up to that) is left to a streaming item.
-__device__ __forceinline__ int f8_tile_rows(int m, int tile, int group) {
-    if (tile == 0) return 0;
-    if (tile == 128) return m <= min(group, 64) ? 0 : m;
-    const int tail = m % tile;
-    return tail <= group ? m - tail : m;
-}
+// Rows of an expert that tiles cover, all or none: an expert that fits a streaming item is left to one.  (A large
+// expert's last rows as a partial tile cost less than the weights read once more for them: 128 experts of 320 rows, K 768,
+// N 2048: 129 us, 153 us with remainders of up to 96 rows streamed; 32 of 300 rows, the gated block's gradient: 121, 156.)
+__device__ __forceinline__ int f8_tile_rows(int m, int tile, int group) { return tile == 0 || m <= group ? 0 : m; }
 
 // One wave-wide copy of 4 bytes a lane to LDS, as dma16.
 #pragma clang diagnostic push
@@ -618,14 +614,13 @@ __device__ __forceinline__ void f8_stream_list(const F8Params& p, int* s_off, in
         const int local = at - uni(s_pre[e]), grp = local / nblocks, nb0 = local - grp * nblocks;
         const int nb1 = min(nblocks, nb0 + end - at);
         const int lo = uni(s_off[e]), hi = uni(s_off[e + 1]);
-        const int row0 = lo + f8_tile_rows(hi - lo, p.tile, p.group) + grp * p.group;
+        const int row0 = lo + grp * p.group;
         const int rows = min(p.group, hi - row0);
         const uint8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
         const uint8_t* ws = p.ws + static_cast<int64_t>(e) * p.ws_stride;
         const int tb = (rows + 31) / 32;
         if (tb == 1) f8_stream_blocks<1, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
-        else if (tb == 2) f8_stream_blocks<2, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
-        else f8_stream_blocks<3, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
+        else f8_stream_blocks<2, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
         at += nb1 - nb0;
     }
 }
@@ -687,7 +682,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     // The 32 tiles that an XCD works on at a time are about as many row as column tiles, whose operands its L2 holds.
     const int band = max(4, 32 / tiles_n);
     prefix_experts(p.offsets, p.E, p.M, s_off, s_pre,
-                   [&](int m) { return (f8_tile_rows(m, TR, p.group) + TR - 1) / TR * tiles_n; });
+                   [&](int m) { return (f8_tile_rows(m, 1, p.group) + TR - 1) / TR * tiles_n; });
     const int n_tiles = uni(s_pre[p.E]);
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int wr = wave >> 1, wc = wave & 1;      // the wave's rows and columns
@@ -713,7 +708,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     auto setup = [&](int t) {
         const int e = uni(find_expert_wave(s_pre, p.E, t));
         const int local = t - uni(s_pre[e]);
-        const int lo = uni(s_off[e]), m = f8_tile_rows(uni(s_off[e + 1]) - lo, TR, p.group);
+        const int lo = uni(s_off[e]), m = f8_tile_rows(uni(s_off[e + 1]) - lo, 1, p.group);
         const int tiles_m = (m + TR - 1) / TR;
         // groups of `band` row tiles, columns by columns
         const int g = local / (band * tiles_n), r = local - g * band * tiles_n, high = min(band, tiles_m - g * band);
@@ -1194,14 +1189,18 @@ static hipError_t launch_tiles(const F8Params& p, int num_cu, hipStream_t s) {
 template <int EPI>
 static hipError_t launch_gemm(const F8Params& p, int num_cu, hipStream_t s) {
     F8Params g = p;
-    const int tiles_n = EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : (p.n.padded() + 255) / 256;
-    const F8Plan plan = f8_plan(p.M, p.E, tiles_n, p.kblocks, num_cu);
-    g.tile = plan.tile;
+    const int blocks = EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : p.n.blocks();
+    const F8Plan plan = f8_plan(p.M, p.E, EPI == F8_STORE_GLU ? blocks : (blocks + 1) / 2, EPI == F8_STORE ? blocks : 0,
+                                p.kblocks, num_cu);
+    g.tile = plan.rows != 0;
     g.group = plan.group;
-    if (g.tile == 256) return launch_tiles<4, 4, EPI>(g, num_cu, s);
-    if (g.tile) return launch_tiles<2, EPI == F8_STORE ? 2 : 4, EPI>(g, num_cu, s);
+    if (plan.rows == 256) return launch_tiles<4, 4, EPI>(g, num_cu, s);
+    if (plan.rows && plan.columns == 256) return launch_tiles<2, 4, EPI>(g, num_cu, s);
+    if (plan.rows) {
+        if constexpr (EPI == F8_STORE) return launch_tiles<2, 2, EPI>(g, num_cu, s);
+    }
     const int64_t groups = static_cast<int64_t>(p.M) / g.group + (p.M < p.E ? p.M : p.E);
-    const int64_t upper = groups * (EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : p.n.blocks());
+    const int64_t upper = groups * blocks;
     hipLaunchKernelGGL((f8_stream_kernel<EPI>), dim3(static_cast<unsigned>(upper < num_cu ? upper : num_cu)), dim3(256), 0, s, g);
     return hipGetLastError();
 }

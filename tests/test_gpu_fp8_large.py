@@ -1,5 +1,5 @@
-"""GPU: the block-scaled 8-bit products at the sizes where 256-row tiles run.
-A row's bits do not depend on the batch, so a large batch is compared bit for
+"""GPU: the block-scaled 8-bit products at the sizes where 256 x 256 and 128 x 256
+tiles run (tests/host/fp8_driver.cpp holds the choice at these sizes).  A row's bits do not depend on the batch, so a large batch is compared bit for
 bit with the same rows in calls of at most 64 rows (streaming items, held to
 the 64-bit definition in test_gpu_fp8.py), and the gated block with its single
 calls."""
@@ -12,8 +12,9 @@ from gpu_harness import bitwise_equal
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
-# whole tiles; remainders of streaming items (1 to 96 rows) and of tiles; experts without rows; small experts
-COUNTS = [1024, 0, 257, 1, 352, 609, 96, 33, 511, 0, 128, 1085]
+# whole and partial tiles, experts without rows, streamed ones
+MANY = [1024, 0, 257, 1, 352, 609, 96, 33, 511, 0, 128, 1085]    # tiles of 128 x 256
+FEW = [1500, 33, 1900]                                           # tiles of 256 x 256
 
 
 @pytest.fixture(autouse=True)
@@ -49,13 +50,13 @@ def _rows_one_by_one(call, x, off, width, E):
     return out
 
 
+@pytest.mark.parametrize("counts", [MANY, FEW], ids=["many", "few"])
 @pytest.mark.parametrize("N,K,halves", [(4096, 8, 1), (4088, 136, 1), (4096, 264, 1), (4128, 1032, 2), (3600, 640, 2)])
-def test_forward_and_dgrad(N, K, halves):
+def test_forward_and_dgrad(counts, N, K, halves):
     gg = _gg()
-    E, lead = len(COUNTS), 5
-    off = _off(COUNTS, lead)
+    E, lead = len(counts), 5
+    off = _off(counts, lead)
     M = int(off[-1]) + 7
-    assert M // 256 * -(-N // 256) >= 224     # enough large tiles for the CUs, or nearly (both sides of the rule)
     x = _normal((M, K), 1)
     q, s = gg.gg_fp8_quantize_weights(_normal((E, N, K), 2, 0.02), halves=halves)
     packed = gg.gg_fp8_pack(q, s, halves=halves)
@@ -74,10 +75,10 @@ def test_forward_and_dgrad(N, K, halves):
     assert bitwise_equal(dx[live], want[live]) and bool((dx[:lead] == 7).all()) and bool((dx[-7:] == 7).all())
 
 
-@pytest.mark.parametrize("H,F,act", [(264, 2048, "swiglu"), (136, 2040, "qgeglu"), (1032, 3968, "swiglu")])
-def test_gated_block_is_its_single_calls(H, F, act):
+@pytest.mark.parametrize("counts", [MANY + [2048, 513, 4096], FEW], ids=["many", "few"])
+@pytest.mark.parametrize("H,F,act", [(264, 2048, "swiglu"), (136, 2040, "qgeglu"), (1032, 3968, "swiglu"), (8, 1928, "swiglu")])
+def test_gated_block_is_its_single_calls(counts, H, F, act):
     gg = _gg()
-    counts = COUNTS + [2048, 513, 4096]
     E = len(counts)
     off = _off(counts, 3)
     M = int(off[-1]) + 2
