@@ -356,8 +356,8 @@ int gg_fp8_quantize_weights(const void* w, int64_t E, int64_t N, int64_t K, int 
 /* Bytes of a packed matrix of E experts, for either direction. */
 size_t gg_fp8_packed_bytes(int64_t E, int64_t N, int64_t K, int halves);
 
-/* Lay out q and s (as written by gg_fp8_quantize_weights, or any e4m3 values
- * with such scales) into `packed` (DEVICE, 16-byte aligned): both dimensions
+/* Lay out q (8-byte aligned) and s (as written by gg_fp8_quantize_weights, or any
+ * e4m3 values with such scales) into `packed` (DEVICE, 16-byte aligned): both dimensions
  * zero-padded to whole blocks, in the operand order of the matrix instruction,
  * then the scales.  transposed = 0: for gg_fp8_forward; 1: for gg_fp8_dgrad.
  * The calls cannot see which one a buffer holds.  Once for frozen weights.

@@ -238,11 +238,18 @@ __global__ void f8_pack_kernel(const uint8_t* __restrict__ q, const uint8_t* __r
         uint32_t w[4] = {0, 0, 0, 0};
         if (row >= 0) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int c = f8_real(cont, st * 64 + 32 * (l >> 5) + 16 * h + j);
+            for (int y = 0; y < 2; ++y) {      // parts are multiples of 8: eights exist or do not
+                const int c = f8_real(cont, st * 64 + 32 * (l >> 5) + 16 * h + 8 * y);
                 if (c < 0) continue;
-                const uint8_t x = transposed ? m[static_cast<int64_t>(c) * K + row] : m[static_cast<int64_t>(row) * K + c];
-                w[j >> 2] |= static_cast<uint32_t>(x) << (8 * (j & 3));
+                if (transposed) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[2 * y + (j >> 2)] |= static_cast<uint32_t>(m[static_cast<int64_t>(c + j) * K + row]) << (8 * (j & 3));
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(m + static_cast<int64_t>(row) * K + c);
+                    w[2 * y] = x.x;
+                    w[2 * y + 1] = x.y;
+                }
             }
         }
         *reinterpret_cast<uint4*>(packed + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);

@@ -124,7 +124,7 @@ int gg_fp8_pack(const uint8_t* q, const uint8_t* s, int64_t E, int64_t N, int64_
     int st = check_fp8_shape(0, E, N, K, halves);
     if (st != GG_OK) return st;
     if (!q || !s || !packed) return GG_ERR_INVALID_ARGUMENT;
-    if (!aligned16(packed)) return GG_ERR_MISALIGNED;
+    if (!aligned16(packed) || !aligned8(q)) return GG_ERR_MISALIGNED;
     const size_t need = gg_fp8_packed_bytes(E, N, K, halves);
     if (packed_bytes < need) return GG_ERR_WORKSPACE_TOO_SMALL;
     st = check_aliasing({range_of(q, E * N * K), range_of(s, gg_fp8_scale_bytes(E, N, K, halves))}, {range_of(packed, need)});

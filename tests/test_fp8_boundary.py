@@ -76,6 +76,7 @@ def test_pack_and_quantize_refusals(gg):
     assert L.gg_fp8_pack(None, 2 * P, 2, 48, 64, 1, 0, 4 * P, need, None) == INV
     assert L.gg_fp8_pack(P, 2 * P, 2, 44, 64, 1, 0, 4 * P, need, None) == INV
     assert L.gg_fp8_pack(P, 2 * P, 2, 48, 64, 1, 0, 4 * P + 8, need, None) == MIS
+    assert L.gg_fp8_pack(P + 4, 2 * P, 2, 48, 64, 1, 0, 4 * P, need, None) == MIS
     assert L.gg_fp8_pack(P, 2 * P, 2, 48, 64, 1, 1, 4 * P, need - 1, None) == WS
     assert L.gg_fp8_pack(P, 2 * P, 2, 48, 64, 1, 0, P, need, None) == ALI
     assert L.gg_fp8_quantize_weights(P, 2, 48, 60, 1, 4 * P, 8 * P, None) == INV
