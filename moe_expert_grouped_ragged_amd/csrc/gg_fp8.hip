@@ -396,6 +396,8 @@ __device__ __forceinline__ void f8_quant_panel(const F8Params& p, int row0, int 
 // nothing drains at a block's end, where the sums go to the epilogue, and
 // loads are repeated only at the stretch's own end.  One token's eight experts,
 // K = N = 4096: 134 MB in 25 us, 5.4 TB/s.
+// R C column blocks of 4 KiB are in flight: 8 (that token 27.5 us with its launch, 28.4 with 12; its gated block 47.3,
+// 49.4 with 12 there, 48.8 with 16).
 //
 // With a quantized output a block's maximum joins four waves' columns over LDS; the block's rows of h1 are loaded
 // when the block begins, in front of its weights, so that nothing waits for them at its end.
