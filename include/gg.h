@@ -335,14 +335,33 @@ int gg_int8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_
  * of the weights serves both directions.  `halves` is 2 for a matrix whose N
  * rows are two halves (W1: gate rows, then up rows): blocks of N then start
  * anew at the second half, so that none holds values of both (for F a multiple
- * of 128 the blocks are the same either way).  Sums are fp32, in one order for
- * all batches, so a row's result does not depend on the rest of the batch.  A
+ * of 128 the blocks are the same either way).  Sums run in one order for all
+ * batches, so a row's result does not depend on the rest of the batch.  A
  * block with a NaN or an infinity becomes NaNs, so such a row of v gives a row of
  * NaNs, and no other row does.
+ *
+ * Sums are of one of two kinds.  GG_FP8_SUMS_FP32: the products are exact and
+ * added in fp32, for weights whose scale is at most 2^118.
+ * GG_FP8_SUMS_SCALED: those of the 8-bit matrix instruction, at up to twice the
+ * rate.  It cuts each product towards zero below 2^-13 of the power of two of
+ * the largest's factors among its eight neighbours (columns 8i to 8i + 7) before
+ * it adds them, and is otherwise fp32: off by up to 7 * 2^-13 of the eight's
+ * largest product, so where the products nearly cancel, by more than the result.
+ * GG_FP8_SUMS_DEFAULT is SCALED for results that end in bf16 (forward with halves =
+ * 1, gradient with halves = 2; the gated block's y and dx) and FP32 for those that
+ * the gated MLP quantizes again (forward with halves = 2: H1; gradient with halves =
+ * 1: dA), where a value moved to its neighbour in bf16 may move by an eighth.  The
+ * calls without `sums` take the default.
  *
  * Limits: 1 <= E <= GG_MAX_EXPERTS; N and K positive multiples of 8 below
  * 2^22, N of 16 with halves = 2; one packed expert matrix (both dimensions
  * padded to whole blocks) below 2 GiB; 0 <= M < 2^31.  Conventions as above. */
+
+enum {
+    GG_FP8_SUMS_DEFAULT = 0,
+    GG_FP8_SUMS_FP32 = 1,
+    GG_FP8_SUMS_SCALED = 2
+};
 
 /* Bytes of the weights' scales: E * halves * ceil(N / halves / 128) * ceil(K / 128),
  * ordered [expert][half][row block][column block].  0 for sizes outside the limits. */
@@ -375,6 +394,9 @@ size_t gg_fp8_workspace_bytes(int64_t M, int64_t width, int halves);
 int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed, int64_t E, int64_t N,
                    int64_t K, int halves, int activation, void* a_out, void* workspace, size_t workspace_bytes, void* y,
                    hipStream_t stream);
+int gg_fp8_forward_sums(const void* x, const int64_t* offsets, int64_t M, const void* packed, int64_t E, int64_t N,
+                        int64_t K, int halves, int activation, void* a_out, void* workspace, size_t workspace_bytes,
+                        void* y, int sums, hipStream_t stream);
 
 /* Input gradient: dy [M][N] with GG_ACT_NONE (h1 and dh1_out NULL); with an
  * activation halves = 2, N = 2F, dy is dA [M][F], h1 [M][2F] the saved FC1
@@ -383,6 +405,9 @@ int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void*
 int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed, int64_t E,
                  int64_t N, int64_t K, int halves, int activation, void* dh1_out, void* workspace,
                  size_t workspace_bytes, void* dx, hipStream_t stream);
+int gg_fp8_dgrad_sums(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed, int64_t E,
+                      int64_t N, int64_t K, int halves, int activation, void* dh1_out, void* workspace,
+                      size_t workspace_bytes, void* dx, int sums, hipStream_t stream);
 
 /* ---- The gated feed-forward block of such products: both projections, the
  * activation and the down projection, and the block's input gradient.
@@ -391,7 +416,7 @@ int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t
  *   input grad.  dA = bf16(quant(dY) W2_e),   dH1 = bf16 of the derivative at H1 times dA,
  *                dX = bf16(quant(dH1) W1_e)
  *
- * The results are those of the single calls in a row, bit for bit.
+ * The results are those of the single calls in a row with the same `sums`, bit for bit.
  * fc1: W1 [2F][H], packed with halves = 2; fc2: W2 [H][F], halves = 1; fc1_t,
  * fc2_t: the same, transposed = 1. */
 
@@ -404,12 +429,18 @@ size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad);
 int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2, int64_t E,
                        int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes, void* h1_out,
                        void* y, hipStream_t stream);
+int gg_fp8_glu_forward_sums(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2,
+                            int64_t E, int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes,
+                            void* h1_out, void* y, int sums, hipStream_t stream);
 
 /* dy [M][H], h1 [M][2F] as the forward saved it; dx [M][H].  dH1 stays in 8
  * bits, in the workspace.  Launches as the forward's. */
 int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
                      const void* fc2_t, int64_t E, int64_t H, int64_t F, int activation, void* workspace,
                      size_t workspace_bytes, void* dx, hipStream_t stream);
+int gg_fp8_glu_dgrad_sums(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
+                          const void* fc2_t, int64_t E, int64_t H, int64_t F, int activation, void* workspace,
+                          size_t workspace_bytes, void* dx, int sums, hipStream_t stream);
 
 /* ---- Low-rank adapters of the experts (trainable; added to a frozen product).
  *

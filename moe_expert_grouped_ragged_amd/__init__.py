@@ -88,6 +88,11 @@ GG_ACT_QGEGLU = 1
 GG_ACT_NONE = -1
 ACTIVATIONS = {"swiglu": GG_ACT_SWIGLU, "qgeglu": GG_ACT_QGEGLU}
 
+GG_FP8_SUMS_DEFAULT = 0
+GG_FP8_SUMS_FP32 = 1
+GG_FP8_SUMS_SCALED = 2
+FP8_SUMS = {None: GG_FP8_SUMS_DEFAULT, "fp32": GG_FP8_SUMS_FP32, "scaled": GG_FP8_SUMS_SCALED}
+
 EXPORTED = ("gg_status_string", "gg_packed_bytes", "gg_dgrad_workspace_bytes", "gg_pack_weights",
             "gg_forward_fc1_swiglu", "gg_forward_fc2", "gg_dgrad", "gg_round_bf16",
             "gg_dgrad_glu_workspace_bytes", "gg_forward_fc1_glu", "gg_dgrad_glu", "gg_dgrad_recompute",
@@ -98,7 +103,8 @@ EXPORTED = ("gg_status_string", "gg_packed_bytes", "gg_dgrad_workspace_bytes", "
             "gg_adapter_forward", "gg_adapter_workspace_bytes", "gg_adapter_backward",
             "gg_fp8_scale_bytes", "gg_fp8_quantize_weights", "gg_fp8_packed_bytes", "gg_fp8_pack",
             "gg_fp8_workspace_bytes", "gg_fp8_forward", "gg_fp8_dgrad",
-            "gg_fp8_glu_workspace_bytes", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad")
+            "gg_fp8_glu_workspace_bytes", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad",
+            "gg_fp8_forward_sums", "gg_fp8_dgrad_sums", "gg_fp8_glu_forward_sums", "gg_fp8_glu_dgrad_sums")
 
 
 def _load() -> ctypes.CDLL:
@@ -157,12 +163,16 @@ def _load() -> ctypes.CDLL:
     lib.gg_fp8_glu_workspace_bytes.restype = sz
     lib.gg_fp8_glu_forward.argtypes = [p, p, i64, p, p, i64, i64, i64, i32, p, sz, p, p, p]
     lib.gg_fp8_glu_dgrad.argtypes = [p, p, p, i64, p, p, i64, i64, i64, i32, p, sz, p, p]
+    for name in ("gg_fp8_forward", "gg_fp8_dgrad", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad"):
+        plain = getattr(lib, name).argtypes
+        getattr(lib, name + "_sums").argtypes = [*plain[:-1], i32, plain[-1]]
     for name in ("gg_pack_weights", "gg_pack_frag", "gg_forward_fc1_swiglu", "gg_forward_fc2",
                  "gg_forward_fc2_frag", "gg_dgrad", "gg_round_bf16", "gg_forward_fc1_glu", "gg_dgrad_glu",
                  "gg_dgrad_recompute", "gg_dgrad_noalloc", "gg_scale_rows", "gg_scale_rows_backward",
                  "gg_int8_quantize_rows", "gg_int8_pack", "gg_int8_forward", "gg_int8_dgrad",
                  "gg_adapter_forward", "gg_adapter_backward", "gg_fp8_quantize_weights", "gg_fp8_pack",
-                 "gg_fp8_forward", "gg_fp8_dgrad", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad"):
+                 "gg_fp8_forward", "gg_fp8_dgrad", "gg_fp8_glu_forward", "gg_fp8_glu_dgrad",
+                 "gg_fp8_forward_sums", "gg_fp8_dgrad_sums", "gg_fp8_glu_forward_sums", "gg_fp8_glu_dgrad_sums"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -881,6 +891,12 @@ def fp8_glu_workspace_bytes(M: int, H: int, F: int, dgrad: bool = False) -> int:
     return int(lib.gg_fp8_glu_workspace_bytes(M, H, F, int(bool(dgrad))))
 
 
+def _fp8_sums(sums) -> int:
+    if sums not in FP8_SUMS:
+        raise ValueError(f"sums must be one of {list(FP8_SUMS)}")
+    return FP8_SUMS[sums]
+
+
 def _fp8_shape(E, N, K, halves) -> int:
     """Bytes of a packed matrix of these sizes, which are checked."""
     if halves not in (1, 2):
@@ -968,11 +984,16 @@ def _fp8_packed(packed: torch.Tensor, E: int, N: int, K: int, halves: int, trans
 def gg_fp8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
                    halves: int = 1, activation=None, save_a: bool = False, a_out: Optional[torch.Tensor] = None,
                    y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                   stream: Optional[torch.cuda.Stream] = None, sums: Optional[str] = None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(y [M, N], A or None): the rows quantized in blocks of 128, times each
     expert's 8-bit matrix (gg_fp8_pack with the same halves).  activation None:
     x is [M, K]; "swiglu" | "qgeglu": x is H1 [M, 2K], the product's operand is
-    A = act(gate) * up [M, K], returned with save_a (or given a_out)."""
+    A = act(gate) * up [M, K], returned with save_a (or given a_out).
+    sums: "fp32"; "scaled", the 8-bit instruction's, which cut products below
+    2^-13 of the largest of eight and take about half as long in large batches;
+    None: "fp32" with halves=2 (H1, which is quantized again), else "scaled"."""
+    how = _fp8_sums(sums)
     _bf16_cuda(x, "x")
     dev, M = x.device, x.shape[0]
     act = GG_ACT_NONE if activation is None else _activation(activation)
@@ -989,9 +1010,9 @@ def gg_fp8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
     if a_out is None and save_a:
         a_out = _out(None, (M, K), "a_out", dev)
     y = _out(y, (M, N), "y", dev)
-    _check(lib.gg_fp8_forward(x.data_ptr(), off.data_ptr(), M, packed.data_ptr(), E, N, K, halves, act, _ptr(a_out),
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), y.data_ptr(),
-                              _stream_ptr(stream, dev)), "gg_fp8_forward")
+    _check(lib.gg_fp8_forward_sums(x.data_ptr(), off.data_ptr(), M, packed.data_ptr(), E, N, K, halves, act, _ptr(a_out),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), y.data_ptr(), how,
+                                   _stream_ptr(stream, dev)), "gg_fp8_forward")
     return y, a_out
 
 
@@ -999,12 +1020,15 @@ def gg_fp8_forward(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
 def gg_fp8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, E: int, N: int, K: int,
                  halves: int = 1, h1: Optional[torch.Tensor] = None, activation=None, save_dh1: bool = True,
                  dh1_out: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
-                 ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                 workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                 sums: Optional[str] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(dx [M, K], dH1 or None): input gradient through 8-bit weights
     (gg_fp8_pack_transposed with the same halves).  activation None: dy is
     [M, N]; else halves = 2, N = 2F, dy is dA [M, F], h1 the saved [M, 2F], and
-    dH1 [M, 2F] is returned unless save_dh1 is False."""
+    dH1 [M, 2F] is returned unless save_dh1 is False.  sums: as for
+    gg_fp8_forward; None: "fp32" with halves=1 (dA, which is quantized again
+    behind the derivative), else "scaled"."""
+    how = _fp8_sums(sums)
     _bf16_cuda(dy, "dy")
     dev, M = dy.device, dy.shape[0]
     act = GG_ACT_NONE if activation is None else _activation(activation)
@@ -1027,9 +1051,9 @@ def gg_fp8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, 
     if dh1_out is None and h1 is not None and save_dh1:
         dh1_out = _out(None, (M, N), "dh1_out", dev)
     dx = _out(dx, (M, K), "dx", dev)
-    _check(lib.gg_fp8_dgrad(dy.data_ptr(), _ptr(h1), off.data_ptr(), M, packed.data_ptr(), E, N, K, halves, act,
-                            _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                            dx.data_ptr(), _stream_ptr(stream, dev)), "gg_fp8_dgrad")
+    _check(lib.gg_fp8_dgrad_sums(dy.data_ptr(), _ptr(h1), off.data_ptr(), M, packed.data_ptr(), E, N, K, halves, act,
+                                 _ptr(dh1_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 dx.data_ptr(), how, _stream_ptr(stream, dev)), "gg_fp8_dgrad")
     return dx, dh1_out
 
 
@@ -1037,10 +1061,13 @@ def gg_fp8_dgrad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, 
 def gg_fp8_glu_forward(x: torch.Tensor, offsets: torch.Tensor, fc1: torch.Tensor, fc2: torch.Tensor,
                        E: int, H: int, F: int, activation="swiglu", save_h1: bool = True,
                        h1_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
-                       workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                       workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                       sums: Optional[str] = None
                        ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """The gated block: x [M, H] -> (y [M, H], H1 [M, 2F] or None).  fc1: W1
-    [E, 2F, H] by gg_fp8_pack(..., halves=2); fc2: W2 [E, H, F] by gg_fp8_pack."""
+    [E, 2F, H] by gg_fp8_pack(..., halves=2); fc2: W2 [E, H, F] by gg_fp8_pack.
+    sums: both products' (None: "fp32" for H1, "scaled" for y), as for gg_fp8_forward."""
+    how = _fp8_sums(sums)
     _bf16_cuda(x, "x")
     M, dev = x.shape[0], x.device
     _bf16_cuda(x, "x", shape=(M, H))
@@ -1056,9 +1083,9 @@ def gg_fp8_glu_forward(x: torch.Tensor, offsets: torch.Tensor, fc1: torch.Tensor
     if h1_out is None and save_h1:
         h1_out = _out(None, (M, 2 * F), "h1_out", dev)
     y = _out(y, (M, H), "y", dev)
-    _check(lib.gg_fp8_glu_forward(x.data_ptr(), off.data_ptr(), M, fc1.data_ptr(), fc2.data_ptr(), E, H, F, act,
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(h1_out),
-                                  y.data_ptr(), _stream_ptr(stream, dev)), "gg_fp8_glu_forward")
+    _check(lib.gg_fp8_glu_forward_sums(x.data_ptr(), off.data_ptr(), M, fc1.data_ptr(), fc2.data_ptr(), E, H, F, act,
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(h1_out),
+                                       y.data_ptr(), how, _stream_ptr(stream, dev)), "gg_fp8_glu_forward")
     return y, h1_out
 
 
@@ -1066,9 +1093,11 @@ def gg_fp8_glu_forward(x: torch.Tensor, offsets: torch.Tensor, fc1: torch.Tensor
 def gg_fp8_glu_dgrad(dy: torch.Tensor, h1: torch.Tensor, offsets: torch.Tensor, fc1_t: torch.Tensor,
                      fc2_t: torch.Tensor, E: int, H: int, F: int, activation="swiglu",
                      dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+                     stream: Optional[torch.cuda.Stream] = None, sums: Optional[str] = None) -> torch.Tensor:
     """The gated block's input gradient: dy [M, H] and the saved h1 [M, 2F] ->
-    dx [M, H].  fc1_t, fc2_t: the weights of gg_fp8_glu_forward by gg_fp8_pack_transposed."""
+    dx [M, H].  fc1_t, fc2_t: the weights of gg_fp8_glu_forward by gg_fp8_pack_transposed.
+    sums: both products' (None: "fp32" for dA, "scaled" for dx), as for gg_fp8_forward."""
+    how = _fp8_sums(sums)
     _bf16_cuda(dy, "dy")
     M, dev = dy.shape[0], dy.device
     _bf16_cuda(dy, "dy", shape=(M, H))
@@ -1081,9 +1110,9 @@ def gg_fp8_glu_dgrad(dy: torch.Tensor, h1: torch.Tensor, offsets: torch.Tensor, 
     act = _activation(activation)
     workspace = _workspace(workspace, fp8_glu_workspace_bytes(M, H, F, True), dev)
     dx = _out(dx, (M, H), "dx", dev)
-    _check(lib.gg_fp8_glu_dgrad(dy.data_ptr(), h1.data_ptr(), off.data_ptr(), M, fc1_t.data_ptr(), fc2_t.data_ptr(),
-                                E, H, F, act, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                dx.data_ptr(), _stream_ptr(stream, dev)), "gg_fp8_glu_dgrad")
+    _check(lib.gg_fp8_glu_dgrad_sums(dy.data_ptr(), h1.data_ptr(), off.data_ptr(), M, fc1_t.data_ptr(), fc2_t.data_ptr(),
+                                     E, H, F, act, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                     dx.data_ptr(), how, _stream_ptr(stream, dev)), "gg_fp8_glu_dgrad")
     return dx
 
 

@@ -91,6 +91,7 @@ struct F8Params {
     uint8_t* s_out;
     int tile;                // whether there are tiles (set by the launcher)
     int group;               // rows of a streaming item, at most; 0: there are none (set by the launcher)
+    int fp32_sums;           // sums in fp32 (operands as bf16), or the scaled 8-bit instruction's
 };
 
 constexpr int F8_GROUP = 64;                    // rows of a streaming item, at most

@@ -265,20 +265,47 @@ __global__ void f8_pack_kernel(const uint8_t* __restrict__ q, const uint8_t* __r
 
 // ---------------------------------------------------------------- product
 //
-// out[r][n] = sum over blocks of 128 of 2^(s_r + s_w) sum q w: the matrix
-// instruction multiplies by both scales, so the fp32 sums run over all blocks
-// without a step between them.  The instruction adds eight neighbouring
-// products at a time, each cut towards zero below 2^-13 of the power of two of
-// the largest's factors, and joins these sums in fp32 (found with planted
-// values; the 8-bit instructions without scales cut at the same place).  That
-// is its own way of summing and a choice made with it: on normal data it costs
-// about 2^-13 of the result, where the result's rounding to bf16 is up to 2^-8 and
-// the operands' to e4m3 2^-4; bf16 instructions, which keep the products, would
-// need every operand converted and run at half the rate.  Every kernel adds a
-// row's products in the same order (steps of 64 columns, one 32x32x64
-// instruction each), so a row's bits do not depend on the batch.
+// out[r][n] = sum over blocks of 128 of 2^(s_r + s_w) sum q w, in one of two
+// ways of summing.  Either way a kernel adds a row's products in the same order
+// (steps of 64 columns), so a row's bits do not depend on the batch.
+//
+// The scaled instruction (F8Params::fp32_sums = 0) multiplies by both scales, so
+// the sums run over all blocks without a step between them.  It adds eight
+// neighbouring products at a time, each cut towards zero below 2^-13 of the power
+// of two of the largest's factors, and joins these sums in fp32 (found with
+// planted values; the 8-bit instructions without scales cut at the same place).
+// On normal data that costs about 2^-13 of the result, next to the result's
+// rounding to bf16, up to 2^-8: enough for a result that ends there.  Where the
+// result is quantized again it is not: 1.5% of H1 round to another bf16 value, and
+// of 768 values of A one or two a row to their neighbour in e4m3, which moves all
+// of that row of y by up to 0.7% of its norm.
+//
+// With fp32 sums (fp32_sums = 1) both operands become bf16 values in registers,
+// times their scales, and the bf16 instruction multiplies them: e4m3 has four
+// significant bits, so value and product are exact, and the sums are fp32's (a
+// product of 2^-24 of the largest is kept, 2^-26 is not).  Rows take half of
+// their scale and weights twice theirs: a row's largest values times their scale
+// round to 2^128, which bf16 does not hold.
 __device__ __forceinline__ f32x16 f8_mma(i32x8 w, i32x8 t, f32x16 acc, int ws, int ts) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, t, acc, 0, 0, 0, ws, 0, ts);
+}
+typedef __attribute__((ext_vector_type(4))) uint32_t f8_bf16x8;     // eight bf16 values
+__device__ __forceinline__ f32x16 f8_mma_bf16(f8_bf16x8 w, f8_bf16x8 t, f32x16 acc) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, t), acc, 0, 0, 0);
+}
+__device__ __forceinline__ float f8_row_factor(int byte) { return __builtin_bit_cast(float, static_cast<uint32_t>(byte - 1) << 23); }
+__device__ __forceinline__ float f8_weight_factor(uint32_t byte) { return __builtin_bit_cast(float, min(byte + 1, 255u) << 23); }
+// Eights: the values 8 S to 8 S + 7 of a lane's 32, which one 16-column instruction takes (any 16 columns do, as long as
+// both operands have the same: those and the other half of the lanes').  Pair P of them, times a power of two.
+template <int S, int P>
+__device__ __forceinline__ void f8_pair(f8_bf16x8& v, i32x8 raw, float factor) {
+    v[P] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<uint32_t>(raw[2 * S + P / 2]), factor, P % 2 != 0));
+}
+template <int S>
+__device__ __forceinline__ f8_bf16x8 f8_eight(i32x8 raw, float factor) {
+    f8_bf16x8 v;
+    static_for<4>([&](auto p) { f8_pair<S, decltype(p)::value>(v, raw, factor); });
+    return v;
 }
 __device__ __forceinline__ i32x8 f8_join(i32x4 a, i32x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -401,7 +428,7 @@ __device__ __forceinline__ void f8_quant_panel(const F8Params& p, int row0, int 
 //
 // With a quantized output a block's maximum joins four waves' columns over LDS; the block's rows of h1 are loaded
 // when the block begins, in front of its weights, so that nothing waits for them at its end.
-template <int TB, int EPI>
+template <int TB, int EPI, int FP32>
 __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_t* w, const uint8_t* ws, int row0, int rows,
                                                  int nb0, int nb1, uint8_t* panel, uint32_t (*s_top)[4][F8_GROUP]) {
     constexpr int C = EPI == F8_STORE_GLU ? 2 : 1;   // column blocks of a wave
@@ -590,9 +617,21 @@ __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_
                 for (int i = 0; i < TB; ++i) {
                     const uint8_t* o = op + (u * TB + i) * 2048;
                     const i32x8 t = f8_join(*reinterpret_cast<const i32x4*>(o), *reinterpret_cast<const i32x4*>(o + 1024));
+                    if constexpr (FP32 == 0) {
 #pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        acc[c][i] = f8_mma(f8_join(wv[at][c][2 * u], wv[at][c][2 * u + 1]), t, acc[c][i], wsv[at][c], ts[i]);
+                        for (int c = 0; c < C; ++c)
+                            acc[c][i] = f8_mma(f8_join(wv[at][c][2 * u], wv[at][c][2 * u + 1]), t, acc[c][i], wsv[at][c], ts[i]);
+                    } else {
+                        static_for<4>([&](auto s_tag) {
+                            constexpr int s = decltype(s_tag)::value;
+                            const f8_bf16x8 tb = f8_eight<s>(t, f8_row_factor(ts[i]));
+#pragma unroll
+                            for (int c = 0; c < C; ++c)
+                                acc[c][i] = f8_mma_bf16(f8_eight<s>(f8_join(wv[at][c][2 * u], wv[at][c][2 * u + 1]),
+                                                                    f8_weight_factor(static_cast<uint32_t>(wsv[at][c]))),
+                                                        tb, acc[c][i]);
+                        });
+                    }
                 }
             if (++k == nu) {
                 k = 0;
@@ -613,7 +652,7 @@ __device__ __forceinline__ void f8_stream_blocks(const F8Params& p, const uint8_
 // Next to tiles, experts that fit one item are streamed, whole.  (A large expert's last rows as a partial tile cost
 // less than the weights read once more for them: 128 experts of 320 rows, K 768, N 2048: 129 us, 153 us with remainders of
 // up to 96 rows streamed; 32 of 300 rows, the gated block's gradient: 121 us, 156.)
-template <int EPI>
+template <int EPI, int FP32>
 __device__ __forceinline__ void f8_stream_list(const F8Params& p, int* s_off, int* s_pre, uint8_t* panel,
                                                uint32_t (*s_top)[4][F8_GROUP]) {
     const int nblocks = EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : p.n.blocks();
@@ -632,19 +671,19 @@ __device__ __forceinline__ void f8_stream_list(const F8Params& p, int* s_off, in
         const uint8_t* w = p.w + static_cast<int64_t>(e) * p.w_stride;
         const uint8_t* ws = p.ws + static_cast<int64_t>(e) * p.ws_stride;
         const int tb = (rows + 31) / 32;
-        if (tb == 1) f8_stream_blocks<1, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
-        else f8_stream_blocks<2, EPI>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
+        if (tb == 1) f8_stream_blocks<1, EPI, FP32>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
+        else f8_stream_blocks<2, EPI, FP32>(p, w, ws, row0, rows, nb0, nb1, panel, s_top);
         at += nb1 - nb0;
     }
 }
 
-template <int EPI>
+template <int EPI, int FP32>
 __global__ __launch_bounds__(256, 1) void f8_stream_kernel(const F8Params p) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[F8_RING];
     __shared__ uint32_t s_top[2][4][F8_GROUP];
     __shared__ int s_off[GG_KMAX_EXPERTS + 1];
     __shared__ int s_pre[GG_KMAX_EXPERTS + 1];
-    f8_stream_list<EPI>(p, s_off, s_pre, s_ring, s_top);
+    f8_stream_list<EPI, FP32>(p, s_off, s_pre, s_ring, s_top);
 }
 
 // A value kept in an accumulation register, and back.
@@ -685,7 +724,7 @@ constexpr int F8_STG_BYTES = 32 * 128;   // per wave: 32 rows x 64 columns of bf
 // 1.6 PFLOP/s: besides its 12 stages a tile waits about 6 us for its 128 KiB of stores, 3 us of them for the first
 // one, as the loads behind them count only when they are done.  Two workgroups of 128 x 256 on a CU hide that wait but
 // read half as much again (the first case 20% slower, the second equal).
-template <int BR, int BC, int EPI>
+template <int BR, int BC, int EPI, int FP32>
 __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     constexpr int TR = 64 * BR, TC = 64 * BC;               // rows and packed columns of a tile
     constexpr int OC = EPI == F8_STORE_GLU ? TC / 2 : TC;   // columns of what it makes
@@ -798,7 +837,9 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     };
 
     f32x16 acc[BR][BC];    // [row block][column block]
-    i32x8 tf[2][BR], wf[2][BC];
+    constexpr int SETS = FP32 ? 1 : 2;      // of fragments as they are read
+    i32x8 tf[SETS][BR], wf[SETS][BC];
+    f8_bf16x8 tb[2][4], wb[BC][4];          // FP32: as bf16, rows of two row blocks
     int ts[BR], ts_next[BR], wsc[WS];       // scales of the block that is multiplied, and of the next
     uint32_t wd[WS], wd_next[WS];           // the weights' scales, four blocks in a dword
     // a lane's first 16 bytes of a fragment in a slot; its second are 16 bytes off in the swizzled rows
@@ -806,12 +847,12 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     const uint32_t w_at = W_AT + BC * wc * 2048 + lane * 16, s_at = S_AT + (32 * BR * wr + (lane & 31)) * 4;
     // fragment i of the slot at sl, of the parity u
     auto read_t = [&](uint32_t sl, auto i_tag, auto u_tag) {
-        constexpr int u = decltype(u_tag)::value, i = decltype(i_tag)::value;
+        constexpr int u = decltype(u_tag)::value % SETS, i = decltype(i_tag)::value;
         tf[u][i] = f8_join(*reinterpret_cast<const i32x4*>(s_ring + (sl + t_at) + i * 32 * F8_STAGE),
                            *reinterpret_cast<const i32x4*>(s_ring + (sl + (t_at ^ 16)) + i * 32 * F8_STAGE));
     };
     auto read_w = [&](uint32_t sl, auto j_tag, auto u_tag) {
-        constexpr int u = decltype(u_tag)::value, j = decltype(j_tag)::value;
+        constexpr int u = decltype(u_tag)::value % SETS, j = decltype(j_tag)::value;
         const uint8_t* f = s_ring + (sl + w_at) + j * 2048;
         wf[u][j] = f8_join(*reinterpret_cast<const i32x4*>(f), *reinterpret_cast<const i32x4*>(f + 1024));
     };
@@ -830,13 +871,19 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     };
     // matrix instruction m of a stage, rows first; the tile's first stage starts its sums from zero
     auto mma = [&](auto u_tag, auto m_tag, auto first_tag) {
-        constexpr int u = decltype(u_tag)::value, i = decltype(m_tag)::value / BC, j = decltype(m_tag)::value % BC;
+        constexpr int u = decltype(u_tag)::value % SETS, i = decltype(m_tag)::value / BC, j = decltype(m_tag)::value % BC;
         const int s = wsc[WS == 2 && j >= BC / 2];
         if constexpr (decltype(first_tag)::value != 0)
             acc[i][j] = f8_mma(wf[u][j], tf[u][i], f32x16{}, s, ts[i]);
         else
             acc[i][j] = f8_mma(wf[u][j], tf[u][i], acc[i][j], s, ts[i]);
         asm volatile("" : "+a"(acc[i][j]));     // in its place: the compiler sinks matrix instructions past branches
+    };
+    // FP32: eights s of the weights of block j as bf16
+    auto weights_bf16 = [&](auto j_tag, auto s_tag, uint32_t byte) {
+        constexpr int j = decltype(j_tag)::value, s = decltype(s_tag)::value;
+        wb[j][s] = f8_eight<s>(wf[0][j], f8_weight_factor(byte));
+        asm volatile("" : "+v"(wb[j][s]));      // in its place, as the matrix instructions
     };
     auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
     // Waits until the next stage has landed: the copies of the ring's other stages, and `behind` stores among them, may
@@ -855,22 +902,95 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     // after the epilogue.
     uint32_t cur = 0;
     const uint8_t* cur_ws[WS];
-    auto stage = [&](int st, int behind, auto u_tag, auto first_tag) {
-        constexpr int u = decltype(u_tag)::value;
-        if constexpr (u == 0) {
-            const int k = st >> 1;
+    // The stages and what they call are inlined by force: a call would put the accumulators into memory.
+    //
+    // the scales of block k, where it begins
+    auto roll_scales = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < BR; ++i) ts[i] = ts_next[i];
-            if ((k & 3) == 0) {
+        for (int i = 0; i < BR; ++i) ts[i] = ts_next[i];
+        if ((k & 3) == 0) {
+#pragma unroll
+            for (int c = 0; c < WS; ++c) {
+                wd[c] = wd_next[c];
+                wd_next[c] = scalar_load(cur_ws[c] + min(k + 4, p.ws_ld - 4));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < WS; ++c) wsc[c] = static_cast<int>(wd[c] >> (8 * (k & 3)));
+    };
+    // The stage with fp32 sums: four bf16 instructions for each scaled one.  Of its BR x 4 slots, slot (i, s) multiplies
+    // eights s of row block i by those of all columns.  Behind a slot's instructions eights of the next row block become
+    // bf16, and behind the last row block's those of the next stage's weights and first row block, in the registers that
+    // are read for the last time there.  So fragments are read into one set of registers, and a conversion waits for
+    // neither a read nor an instruction: two of 8 cycles go with an instruction of 32 (up to four in a loop of nothing
+    // else take no time; where the compiler had moved them to their use, the tiles took 12% more).
+    //
+    // 65536 rows, H 4096, F 2048, H1 and A: 1.89 ms (matrix pipe 69% busy at 1.6 GHz: the chip's power), 1.01 with scaled sums.
+    auto stage_fp32 = [&](int st, int behind, auto u_tag, auto first_tag) __attribute__((always_inline)) {
+        constexpr int u = decltype(u_tag)::value;
+        if constexpr (u == 0) roll_scales(st >> 1);
+        constexpr int Q = 4 * BR, SYNC = BR == 4 ? 3 : 0, REST = Q - 1 - SYNC;
+        uint32_t refill = 0;
+        uint32_t wnext[WS];     // the weights' scales of the next stage
+        static_for<Q>([&](auto q_tag) {
+            constexpr int q = decltype(q_tag)::value, i = q / 4, s = q % 4;
+            if constexpr (q == 4 * (BR - 1)) {
 #pragma unroll
                 for (int c = 0; c < WS; ++c) {
-                    wd[c] = wd_next[c];
-                    wd_next[c] = scalar_load(cur_ws[c] + min(k + 4, p.ws_ld - 4));
+                    const int k = (st + 1) >> 1;
+                    wnext[c] = u == 0 ? static_cast<uint32_t>(wsc[c]) : ((k & 3) == 0 ? wd_next[c] : wd[c]) >> (8 * (k & 3));
+                    wnext[c] &= 255;
                 }
             }
-#pragma unroll
-            for (int c = 0; c < WS; ++c) wsc[c] = static_cast<int>(wd[c] >> (8 * (k & 3)));
-        }
+            static_for<BC>([&](auto j_tag) {
+                constexpr int j = decltype(j_tag)::value;
+                if constexpr (decltype(first_tag)::value != 0 && s == 0)
+                    acc[i][j] = f8_mma_bf16(wb[j][s], tb[i % 2][s], f32x16{});
+                else
+                    acc[i][j] = f8_mma_bf16(wb[j][s], tb[i % 2][s], acc[i][j]);
+                asm volatile("" : "+a"(acc[i][j]));
+                if constexpr (i < BR - 1) {
+                    static_for<4 / BC>([&](auto y) {
+                        f8_pair<s, j * (4 / BC) + decltype(y)::value>(tb[(i + 1) % 2][s], tf[0][i + 1], f8_row_factor(ts[i + 1]));
+                    });
+                    if constexpr (j == BC - 1) asm volatile("" : "+v"(tb[(i + 1) % 2][s]));
+                } else {
+                    weights_bf16(j_tag, GrpTag<s>{}, wnext[WS == 2 && j >= BC / 2]);
+                    static_for<4 / BC>([&](auto y) {
+                        f8_pair<s, j * (4 / BC) + decltype(y)::value>(tb[0][s], tf[0][0], f8_row_factor(u == 0 ? ts[0] : ts_next[0]));
+                    });
+                    if constexpr (j == BC - 1) asm volatile("" : "+v"(tb[0][s]));
+                }
+                fence();
+            });
+            if constexpr (q == SYNC) {
+                // stage st + 1 has landed, and every wave holds its fragments of stage st, as in stage()
+                wait_ahead(behind);
+                block_barrier();
+                refill = cur;
+                cur = cur + SLOT_BYTES == SLOTS * SLOT_BYTES ? 0 : cur + SLOT_BYTES;
+            } else if constexpr (q > SYNC) {
+                constexpr int m = q - SYNC - 1;
+                if constexpr (u == 1 && m == 0) read_s(cur, (st + 1) >> 1);
+                // the first row block and the weights before the last row block's slots; row block i > 0 when it has become bf16
+                constexpr int BEFORE = BR == 4 ? 5 : 2, EACH = (BC + 1 + BEFORE - 1) / BEFORE;
+                constexpr int f0 = m * EACH, f1 = f0 + EACH;
+                static_for<(f1 < BC + 1 ? f1 : BC + 1) - (f0 < BC + 1 ? f0 : BC + 1)>(
+                    [&](auto f) { read(cur, GrpTag<f0 + decltype(f)::value>{}, GrpTag<0>{}); });
+                static_for<BR - 1>([&](auto r_tag) {
+                    constexpr int r = decltype(r_tag)::value + 1, after = BR == 4 && r == 1 ? 9 : (BR == 4 && r == 2 ? 10 : 4 * r);
+                    if constexpr (q == after) read_t(cur, GrpTag<r>{}, GrpTag<0>{});
+                });
+                constexpr int a = m * P / REST, z = (m + 1) * P / REST;
+                static_for<z - a>([&](auto j) { piece(refill, GrpTag<a + decltype(j)::value>{}); });
+                fence();
+            }
+        });
+        advance();
+    };
+    auto stage_scaled = [&](int st, int behind, auto u_tag, auto first_tag) __attribute__((always_inline)) {
+        constexpr int u = decltype(u_tag)::value;
+        if constexpr (u == 0) roll_scales(st >> 1);
         static_for<BC>([&](auto m) { mma(u_tag, m, first_tag); });
         fence();
         // stage st + 1 has landed, and every wave holds its fragments of stage st, whose slot is refilled from here on
@@ -892,6 +1012,10 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
             fence();
         });
         advance();
+    };
+    auto stage = [&](int st, int behind, auto u_tag, auto first_tag) __attribute__((always_inline)) {
+        if constexpr (FP32) stage_fp32(st, behind, u_tag, first_tag);
+        else stage_scaled(st, behind, u_tag, first_tag);
     };
 
     // a stage without products
@@ -924,6 +1048,13 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
         for (int c = 0; c < WS; ++c) cur_ws[c] = tile.ws[c];
         read_s(cur, 0);
         static_for<BR + BC>([&](auto f) { read(cur, f, GrpTag<0>{}); });
+        if constexpr (FP32)
+            static_for<4>([&](auto s_tag) {
+                static_for<BC>([&](auto j_tag) {
+                    weights_bf16(j_tag, s_tag, wd_next[WS == 2 && decltype(j_tag)::value >= BC / 2] & 255);
+                });
+                tb[0][decltype(s_tag)::value] = f8_eight<decltype(s_tag)::value>(tf[0][0], f8_row_factor(ts_next[0]));
+            });
         stage(0, stores, GrpTag<0>{}, GrpTag<1>{});     // an even number of stages, at least two
         stage(1, stores, GrpTag<1>{}, GrpTag<0>{});
 #pragma unroll 1
@@ -1161,7 +1292,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     wait_vmcnt<0>();     // the last copies: none is under way to LDS that is another workgroup's
     if (p.group == 0) return;
     __syncthreads();
-    f8_stream_list<EPI>(p, s_off, s_pre, s_ring, reinterpret_cast<uint32_t(*)[4][F8_GROUP]>(s_stg));
+    f8_stream_list<EPI, FP32>(p, s_off, s_pre, s_ring, reinterpret_cast<uint32_t(*)[4][F8_GROUP]>(s_stg));
 }
 
 // ---------------------------------------------------------------- launchers
@@ -1202,17 +1333,17 @@ hipError_t launch_f8_pack(const uint8_t* q, const uint8_t* s, int E, const F8Dim
     return hipGetLastError();
 }
 
-template <int BR, int BC, int EPI>
+template <int BR, int BC, int EPI, int FP32>
 static hipError_t launch_tiles(const F8Params& p, int num_cu, hipStream_t s) {
     constexpr int TR = 64 * BR, OC = EPI == F8_STORE_GLU ? 32 * BC : 64 * BC;
     const int width = EPI == F8_STORE_GLU ? p.n.part_p : p.n.padded();
     const int64_t upper = (static_cast<int64_t>(p.M) / TR + (p.M < p.E ? p.M : p.E)) * ((width + OC - 1) / OC);
     const dim3 grid(static_cast<unsigned>(upper < num_cu && p.group == 0 ? upper : num_cu));
-    hipLaunchKernelGGL((f8_tile_kernel<BR, BC, EPI>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((f8_tile_kernel<BR, BC, EPI, FP32>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
-template <int EPI>
+template <int EPI, int FP32>
 static hipError_t launch_gemm(const F8Params& p, int num_cu, hipStream_t s) {
     F8Params g = p;
     const int blocks = EPI == F8_STORE_GLU ? p.n.part_p / F8_BLOCK : p.n.blocks();
@@ -1220,22 +1351,22 @@ static hipError_t launch_gemm(const F8Params& p, int num_cu, hipStream_t s) {
                                 p.kblocks, num_cu);
     g.tile = plan.rows != 0;
     g.group = plan.group;
-    if (plan.rows == 256) return launch_tiles<4, 4, EPI>(g, num_cu, s);
-    if (plan.rows && plan.columns == 256) return launch_tiles<2, 4, EPI>(g, num_cu, s);
+    if (plan.rows == 256) return launch_tiles<4, 4, EPI, FP32>(g, num_cu, s);
+    if (plan.rows && plan.columns == 256) return launch_tiles<2, 4, EPI, FP32>(g, num_cu, s);
     if (plan.rows) {
-        if constexpr (EPI == F8_STORE) return launch_tiles<2, 2, EPI>(g, num_cu, s);
+        if constexpr (EPI == F8_STORE) return launch_tiles<2, 2, EPI, FP32>(g, num_cu, s);
     }
     const int64_t groups = static_cast<int64_t>(p.M) / g.group + (p.M < p.E ? p.M : p.E);
     const int64_t upper = groups * blocks;
-    hipLaunchKernelGGL((f8_stream_kernel<EPI>), dim3(static_cast<unsigned>(upper < num_cu ? upper : num_cu)), dim3(256), 0, s, g);
+    hipLaunchKernelGGL((f8_stream_kernel<EPI, FP32>), dim3(static_cast<unsigned>(upper < num_cu ? upper : num_cu)), dim3(256), 0, s, g);
     return hipGetLastError();
 }
 
 hipError_t launch_f8_gemm(F8Epilogue epilogue, const F8Params& p, int num_cu, hipStream_t s) {
     switch (epilogue) {
-        case F8_STORE: return launch_gemm<F8_STORE>(p, num_cu, s);
-        case F8_STORE_GLU: return launch_gemm<F8_STORE_GLU>(p, num_cu, s);
-        default: return launch_gemm<F8_STORE_DGLU>(p, num_cu, s);
+        case F8_STORE: return p.fp32_sums ? launch_gemm<F8_STORE, 1>(p, num_cu, s) : launch_gemm<F8_STORE, 0>(p, num_cu, s);
+        case F8_STORE_GLU: return p.fp32_sums ? launch_gemm<F8_STORE_GLU, 1>(p, num_cu, s) : launch_gemm<F8_STORE_GLU, 0>(p, num_cu, s);
+        default: return p.fp32_sums ? launch_gemm<F8_STORE_DGLU, 1>(p, num_cu, s) : launch_gemm<F8_STORE_DGLU, 0>(p, num_cu, s);
     }
 }
 

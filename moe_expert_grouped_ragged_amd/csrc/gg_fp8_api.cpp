@@ -84,6 +84,10 @@ int quantize_and_multiply(F8Mode mode, F8Epilogue epilogue, const F8QuantParams&
     return launch_f8_gemm(epilogue, g, num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
+// Whether a product's sums are fp32's: as asked for, else where its result is quantized again (it is not the last one).
+bool sums_known(int sums) { return sums >= GG_FP8_SUMS_DEFAULT && sums <= GG_FP8_SUMS_SCALED; }
+int fp32_sums(int sums, bool last) { return sums == GG_FP8_SUMS_FP32 || (sums == GG_FP8_SUMS_DEFAULT && !last); }
+
 // Quantized rows start on 256 bytes.
 size_t glu_rows(int64_t M, const F8Dim& d) { return (static_cast<size_t>(f8_rows_bytes(M, d)) + 255) / 256 * 256; }
 
@@ -145,8 +149,16 @@ size_t gg_fp8_workspace_bytes(int64_t M, int64_t width, int halves) {
 int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed, int64_t E, int64_t N,
                    int64_t K, int halves, int activation, void* a_out, void* workspace, size_t workspace_bytes, void* y,
                    hipStream_t stream) {
+    return gg_fp8_forward_sums(x, offsets, M, packed, E, N, K, halves, activation, a_out, workspace, workspace_bytes, y,
+                               GG_FP8_SUMS_DEFAULT, stream);
+}
+
+int gg_fp8_forward_sums(const void* x, const int64_t* offsets, int64_t M, const void* packed, int64_t E, int64_t N,
+                        int64_t K, int halves, int activation, void* a_out, void* workspace, size_t workspace_bytes,
+                        void* y, int sums, hipStream_t stream) {
     int st = check_fp8_shape(M, E, N, K, halves);
     if (st != GG_OK) return st;
+    if (!sums_known(sums)) return GG_ERR_INVALID_ARGUMENT;
     const bool glu = activation != GG_ACT_NONE;
     const float slope = glu ? act_slope(activation) : 1.0f;
     if (slope == 0.0f || (!glu && a_out)) return GG_ERR_INVALID_ARGUMENT;
@@ -166,15 +178,25 @@ int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void*
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     uint8_t* q = static_cast<uint8_t*>(workspace);
     const F8Dim n = f8_dim(N, halves), k = f8_dim(K, 1);
+    F8Params g = product(q, offsets, M, packed, E, n, k, y);
+    g.fp32_sums = fp32_sums(sums, halves == 1);
     return quantize_and_multiply(glu ? F8_GLU : F8_PLAIN, F8_STORE, quantization(x, nullptr, offsets, M, E, k, slope, a_out, q),
-                                 product(q, offsets, M, packed, E, n, k, y), info.num_cu, stream);
+                                 g, info.num_cu, stream);
 }
 
 int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed, int64_t E,
                  int64_t N, int64_t K, int halves, int activation, void* dh1_out, void* workspace,
                  size_t workspace_bytes, void* dx, hipStream_t stream) {
+    return gg_fp8_dgrad_sums(dy, h1, offsets, M, packed, E, N, K, halves, activation, dh1_out, workspace, workspace_bytes,
+                             dx, GG_FP8_SUMS_DEFAULT, stream);
+}
+
+int gg_fp8_dgrad_sums(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed, int64_t E,
+                      int64_t N, int64_t K, int halves, int activation, void* dh1_out, void* workspace,
+                      size_t workspace_bytes, void* dx, int sums, hipStream_t stream) {
     int st = check_fp8_shape(M, E, N, K, halves);
     if (st != GG_OK) return st;
+    if (!sums_known(sums)) return GG_ERR_INVALID_ARGUMENT;
     const bool glu = activation != GG_ACT_NONE;
     const float slope = glu ? act_slope(activation) : 1.0f;
     if (slope == 0.0f || (glu && halves != 2) || (!glu && (h1 || dh1_out))) return GG_ERR_INVALID_ARGUMENT;
@@ -195,8 +217,10 @@ int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t
     if ((st = debug_validate_offsets(offsets, E, M, stream)) != GG_OK) return st;
     uint8_t* q = static_cast<uint8_t*>(workspace);
     const F8Dim n = f8_dim(N, halves), k = f8_dim(K, 1);
+    F8Params g = product(q, offsets, M, packed, E, k, n, dx);
+    g.fp32_sums = fp32_sums(sums, halves == 2);
     return quantize_and_multiply(glu ? F8_DGLU : F8_PLAIN, F8_STORE, quantization(dy, h1, offsets, M, E, n, slope, dh1_out, q),
-                                 product(q, offsets, M, packed, E, k, n, dx), info.num_cu, stream);
+                                 g, info.num_cu, stream);
 }
 
 size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad) {
@@ -207,8 +231,16 @@ size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad) {
 int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2, int64_t E,
                        int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes, void* h1_out,
                        void* y, hipStream_t stream) {
+    return gg_fp8_glu_forward_sums(x, offsets, M, fc1, fc2, E, H, F, activation, workspace, workspace_bytes, h1_out, y,
+                                   GG_FP8_SUMS_DEFAULT, stream);
+}
+
+int gg_fp8_glu_forward_sums(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2,
+                            int64_t E, int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes,
+                            void* h1_out, void* y, int sums, hipStream_t stream) {
     int st = check_glu_shape(M, E, H, F);
     if (st != GG_OK) return st;
+    if (!sums_known(sums)) return GG_ERR_INVALID_ARGUMENT;
     const float slope = act_slope(activation);
     if (slope == 0.0f) return GG_ERR_INVALID_ARGUMENT;
     if (M == 0) return GG_OK;
@@ -229,19 +261,30 @@ int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const v
     uint8_t *qx = static_cast<uint8_t*>(workspace), *qa = qx + glu_rows(M, h);
     F8Params g = product(qx, offsets, M, fc1, E, f2, h, h1_out);
     g.slope = slope;
+    g.fp32_sums = fp32_sums(sums, false);
     g.q_out = qa;
     g.s_out = qa + M * f.padded();
     st = quantize_and_multiply(F8_PLAIN, F8_STORE_GLU, quantization(x, nullptr, offsets, M, E, h, 1.0f, nullptr, qx), g, info.num_cu,
                                stream);
     if (st != GG_OK) return st;
-    return launch_f8_gemm(F8_STORE, product(qa, offsets, M, fc2, E, h, f, y), info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+    g = product(qa, offsets, M, fc2, E, h, f, y);
+    g.fp32_sums = fp32_sums(sums, true);
+    return launch_f8_gemm(F8_STORE, g, info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
                      const void* fc2_t, int64_t E, int64_t H, int64_t F, int activation, void* workspace,
                      size_t workspace_bytes, void* dx, hipStream_t stream) {
+    return gg_fp8_glu_dgrad_sums(dy, h1, offsets, M, fc1_t, fc2_t, E, H, F, activation, workspace, workspace_bytes, dx,
+                                 GG_FP8_SUMS_DEFAULT, stream);
+}
+
+int gg_fp8_glu_dgrad_sums(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* fc1_t,
+                          const void* fc2_t, int64_t E, int64_t H, int64_t F, int activation, void* workspace,
+                          size_t workspace_bytes, void* dx, int sums, hipStream_t stream) {
     int st = check_glu_shape(M, E, H, F);
     if (st != GG_OK) return st;
+    if (!sums_known(sums)) return GG_ERR_INVALID_ARGUMENT;
     const float slope = act_slope(activation);
     if (slope == 0.0f) return GG_ERR_INVALID_ARGUMENT;
     if (M == 0) return GG_OK;
@@ -264,12 +307,15 @@ int gg_fp8_glu_dgrad(const void* dy, const void* h1, const int64_t* offsets, int
     F8Params g = product(qy, offsets, M, fc2_t, E, f, h, nullptr);
     g.h1 = static_cast<const uint16_t*>(h1);
     g.slope = slope;
+    g.fp32_sums = fp32_sums(sums, false);
     g.q_out = qd;
     g.s_out = qd + M * f2.padded();
     st = quantize_and_multiply(F8_PLAIN, F8_STORE_DGLU, quantization(dy, nullptr, offsets, M, E, h, 1.0f, nullptr, qy), g, info.num_cu,
                                stream);
     if (st != GG_OK) return st;
-    return launch_f8_gemm(F8_STORE, product(qd, offsets, M, fc1_t, E, h, f2, dx), info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+    g = product(qd, offsets, M, fc1_t, E, h, f2, dx);
+    g.fp32_sums = fp32_sums(sums, true);
+    return launch_f8_gemm(F8_STORE, g, info.num_cu, stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 }  // extern "C"
