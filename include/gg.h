@@ -390,7 +390,9 @@ size_t gg_fp8_workspace_bytes(int64_t M, int64_t width, int halves);
 
 /* Forward: x [M][K] with GG_ACT_NONE, or H1 [M][2K] with an activation, in
  * which case a_out (may be NULL) receives A [M][K].  packed: gg_fp8_pack(...,
- * halves, transposed = 0).  y [M][N].  Two launches, or one for up to 64 rows. */
+ * halves, transposed = 0).  y [M][N].  Two launches: the rows are quantized, then
+ * multiplied.  One where the product quantizes them: GG_ACT_NONE, M <= 64, M <=
+ * 8 (E + 1), and K at most 4096 in whole blocks. */
 int gg_fp8_forward(const void* x, const int64_t* offsets, int64_t M, const void* packed, int64_t E, int64_t N,
                    int64_t K, int halves, int activation, void* a_out, void* workspace, size_t workspace_bytes, void* y,
                    hipStream_t stream);
@@ -401,7 +403,8 @@ int gg_fp8_forward_sums(const void* x, const int64_t* offsets, int64_t M, const 
 /* Input gradient: dy [M][N] with GG_ACT_NONE (h1 and dh1_out NULL); with an
  * activation halves = 2, N = 2F, dy is dA [M][F], h1 [M][2F] the saved FC1
  * output, and dh1_out (may be NULL) receives dH1 [M][2F].  packed:
- * gg_fp8_pack(..., halves, transposed = 1).  dx [M][K].  Launches as the forward's. */
+ * gg_fp8_pack(..., halves, transposed = 1).  dx [M][K].  Launches as the forward's,
+ * with N (each half of it in whole blocks) in K's place. */
 int gg_fp8_dgrad(const void* dy, const void* h1, const int64_t* offsets, int64_t M, const void* packed, int64_t E,
                  int64_t N, int64_t K, int halves, int activation, void* dh1_out, void* workspace,
                  size_t workspace_bytes, void* dx, hipStream_t stream);
@@ -425,7 +428,7 @@ size_t gg_fp8_glu_workspace_bytes(int64_t M, int64_t H, int64_t F, int dgrad);
 
 /* x [M][H]; h1_out [M][2F] (saved for the gradient) may be NULL; y [M][H].
  * A goes from the first product to the second in 8 bits, in the workspace.
- * Three launches, or two for up to 64 rows. */
+ * Three launches, or two where gg_fp8_forward with K = H and GG_ACT_NONE has one. */
 int gg_fp8_glu_forward(const void* x, const int64_t* offsets, int64_t M, const void* fc1, const void* fc2, int64_t E,
                        int64_t H, int64_t F, int activation, void* workspace, size_t workspace_bytes, void* h1_out,
                        void* y, hipStream_t stream);
