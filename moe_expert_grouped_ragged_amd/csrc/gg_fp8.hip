@@ -179,11 +179,12 @@ __global__ __launch_bounds__(256) void f8_quant_kernel(const F8QuantParams p) {
     }
 }
 
-// A workgroup a 128 x 128 block: 16 rows of 16 lanes of eight columns at a time, held in registers.
+// A workgroup a 128 x 128 block: 16 rows of 16 lanes of eight columns at a time, held in registers.  The grid has a row
+// for each expert: a dimension of it holds less than 2^32 threads, 2^24 blocks (34 GB of weights 8 rows high).
 __global__ __launch_bounds__(256) void f8_quant_weights_kernel(const uint16_t* __restrict__ w, F8Dim n, F8Dim k,
                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
     __shared__ uint32_t s_top[4];
-    const int64_t b = blockIdx.x;
+    const int64_t b = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int kb = static_cast<int>(b % k.blocks());
     const int64_t nb = b / k.blocks();                  // over all experts
     const int per = n.part_p / F8_BLOCK;                // blocks of a part; the parts of all experts follow each other
@@ -1318,8 +1319,8 @@ hipError_t launch_f8_quant(F8Mode mode, const F8QuantParams& p, int num_cu, hipS
 
 hipError_t launch_f8_quant_weights(const uint16_t* w, int E, const F8Dim& n, const F8Dim& k, uint8_t* q, uint8_t* s,
                                    hipStream_t stream) {
-    const int64_t blocks = static_cast<int64_t>(E) * n.blocks() * k.blocks();
-    hipLaunchKernelGGL(f8_quant_weights_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, w, n, k, q, s);
+    const dim3 grid(static_cast<unsigned>(n.blocks() * k.blocks()), static_cast<unsigned>(E));    // at most 2^17, 2^10
+    hipLaunchKernelGGL(f8_quant_weights_kernel, grid, dim3(256), 0, stream, w, n, k, q, s);
     return hipGetLastError();
 }
 
