@@ -892,7 +892,7 @@ def fp8_glu_workspace_bytes(M: int, H: int, F: int, dgrad: bool = False) -> int:
 
 
 def _fp8_sums(sums) -> int:
-    if sums not in FP8_SUMS:
+    if not (sums is None or isinstance(sums, str)) or sums not in FP8_SUMS:
         raise ValueError(f"sums must be one of {list(FP8_SUMS)}")
     return FP8_SUMS[sums]
 
