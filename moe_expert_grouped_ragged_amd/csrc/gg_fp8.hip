@@ -924,7 +924,7 @@ __global__ __launch_bounds__(256, 1) void f8_tile_kernel(const F8Params p) {
     // bf16, and behind the last row block's those of the next stage's weights and first row block, in the registers that
     // are read for the last time there.  So fragments are read into one set of registers, and a conversion waits for
     // neither a read nor an instruction: two of 8 cycles go with an instruction of 32 (up to four in a loop of nothing
-    // else take no time; where the compiler had moved them to their use, the tiles took 12% more).
+    // else take no time; where the compiler had moved them to their use, the tiles took 10% more).
     //
     // 65536 rows, H 4096, F 2048, H1 and A: 1.89 ms (matrix pipe 69% busy at 1.6 GHz: the chip's power), 1.01 with scaled sums.
     auto stage_fp32 = [&](int st, int behind, auto u_tag, auto first_tag) __attribute__((always_inline)) {
